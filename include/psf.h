@@ -397,6 +397,128 @@ int psf_lse_merge_live_rows(float* o_acc, void* o_run, float* l_acc, const void*
 int psf_grad_add_live_rows(void* dst, const void* src, const int32_t* cu_q, const int32_t* cu_k,
                            const int32_t* dev_meta, int nseg, int T, int H, int D, int dtype, void* stream);
 
+/*
+ * 8-bit paged key/value cache, for serving: append, attention of a few query
+ * rows per sequence, eviction by accumulated attention weight, gather.
+ *                           [no counterpart on the pages: an addition of this
+ *                            library; the attention is the varlen forward's
+ *                            (scale, softcap, causal alignment, left window, lse)]
+ *
+ *  A cache is a pool of pages. A page holds page_size tokens (16, 32, 64 or 128)
+ *  of every KV head as e4m3 codes, with one fp32 scale per (page, head) for K
+ *  and one for V: a code c stands for the value c * scale.
+ *    k [num_pages, Hkv, page_size, Dqk], v [num_pages, Hkv, page_size, Dv] e4m3,
+ *    k_scale, v_scale [num_pages, Hkv] fp32 (finite, >= 0), contiguous,
+ *    weight [num_pages, Hkv, page_size] fp32, contiguous, or NULL: the attention
+ *    weight each token has received so far, for eviction.
+ *  k_strides / v_strides: element strides (page, head, row), all zero for the
+ *  contiguous ones; else positive multiples of 16 below 2^38 (a dimension of
+ *  extent 1 is ignored), and no overlap. The last dim is contiguous, base
+ *  pointers 16-byte aligned. Head dims as for the attention calls.
+ *
+ *  Sequences: page_table int32 [B, max_pages] (contiguous) lists the pages of
+ *  each sequence in order, seq_lens int32 [B] its tokens: token j of sequence b
+ *  is row j % page_size of page page_table[b][j / page_size]. Entries past
+ *  ceil(seq_lens[b] / page_size) are not read. Several sequences may name the
+ *  same page (a shared prefix) as long as no call writes to it. All of it is
+ *  read on the device: nothing synchronises, and the calls can be captured.
+ *  A length outside [0, max_pages * page_size], rows outside the packed tensor,
+ *  or a page outside [0, num_pages) is a PSF_EDEVICE_ARGS device status; nothing
+ *  outside the tensors is touched, a page that does not exist is not written,
+ *  and the results of the other sequences stand.
+ */
+typedef struct {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  float* weight;
+  int num_pages, page_size, Hkv, Dqk, Dv;
+  int64_t k_strides[3], v_strides[3];
+} psf_kv_cache;
+
+/*
+ * Quantise new rows into the cache.
+ *  k [T, Hkv, Dqk], v [T, Hkv, Dv] (dtype): the new tokens of all sequences,
+ *  packed; sequence b's are rows [cu_new[b], cu_new[b + 1]) (int32 [B + 1]), or,
+ *  with cu_new NULL, T / B rows each (B must divide T). seq_lens counts them
+ *  already: they go to positions seq_lens[b] - n_b .. seq_lens[b] - 1.
+ *  Scale: s(a) is the smallest power of two >= 2^-126 with a <= 448 s. A page
+ *  whose first row is new gets s(largest finite magnitude of its new rows); a
+ *  page that holds older tokens of the sequence gets the larger of its scale and
+ *  that, and where it grows the older codes c become RNE_e4m3(c * (old / new)),
+ *  exact down to the format's subnormals. New codes are RNE_e4m3(x / scale); a
+ *  value that is not finite becomes NaN. The weights of new tokens become 0.
+ *  Rows of T past cu_new[B] are not read; rows of a page past the new ones keep
+ *  their contents. A page that is written belongs to one sequence.
+ *  strides: NULL, or 6 element strides (batch, head, row) of k, v (batch ignored).
+ */
+int psf_kv_cache_append(const psf_kv_cache* cache, const void* k, const void* v, const int64_t* strides, int dtype,
+                        const int32_t* cu_new, const int32_t* page_table, const int32_t* seq_lens, int B,
+                        int max_pages, int T, void* stream);
+
+/*
+ * Attention of packed query rows over the cache.
+ *  q [T, Hq, Dqk], out [T, Hq, Dv] (dtype), lse [Hq, T] fp32. Sequence b's query
+ *  rows are [cu_q[b], cu_q[b + 1]), or T / B each with cu_q NULL; max_q: the most
+ *  rows of a sequence (more is a PSF_EDEVICE_ARGS status). They are the last
+ *  tokens of the sequence: row i of m sits at position seq_lens[b] - m + i, the
+ *  bottom-right alignment of the causal mask and the window. scale, causal,
+ *  window_left, softcap, GQA and rows without keys as for psf_attn_varlen_fwd;
+ *  rows past cu_q[B] get out = 0 and lse = -inf.
+ *  One query row per sequence is the decode step; a few are drafted tokens or the
+ *  tail of a prompt. Any number is computed, a tile of rows at a time; for long
+ *  prompt chunks psf_kv_cache_gather and psf_attn_varlen_fwd are faster.
+ *  Codes that are NaN make a row NaN only where it sees them.
+ *  flags: 0, or PSF_CACHE_ACCUMULATE: weight[page, hkv, row] += the sum over the
+ *  sequence's query rows and the Hq / Hkv heads of hkv of exp(logit - lse), for
+ *  every token seen. With a page in several sequences the order of the additions
+ *  is not fixed. Other bits: PSF_EINVAL.
+ *  strides: NULL, or 6 element strides (batch, head, row) of q, out (batch ignored).
+ *  workspace: psf_attn_cache_workspace_size(...) bytes, 16-byte aligned; nothing in it
+ *  has to be kept or cleared between calls.
+ */
+#define PSF_CACHE_ACCUMULATE 1
+size_t psf_attn_cache_workspace_size(int B, int max_pages, int page_size, int Hq, int Hkv, int Dqk, int Dv,
+                                     int max_q, int flags);
+int psf_attn_cache_fwd(const void* q, const psf_kv_cache* cache, void* out, float* lse, const int32_t* cu_q,
+                       const int32_t* page_table, const int32_t* seq_lens, int B, int max_pages, int T, int max_q,
+                       int Hq, const int64_t* strides, int dtype, float scale, int causal, int32_t window_left,
+                       float softcap, int flags, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Evict down to `budget` tokens per sequence and KV head, in place.
+ *  A sequence longer than budget keeps, for each KV head on its own, its last
+ *  `recent` tokens and the budget - recent others of largest weight (of equal
+ *  weights the earliest; NaN counts as the largest), in their order, moved to
+ *  positions 0 .. budget - 1; weights move along. new_lens[b] = min(seq_lens[b],
+ *  budget); other sequences are not touched. A new block's scale is the largest
+ *  old scale of its tokens, codes become RNE_e4m3(c * (old / new)). Rows past the
+ *  kept ones keep their contents; pages past ceil(budget / page_size) are free.
+ *  After an eviction positions count kept tokens (so do windows).
+ *  A sequence with a page that does not exist is left as it is, its new length
+ *  its old one. Needs cache->weight, 1 <= budget, 0 <= recent <= budget. new_lens
+ *  must not be seq_lens. A page belongs to one sequence.
+ *  workspace: psf_kv_cache_evict_workspace_size(...) bytes, 16-byte aligned.
+ */
+size_t psf_kv_cache_evict_workspace_size(int B, int max_pages, int page_size, int Hkv, int budget);
+int psf_kv_cache_evict(const psf_kv_cache* cache, const int32_t* page_table, const int32_t* seq_lens,
+                       int32_t* new_lens, int B, int max_pages, int budget, int recent, void* workspace,
+                       size_t ws_bytes, void* stream);
+
+/*
+ * The cached rows of all sequences as packed 16-bit tensors.
+ *  k [total_k, Hkv, Dqk], v [total_k, Hkv, Dv] (dtype, contiguous): row
+ *  cu_k[b] + j is token j of sequence b, code * scale rounded once (with scales
+ *  written by the append, exact in bf16). cu_k int32 [B + 1]: prefix sums of
+ *  seq_lens. With q, cu_k and these the varlen forward attends a long prompt
+ *  chunk over its cached prefix. total_k bounds the sum of the lengths (more is a
+ *  PSF_EDEVICE_ARGS status, and the rows past it are dropped); rows past cu_k[B]
+ *  are not written.
+ */
+int psf_kv_cache_gather(const psf_kv_cache* cache, const int32_t* page_table, const int32_t* seq_lens, int B,
+                        int max_pages, void* k, void* v, int32_t* cu_k, int total_k, int dtype, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -46,7 +46,21 @@ SIGNATURES = {
     "psf_build_cross_segments": (I, [P, I, I, I, I, I, I, P, P, P, P]),
     "psf_lse_merge_live_rows": (I, [P, P, P, P, P, P, P, P, I, I, I, I, I, P]),
     "psf_grad_add_live_rows": (I, [P, P, P, P, P, I, I, I, I, I, P]),
+    "psf_kv_cache_append": (I, [P, P, P, P, I, P, P, P, I, I, I, P]),
+    "psf_attn_cache_workspace_size": (SZ, [I, I, I, I, I, I, I, I, I]),
+    "psf_attn_cache_fwd": (I, [P, P, P, P, P, P, P, I, I, I, I, I, P, I, F, I, I32, F, I, P, SZ, P]),
+    "psf_kv_cache_evict_workspace_size": (SZ, [I, I, I, I, I]),
+    "psf_kv_cache_evict": (I, [P, P, P, P, I, I, I, I, P, SZ, P]),
+    "psf_kv_cache_gather": (I, [P, P, P, I, I, P, P, P, I, I, P]),
 }
+
+
+class KVCacheStruct(ctypes.Structure):
+    """psf_kv_cache of include/psf.h."""
+
+    _fields_ = [("k", P), ("v", P), ("k_scale", P), ("v_scale", P), ("weight", P), ("num_pages", I),
+                ("page_size", I), ("Hkv", I), ("Dqk", I), ("Dv", I), ("k_strides", I64 * 3), ("v_strides", I64 * 3)]
+
 
 PSF_LAYOUT_THD = 0
 PSF_LAYOUT_BHSD = 1
@@ -55,6 +69,7 @@ PSF_DTYPE_F16 = 1
 PSF_SEGMENTS_SKIP_PAD = 1
 PSF_FWD_PACK_GQA = 1
 PSF_BWD_PACK_GQA = 1
+PSF_CACHE_ACCUMULATE = 1
 ERRORS = {-1: "PSF_EINVAL", -2: "PSF_EUNSUPPORTED", -3: "PSF_ECUDA", -4: "PSF_EDEVICE_ARGS",
           -5: "PSF_ETIMEOUT", -6: "PSF_EWORKSPACE"}
 

@@ -14,6 +14,7 @@
 #include "bwd.cuh"
 #include "fwd.cuh"
 #include "launch.h"
+#include "launch_cache.h"
 #include "tmap.h"
 
 using namespace psf;
@@ -588,6 +589,116 @@ int noalloc_scratch(void** out) {
   return PSF_OK;
 }
 
+// ---------------------------------------------------------------- 8-bit cache
+// Element (= byte) strides (page, head, row) of a cache tensor.
+int cache_strides(const int64_t* given, const char* name, const psf_kv_cache& c, int D, int64_t* sp, int64_t* sh,
+                  int64_t* sr) {
+  const int64_t ext[3] = {c.num_pages, c.Hkv, c.page_size};
+  int64_t st[3] = {(int64_t)c.Hkv * c.page_size * D, (int64_t)c.page_size * D, D};
+  if (given[0] || given[1] || given[2]) {
+    for (int i = 0; i < 3; ++i) {
+      if (ext[i] <= 1) continue;
+      if (given[i] <= 0 || given[i] % 16 != 0 || given[i] >= ((int64_t)1 << 38))
+        return fail(PSF_EINVAL, "cache %s: stride %lld must be a positive multiple of 16 below 2^38", name,
+                    (long long)given[i]);
+      st[i] = given[i];
+    }
+    int ord[3] = {0, 1, 2};
+    for (int a = 0; a < 3; ++a)
+      for (int b = a + 1; b < 3; ++b)
+        if (st[ord[b]] < st[ord[a]]) {
+          const int x = ord[a];
+          ord[a] = ord[b];
+          ord[b] = x;
+        }
+    int64_t span = D;
+    for (int i = 0; i < 3; ++i) {
+      const int d = ord[i];
+      if (ext[d] <= 1) continue;
+      if (st[d] < span) return fail(PSF_EINVAL, "cache %s: the strided view overlaps itself", name);
+      span += st[d] * (ext[d] - 1);
+    }
+  }
+  *sp = st[0];
+  *sh = st[1];
+  *sr = st[2];
+  return PSF_OK;
+}
+
+int cache_view(const psf_kv_cache* cache, CacheView* v) {
+  if (!cache) return fail(PSF_EINVAL, "null cache");
+  const psf_kv_cache& c = *cache;
+  if (c.num_pages < 1 || c.Hkv < 1 || c.Hkv > 65535)
+    return fail(PSF_EINVAL, "cache: bad sizes num_pages=%d Hkv=%d", c.num_pages, c.Hkv);
+  if (c.page_size != 16 && c.page_size != 32 && c.page_size != 64 && c.page_size != 128)
+    return fail(PSF_EINVAL, "cache: page_size %d not in {16, 32, 64, 128}", c.page_size);
+  if (!supported_dims(c.Dqk, c.Dv))
+    return fail(PSF_EUNSUPPORTED, "head dims (Dqk=%d, Dv=%d) not in {(64,64),(128,128),(192,128),(512,512)}", c.Dqk, c.Dv);
+  if (!c.k || !c.v || !c.k_scale || !c.v_scale) return fail(PSF_EINVAL, "cache: null tensor pointer");
+  if (!aligned16(c.k) || !aligned16(c.v)) return fail(PSF_EINVAL, "cache: k and v must be 16-byte aligned");
+  int rc;
+  if ((rc = cache_strides(c.k_strides, "k", c, c.Dqk, &v->k_sp, &v->k_sh, &v->k_sr)) ||
+      (rc = cache_strides(c.v_strides, "v", c, c.Dv, &v->v_sp, &v->v_sh, &v->v_sr)))
+    return rc;
+  v->k = static_cast<uint8_t*>(c.k);
+  v->v = static_cast<uint8_t*>(c.v);
+  v->k_scale = c.k_scale;
+  v->v_scale = c.v_scale;
+  v->weight = c.weight;
+  v->pages = c.num_pages;
+  v->page = c.page_size;
+  v->page_lg = c.page_size == 16 ? 4 : c.page_size == 32 ? 5 : c.page_size == 64 ? 6 : 7;
+  v->Hkv = c.Hkv;
+  v->Dqk = c.Dqk;
+  v->Dv = c.Dv;
+  return PSF_OK;
+}
+
+int seq_view(const int32_t* page_table, const int32_t* seq_lens, const int32_t* cu, int B, int max_pages,
+             int page_size, int T, SeqView* s) {
+  if (B < 1 || B > 65535 || max_pages < 1 || T < 0)
+    return fail(PSF_EINVAL, "need 1 <= B <= 65535, max_pages >= 1 and T >= 0 (got B=%d max_pages=%d T=%d)", B, max_pages, T);
+  if ((int64_t)max_pages * page_size > 0x7fffffff) return fail(PSF_EINVAL, "max_pages * page_size exceeds 2^31 - 1");
+  if (!page_table || !seq_lens) return fail(PSF_EINVAL, "null page_table or seq_lens");
+  if (!cu && T % B != 0) return fail(PSF_EINVAL, "without prefix sums B=%d must divide T=%d", B, T);
+  s->table = page_table;
+  s->lens = seq_lens;
+  s->cu = cu;
+  s->B = B;
+  s->max_pages = max_pages;
+  s->T = T;
+  s->each = cu ? 0 : T / B;
+  s->max_rows = T;
+  return PSF_OK;
+}
+
+size_t evict_ws_layout(int B, int max_pages, int page_size, int Hkv, int budget, EvictWorkspace* w, void* base) {
+  const int64_t units = (int64_t)B * Hkv, cap = (int64_t)max_pages * page_size;
+  // A sequence longer than the budget is what makes a unit use its part.
+  const int64_t kept = budget < cap ? budget : cap, blocks = (kept + page_size - 1) / page_size;
+  size_t off = 0;
+  const size_t live = off;
+  off += align256(sizeof(int) * (size_t)units);
+  const size_t src = off;
+  off += align256(sizeof(int32_t) * (size_t)(units * kept));
+  const size_t ratio = off;
+  off += align256(sizeof(float2) * (size_t)(units * kept));
+  const size_t scale = off;
+  off += align256(sizeof(float2) * (size_t)(units * blocks));
+  const size_t keys = off;
+  if (cap > kEvictSmemKeys) off += align256(sizeof(uint32_t) * (size_t)(units * cap));
+  if (w && base) {
+    char* b = static_cast<char*>(base);
+    w->live = reinterpret_cast<int*>(b + live);
+    w->src = reinterpret_cast<int32_t*>(b + src);
+    w->ratio = reinterpret_cast<float2*>(b + ratio);
+    w->scale = reinterpret_cast<float2*>(b + scale);
+    w->keys = reinterpret_cast<uint32_t*>(b + keys);
+    w->cap = cap;
+  }
+  return off;
+}
+
 }  // namespace
 
 extern "C" {
@@ -829,6 +940,132 @@ int psf_grad_add_live_rows(void* dst, const void* src, const int32_t* cu_q, cons
   cudaError_t e = launch_grad_add_live(dst, src, cu_q, cu_k, dev_meta, nseg, T, H, D, dtype == PSF_DTYPE_F16,
                                        static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? PSF_OK : cuda_fail(e, "live-row gradient add launch");
+}
+
+int psf_kv_cache_append(const psf_kv_cache* cache, const void* k, const void* v, const int64_t* strides, int dtype,
+                        const int32_t* cu_new, const int32_t* page_table, const int32_t* seq_lens, int B,
+                        int max_pages, int T, void* stream) {
+  CacheView c;
+  SeqView s;
+  int rc;
+  if ((rc = cache_view(cache, &c)) || (rc = check_dtype(dtype)) ||
+      (rc = seq_view(page_table, seq_lens, cu_new, B, max_pages, c.page, T, &s)))
+    return rc;
+  View vk, vv;
+  if ((rc = strided_view(strides, 0, "k", PSF_LAYOUT_THD, 1, T, c.Hkv, c.Dqk, false, &vk)) ||
+      (rc = strided_view(strides, 1, "v", PSF_LAYOUT_THD, 1, T, c.Hkv, c.Dv, false, &vv)))
+    return rc;
+  if (T == 0) return PSF_OK;
+  if (!k || !v || !aligned16(k) || !aligned16(v)) return fail(PSF_EINVAL, "null or unaligned k or v");
+  DeviceInfo* dev = nullptr;
+  if ((rc = device_info(&dev))) return rc;
+  cudaError_t e = launch_cache_append(c, s, k, vk.ss, vk.sh, v, vv.ss, vv.sh, dtype == PSF_DTYPE_F16, dev->status,
+                                      static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PSF_OK : cuda_fail(e, "cache append launch");
+}
+
+size_t psf_attn_cache_workspace_size(int B, int max_pages, int page_size, int Hq, int Hkv, int Dqk, int Dv,
+                                     int max_q, int flags) {
+  if (B < 1 || max_pages < 1 || page_size < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || Dqk < 1 || Dv < 1 || max_q < 0)
+    return 0;
+  return 256;
+}
+
+int psf_attn_cache_fwd(const void* q, const psf_kv_cache* cache, void* out, float* lse, const int32_t* cu_q,
+                       const int32_t* page_table, const int32_t* seq_lens, int B, int max_pages, int T, int max_q,
+                       int Hq, const int64_t* strides, int dtype, float scale, int causal, int32_t window_left,
+                       float softcap, int flags, void* workspace, size_t ws_bytes, void* stream) {
+  CacheAttnParams p;
+  memset(&p, 0, sizeof(p));
+  int rc;
+  if ((rc = cache_view(cache, &p.c)) || (rc = check_dtype(dtype)) || (rc = check_softcap(softcap)) ||
+      (rc = seq_view(page_table, seq_lens, cu_q, B, max_pages, p.c.page, T, &p.s)) ||
+      (rc = check_common(PSF_LAYOUT_THD, 1, T, 0, Hq, p.c.Hkv, p.c.Dqk, p.c.Dv, scale, window_left, B)))
+    return rc;
+  if (flags & ~PSF_CACHE_ACCUMULATE) return fail(PSF_EINVAL, "unknown cache attention flags 0x%x", flags);
+  if ((flags & PSF_CACHE_ACCUMULATE) && !cache->weight)
+    return fail(PSF_EINVAL, "PSF_CACHE_ACCUMULATE needs a cache with weights");
+  if (Hq > 65535) return fail(PSF_EINVAL, "more than 65535 query heads");
+  if (max_q < 0 || (!cu_q && max_q < p.s.each))
+    return fail(PSF_EINVAL, "max_q=%d is less than the %d rows per sequence", max_q, p.s.each);
+  View vq, vo;
+  if ((rc = strided_view(strides, 0, "q", PSF_LAYOUT_THD, 1, T, Hq, p.c.Dqk, false, &vq)) ||
+      (rc = strided_view(strides, 1, "out", PSF_LAYOUT_THD, 1, T, Hq, p.c.Dv, true, &vo)))
+    return rc;
+  if (T == 0) return PSF_OK;
+  if (!q || !out || !lse || !aligned16(q) || !aligned16(out)) return fail(PSF_EINVAL, "null or unaligned q, out or lse");
+  const size_t need = psf_attn_cache_workspace_size(B, max_pages, p.c.page, Hq, p.c.Hkv, p.c.Dqk, p.c.Dv, max_q, flags);
+  if (!workspace || ws_bytes < need || !aligned16(workspace))
+    return fail(PSF_EWORKSPACE, "cache attention workspace needs %zu bytes, 16-byte aligned (got %zu)", need, ws_bytes);
+  DeviceInfo* dev = nullptr;
+  if ((rc = device_info(&dev))) return rc;
+  p.s.max_rows = max_q;
+  p.q = q;
+  p.q_ss = vq.ss;
+  p.q_sh = vq.sh;
+  p.out = out;
+  p.o_ss = vo.ss;
+  p.o_sh = vo.sh;
+  p.lse = lse;
+  p.Hq = Hq;
+  p.G = Hq / p.c.Hkv;
+  p.scale = scale;
+  p.softcap = softcap;
+  p.causal = causal ? 1 : 0;
+  p.window = window_left > 0 ? (int)window_left : 0;
+  p.accumulate = (flags & PSF_CACHE_ACCUMULATE) ? 1 : 0;
+  p.f16 = dtype == PSF_DTYPE_F16;
+  p.status = dev->status;
+  p.limit_ns = g_wait_limit_ns;
+  cudaError_t e = launch_cache_attn(p, dev->sms, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PSF_OK : cuda_fail(e, "cache attention launch");
+}
+
+size_t psf_kv_cache_evict_workspace_size(int B, int max_pages, int page_size, int Hkv, int budget) {
+  if (B < 1 || max_pages < 1 || page_size < 1 || Hkv < 1 || budget < 1) return 0;
+  return evict_ws_layout(B, max_pages, page_size, Hkv, budget, nullptr, nullptr);
+}
+
+int psf_kv_cache_evict(const psf_kv_cache* cache, const int32_t* page_table, const int32_t* seq_lens,
+                       int32_t* new_lens, int B, int max_pages, int budget, int recent, void* workspace,
+                       size_t ws_bytes, void* stream) {
+  CacheView c;
+  SeqView s;
+  int rc;
+  if ((rc = cache_view(cache, &c)) || (rc = seq_view(page_table, seq_lens, nullptr, B, max_pages, c.page, 0, &s)))
+    return rc;
+  if (!c.weight) return fail(PSF_EINVAL, "eviction needs a cache with weights");
+  if (budget < 1 || recent < 0 || recent > budget)
+    return fail(PSF_EINVAL, "need budget >= 1 and 0 <= recent <= budget (got budget=%d recent=%d)", budget, recent);
+  if (!new_lens || new_lens == seq_lens) return fail(PSF_EINVAL, "new_lens must be given and not be seq_lens");
+  const size_t need = psf_kv_cache_evict_workspace_size(B, max_pages, c.page, c.Hkv, budget);
+  if (!workspace || ws_bytes < need || !aligned16(workspace))
+    return fail(PSF_EWORKSPACE, "eviction workspace needs %zu bytes, 16-byte aligned (got %zu)", need, ws_bytes);
+  DeviceInfo* dev = nullptr;
+  if ((rc = device_info(&dev))) return rc;
+  EvictWorkspace w;
+  evict_ws_layout(B, max_pages, c.page, c.Hkv, budget, &w, workspace);
+  cudaError_t e = launch_cache_evict(c, s, budget, recent, new_lens, w, dev->sms, dev->status,
+                                     static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PSF_OK : cuda_fail(e, "eviction launch");
+}
+
+int psf_kv_cache_gather(const psf_kv_cache* cache, const int32_t* page_table, const int32_t* seq_lens, int B,
+                        int max_pages, void* k, void* v, int32_t* cu_k, int total_k, int dtype, void* stream) {
+  CacheView c;
+  SeqView s;
+  int rc;
+  if ((rc = cache_view(cache, &c)) || (rc = check_dtype(dtype)) ||
+      (rc = seq_view(page_table, seq_lens, nullptr, B, max_pages, c.page, 0, &s)))
+    return rc;
+  if (total_k < 0) return fail(PSF_EINVAL, "total_k < 0");
+  if (!cu_k || (total_k > 0 && (!k || !v || !aligned16(k) || !aligned16(v))))
+    return fail(PSF_EINVAL, "null or unaligned output");
+  DeviceInfo* dev = nullptr;
+  if ((rc = device_info(&dev))) return rc;
+  cudaError_t e = launch_cache_gather(c, s, k, v, cu_k, total_k, dtype == PSF_DTYPE_F16, dev->status,
+                                      static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PSF_OK : cuda_fail(e, "cache gather launch");
 }
 
 }  // extern "C"

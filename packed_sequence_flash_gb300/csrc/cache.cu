@@ -1,0 +1,477 @@
+// cache.cu -- the memory-bound kernels of the 8-bit paged cache: append
+// (quantise new rows into their pages), gather (pages back to packed 16-bit
+// rows) and eviction (selection of the tokens to keep, compaction in place).
+#include "cache.cuh"
+#include "launch.h"
+#include "launch_cache.h"
+
+namespace psf {
+
+namespace {
+
+// ---------------------------------------------------------------- append
+// One CTA per (sequence, page it enters, head, K or V): the largest new
+// magnitude, the block's scale, the older codes of the page if the scale grew,
+// the new codes. Sequence b's pages are tasks start(b) .. in an index space that
+// leaves floor(cu / page) + 2 b tasks before it, room enough for the
+// floor((n - 2) / page) + 2 pages that n rows can touch, so a CTA finds its
+// page from cu alone.
+constexpr int kAppendThreads = 128;
+constexpr int kAppendHeld = 8;  // 16-byte vectors a thread keeps between its two looks at the rows
+
+template <typename T>
+__global__ void __launch_bounds__(kAppendThreads)
+    append_kernel(CacheView c, SeqView s, const T* kin, int64_t k_ss, int64_t k_sh, const T* vin, int64_t v_ss,
+                  int64_t v_sh, int* status) {
+  __shared__ float warp_top[kAppendThreads / 32];
+  const int tid = threadIdx.x, h = blockIdx.y;
+  const bool is_v = blockIdx.z;
+  auto start = [&](int b) -> int64_t { return (s.cu ? s.cu[b] : b * s.each) / c.page + 2 * (int64_t)b; };
+  const int b = warp_find(s.B, blockIdx.x, start);
+  const Seq q = seq_at(s, c.page, b);
+  if (q.bad || q.m > q.n) {
+    if (tid == 0) record_status(status, kStatusDeviceArgs);
+    return;
+  }
+  const int64_t nth = (int64_t)blockIdx.x - start(b);
+  const int first = q.n - q.m;  // position of the first new token
+  const int64_t pi = (first >> c.page_lg) + nth;
+  if (nth < 0 || q.m == 0 || pi > (q.n - 1) >> c.page_lg) return;
+  const int pg = s.table[(int64_t)b * s.max_pages + pi];
+  if (pg < 0 || pg >= c.pages) {
+    if (tid == 0) record_status(status, kStatusDeviceArgs);
+    return;
+  }
+  const int base = (int)pi << c.page_lg;
+  const int r0 = max(first - base, 0), r1 = min(q.n - base, c.page);  // new rows of the page
+  const int D = is_v ? c.Dv : c.Dqk;
+  const int lg = D == 192 ? 0 : 31 - __clz(D >> 3);
+  const int vecs = D >> 3;  // 8-element vectors of a row
+  const T* in = is_v ? vin : kin;
+  const int64_t ss = is_v ? v_ss : k_ss;
+  in += (is_v ? v_sh : k_sh) * h + ss * (q.q0 + base + r0 - first);
+  uint8_t* out = is_v ? c.v + c.v_sp * pg + c.v_sh * h : c.k + c.k_sp * pg + c.k_sh * h;
+  const int64_t sr = is_v ? c.v_sr : c.k_sr;
+  float* scale_at = (is_v ? c.v_scale : c.k_scale) + (int64_t)pg * c.Hkv + h;
+  const int items = (r1 - r0) * vecs;
+  auto row_of = [&](int i) { return D == 192 ? i / 24 : i >> lg; };
+
+  uint4 held[kAppendHeld];
+  float top = 0.f;
+  auto look = [&](const uint4& x) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 f = unpack2<T>(w[j]);
+      const float a = fabsf(f.x), d = fabsf(f.y);
+      top = fmaxf(top, a <= 3.402823466e38f ? a : 0.f);
+      top = fmaxf(top, d <= 3.402823466e38f ? d : 0.f);
+    }
+  };
+  auto load = [&](int i) {
+    const int r = row_of(i);
+    return *reinterpret_cast<const uint4*>(in + ss * r + (i - r * vecs) * 8);
+  };
+#pragma unroll
+  for (int u = 0; u < kAppendHeld; ++u) {
+    const int i = u * kAppendThreads + tid;
+    held[u] = i < items ? load(i) : make_uint4(0, 0, 0, 0);
+  }
+#pragma unroll
+  for (int u = 0; u < kAppendHeld; ++u) look(held[u]);
+  for (int i = kAppendHeld * kAppendThreads + tid; i < items; i += kAppendThreads) look(load(i));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if ((tid & 31) == 0) warp_top[tid >> 5] = top;
+  const float old = *scale_at;
+  __syncthreads();  // also: every thread has read the old scale
+#pragma unroll
+  for (int w = 0; w < kAppendThreads / 32; ++w) top = fmaxf(top, warp_top[w]);
+  const float fresh = block_scale(top);
+  const float scale = r0 > 0 ? fmaxf(fresh, old) : fresh;
+  if (tid == 0 && (r0 == 0 || scale != old)) *scale_at = scale;
+
+  if (r0 > 0 && scale != old) {
+    const float r = old / scale;
+    for (int i = tid; i < r0 * (D >> 4); i += kAppendThreads) {
+      const int row = i / (D >> 4);
+      uint4* at = reinterpret_cast<uint4*>(out + sr * row + (i - row * (D >> 4)) * 16);
+      uint4 x = *at;
+      x.x = rescale4(x.x, r);
+      x.y = rescale4(x.y, r);
+      x.z = rescale4(x.z, r);
+      x.w = rescale4(x.w, r);
+      *at = x;
+    }
+  }
+  auto put = [&](int i, const uint4& x) {
+    const int row = row_of(i);
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    uint32_t e[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 f = unpack2<T>(w[j]);
+      e[j] = e4m3_pair(finite_or_nan(f.x) / scale, finite_or_nan(f.y) / scale);
+    }
+    *reinterpret_cast<uint2*>(out + sr * (r0 + row) + (i - row * vecs) * 8) =
+        make_uint2(e[0] | (e[1] << 16), e[2] | (e[3] << 16));
+  };
+#pragma unroll
+  for (int u = 0; u < kAppendHeld; ++u) {
+    const int i = u * kAppendThreads + tid;
+    if (i < items) put(i, held[u]);
+  }
+  for (int i = kAppendHeld * kAppendThreads + tid; i < items; i += kAppendThreads) put(i, load(i));
+  if (!is_v && c.weight)
+    for (int r = r0 + tid; r < r1; r += kAppendThreads) c.weight[((int64_t)pg * c.Hkv + h) * c.page + r] = 0.f;
+}
+
+// ---------------------------------------------------------------- gather
+// cu_k = prefix sums of the lengths (one CTA).
+constexpr int kPrefixThreads = 1024;
+__global__ void __launch_bounds__(kPrefixThreads)
+    gather_prefix_kernel(SeqView s, int page, int32_t* cu_k, int64_t total_k, int* status) {
+  __shared__ int64_t tot[32];
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  int64_t carry = 0;
+  for (int base = 0; base < s.B; base += kPrefixThreads) {
+    const int b = base + tid;
+    int64_t x = 0;
+    if (b < s.B) {
+      const int n = s.lens[b];
+      if (n < 0 || (int64_t)n > (int64_t)s.max_pages * page)
+        record_status(status, kStatusDeviceArgs);
+      else
+        x = n;
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) tot[wid] = x;
+    __syncthreads();
+    int64_t before = 0, all = 0;
+    for (int w = 0; w < 32; ++w) {
+      before += w < wid ? tot[w] : 0;
+      all += tot[w];
+    }
+    const int64_t sum = carry + before + x;
+    if (b < s.B) cu_k[b + 1] = (int32_t)min(sum, (int64_t)0x7fffffff);
+    carry += all;
+    __syncthreads();
+  }
+  if (tid == 0) {
+    cu_k[0] = 0;
+    if (carry > total_k) record_status(status, kStatusDeviceArgs);
+  }
+}
+
+// One CTA per (sequence, page, head, K or V); sequence b's pages are tasks
+// floor(cu_k / page) + b onwards (a sequence of n tokens has at most
+// floor(n / page) + 1 pages). Rows at or past total_k are not written.
+constexpr int kGatherThreads = 128;
+template <typename T>
+__global__ void __launch_bounds__(kGatherThreads)
+    gather_kernel(CacheView c, SeqView s, const int32_t* cu_k, T* ko, T* vo, int64_t total_k, int* status) {
+  const int tid = threadIdx.x, h = blockIdx.y;
+  const bool is_v = blockIdx.z;
+  auto start = [&](int b) -> int64_t { return cu_k[b] / c.page + (int64_t)b; };
+  const int b = warp_find(s.B, blockIdx.x, start);
+  const int64_t pi = (int64_t)blockIdx.x - start(b);
+  const int row0 = cu_k[b], n = cu_k[b + 1] - row0;
+  if (pi < 0 || (pi << c.page_lg) >= n) return;
+  const int pg = s.table[(int64_t)b * s.max_pages + pi];
+  if (pg < 0 || pg >= c.pages) {
+    if (tid == 0) record_status(status, kStatusDeviceArgs);
+    return;
+  }
+  const int D = is_v ? c.Dv : c.Dqk;
+  const int64_t at = row0 + (pi << c.page_lg);
+  const int rows = (int)min((int64_t)min(n - (int)(pi << c.page_lg), c.page), total_k - at);
+  const uint8_t* in = is_v ? c.v + c.v_sp * pg + c.v_sh * h : c.k + c.k_sp * pg + c.k_sh * h;
+  const int64_t sr = is_v ? c.v_sr : c.k_sr;
+  const float scale = (is_v ? c.v_scale : c.k_scale)[(int64_t)pg * c.Hkv + h];
+  T* out = (is_v ? vo : ko) + (at * c.Hkv + h) * D;
+  const int vecs = D >> 4;
+  for (int i = tid; i < rows * vecs; i += kGatherThreads) {
+    const int r = i / vecs, col = (i - r * vecs) * 16;
+    const uint4 x = *reinterpret_cast<const uint4*>(in + sr * r + col);
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    uint32_t o[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 a = e4m3_to_float2(w[j] & 0xffff), d = e4m3_to_float2(w[j] >> 16);
+      o[2 * j] = pack2<T>(a.x * scale, a.y * scale);
+      o[2 * j + 1] = pack2<T>(d.x * scale, d.y * scale);
+    }
+    uint4* to = reinterpret_cast<uint4*>(out + (int64_t)r * c.Hkv * D + col);
+    to[0] = make_uint4(o[0], o[1], o[2], o[3]);
+    to[1] = make_uint4(o[4], o[5], o[6], o[7]);
+  }
+}
+
+// ---------------------------------------------------------------- eviction
+// Order of the weights as unsigned integers: NaN above all, -0 as 0.
+__device__ __forceinline__ uint32_t weight_key(float w) {
+  if (w != w) return 0xffffffffu;
+  const uint32_t u = __float_as_uint(w + 0.f);
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+constexpr int kSelectThreads = 1024;
+
+// Exclusive block-wide prefix sum.
+__device__ int select_scan(int v, int* warp_tot) {
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  int x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) warp_tot[wid] = x;
+  __syncthreads();
+  int before = 0;
+  for (int w = 0; w < wid; ++w) before += warp_tot[w];
+  __syncthreads();
+  return before + x - v;
+}
+
+// One CTA per (head, sequence). The smallest kept weight is found bit by bit
+// over the integer keys (two bits a step, counted in parallel: no atomics, no
+// order), then the kept tokens are listed in their order, the new blocks'
+// scales set and the weights moved. Keys live in shared memory when they fit,
+// else in the workspace.
+__global__ void __launch_bounds__(kSelectThreads)
+    evict_select_kernel(CacheView c, SeqView s, int budget, int recent, int32_t* new_lens, EvictWorkspace ws,
+                        int smem_keys, int* status) {
+  extern __shared__ uint32_t key_smem[];
+  __shared__ int warp_tot[32], cnt[3][32], bad_page;
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  const int h = blockIdx.x, b = blockIdx.y;
+  const int n = s.lens[b];
+  const int32_t* table = s.table + (int64_t)b * s.max_pages;
+  const int64_t unit = (int64_t)b * c.Hkv + h;
+  if (tid == 0) bad_page = n < 0 || (int64_t)n > (int64_t)s.max_pages * c.page;
+  __syncthreads();
+  if (!bad_page && n > budget)
+    for (int i = tid; i < (n + c.page - 1) >> c.page_lg; i += kSelectThreads)
+      if (table[i] < 0 || table[i] >= c.pages) bad_page = 1;
+  __syncthreads();
+  const bool skip = bad_page || n <= budget;
+  if (tid == 0) {
+    if (bad_page) record_status(status, kStatusDeviceArgs);
+    if (h == 0) new_lens[b] = skip ? n : budget;
+    ws.live[unit] = skip ? 0 : 1;
+  }
+  if (skip) return;
+
+  const int old = n - recent, need = budget - recent;
+  uint32_t* keys = old <= smem_keys ? key_smem : ws.keys + unit * ws.cap;
+  auto weight_at = [&](int j) -> float* {
+    return c.weight + ((int64_t)table[j >> c.page_lg] * c.Hkv + h) * c.page + (j & (c.page - 1));
+  };
+  for (int j = tid; j < old; j += kSelectThreads) keys[j] = weight_key(*weight_at(j));
+  __syncthreads();
+  uint32_t thr = 0;
+  for (int bit = 30; bit >= 0; bit -= 2) {
+    const uint32_t one = 1u << bit;
+    int n1 = 0, n2 = 0, n3 = 0;
+    for (int j = tid; j < old; j += kSelectThreads) {
+      const uint32_t k = keys[j];
+      n1 += k >= thr + one;
+      n2 += k >= thr + 2 * one;
+      n3 += k >= thr + 3 * one;
+    }
+    n1 = __reduce_add_sync(0xffffffffu, n1);
+    n2 = __reduce_add_sync(0xffffffffu, n2);
+    n3 = __reduce_add_sync(0xffffffffu, n3);
+    if (lane == 0) {
+      cnt[0][wid] = n1;
+      cnt[1][wid] = n2;
+      cnt[2][wid] = n3;
+    }
+    __syncthreads();
+    n1 = __reduce_add_sync(0xffffffffu, cnt[0][lane]);
+    n2 = __reduce_add_sync(0xffffffffu, cnt[1][lane]);
+    n3 = __reduce_add_sync(0xffffffffu, cnt[2][lane]);
+    thr += n3 >= need ? 3 * one : (n2 >= need ? 2 * one : (n1 >= need ? one : 0));
+    __syncthreads();
+  }
+  // Thread t lists tokens [t per, (t + 1) per); an odd `per` spreads the shared-memory reads.
+  const int per = ((n + kSelectThreads - 1) / kSelectThreads) | 1;
+  const int j0 = min(tid * per, n), j1 = min(j0 + per, n);
+  int above = 0, equal = 0;
+  for (int j = j0; j < min(j1, old); ++j) {
+    above += keys[j] > thr;
+    equal += keys[j] == thr;
+  }
+  int all_above = __reduce_add_sync(0xffffffffu, above);
+  if (lane == 0) cnt[0][wid] = all_above;
+  __syncthreads();
+  all_above = __reduce_add_sync(0xffffffffu, cnt[0][lane]);
+  const int quota = need - all_above;  // tokens with exactly the smallest kept weight: the first ones
+  const int eq_before = select_scan(equal, warp_tot);
+  const int eq_kept = min(max(quota - eq_before, 0), equal);
+  const int mine = above + eq_kept + max(j1 - max(j0, old), 0);
+  int at = select_scan(mine, warp_tot);
+  int32_t* src = ws.src + unit * budget;
+  for (int j = j0, left = eq_kept; j < j1; ++j) {
+    bool keep = j >= old || keys[j] > thr;
+    if (!keep && keys[j] == thr && left > 0) {
+      keep = true;
+      --left;
+    }
+    if (keep) src[at++] = j;
+  }
+  __syncthreads();
+
+  // New blocks: a warp each. scale = the largest of its tokens' scales; the
+  // ratios go to the kernel that moves the codes.
+  const int blocks = (budget + c.page - 1) >> c.page_lg;
+  for (int blk = wid; blk < blocks; blk += kSelectThreads / 32) {
+    float sk[4], sv[4], tk = 0.f, tv = 0.f;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int r = u * 32 + lane, j = (blk << c.page_lg) + r;
+      sk[u] = sv[u] = 0.f;
+      if (r < c.page && j < budget) {
+        const int64_t a = (int64_t)table[src[j] >> c.page_lg] * c.Hkv + h;
+        sk[u] = c.k_scale[a];
+        sv[u] = c.v_scale[a];
+      }
+      tk = fmaxf(tk, sk[u]);
+      tv = fmaxf(tv, sv[u]);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      tk = fmaxf(tk, __shfl_xor_sync(0xffffffffu, tk, o));
+      tv = fmaxf(tv, __shfl_xor_sync(0xffffffffu, tv, o));
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int r = u * 32 + lane, j = (blk << c.page_lg) + r;
+      if (r < c.page && j < budget)
+        ws.ratio[unit * budget + j] = make_float2(tk > 0.f ? sk[u] / tk : 1.f, tv > 0.f ? sv[u] / tv : 1.f);
+    }
+    if (lane == 0) ws.scale[unit * blocks + blk] = make_float2(tk, tv);
+  }
+  __syncthreads();
+  for (int blk = tid; blk < blocks; blk += kSelectThreads) {
+    const float2 t = ws.scale[unit * blocks + blk];
+    const int64_t a = (int64_t)table[blk] * c.Hkv + h;
+    c.k_scale[a] = t.x;
+    c.v_scale[a] = t.y;
+  }
+  // Weights, a batch at a time: a token never moves up, so a batch's writes
+  // touch nothing that a later batch still has to read.
+  for (int base = 0; base < budget; base += kSelectThreads) {
+    const int j = base + tid;
+    const float w = j < budget ? *weight_at(src[j]) : 0.f;
+    __syncthreads();
+    if (j < budget) *weight_at(j) = w;
+  }
+}
+
+// Moves the codes: one CTA per (head, sequence, K or V, column slice), the kept
+// tokens in order and in batches (as for the weights: read a batch, wait, write
+// it). Slices of a row go to CTAs of their own when (head, sequence) pairs alone
+// would not fill the device.
+constexpr int kMoveThreads = 256;
+constexpr int kMoveVecs = 4;
+__global__ void __launch_bounds__(kMoveThreads)
+    evict_move_kernel(CacheView c, SeqView s, int budget, EvictWorkspace ws, int slices) {
+  const int tid = threadIdx.x, h = blockIdx.x, b = blockIdx.y;
+  const bool is_v = blockIdx.z & 1;
+  const int slice = blockIdx.z >> 1;
+  const int64_t unit = (int64_t)b * c.Hkv + h;
+  if (!ws.live[unit]) return;
+  const int D = is_v ? c.Dv : c.Dqk;
+  const int vecs = (D >> 4) / slices;  // 16-byte vectors of this CTA's part of a row
+  const int col = slice * vecs * 16;
+  const int32_t* table = s.table + (int64_t)b * s.max_pages;
+  uint8_t* base = (is_v ? c.v + c.v_sh * h : c.k + c.k_sh * h) + col;
+  const int64_t sp = is_v ? c.v_sp : c.k_sp, sr = is_v ? c.v_sr : c.k_sr;
+  const int32_t* src = ws.src + unit * budget;
+  const float2* ratio = ws.ratio + unit * budget;
+  const int64_t items = (int64_t)budget * vecs;
+  auto at = [&](int j, int v) {
+    return reinterpret_cast<uint4*>(base + sp * table[j >> c.page_lg] + sr * (j & (c.page - 1)) + v * 16);
+  };
+  for (int64_t i0 = 0; i0 < items; i0 += kMoveThreads * kMoveVecs) {
+    uint4 x[kMoveVecs];
+    float r[kMoveVecs];
+#pragma unroll
+    for (int u = 0; u < kMoveVecs; ++u) {
+      const int64_t i = i0 + u * kMoveThreads + tid;
+      if (i < items) {
+        const int j = (int)(i / vecs), v = (int)(i - (int64_t)j * vecs);
+        x[u] = *at(src[j], v);
+        r[u] = is_v ? ratio[j].y : ratio[j].x;
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < kMoveVecs; ++u) {
+      const int64_t i = i0 + u * kMoveThreads + tid;
+      if (i < items) {
+        const int j = (int)(i / vecs), v = (int)(i - (int64_t)j * vecs);
+        if (r[u] != 1.f) {
+          x[u].x = rescale4(x[u].x, r[u]);
+          x[u].y = rescale4(x[u].y, r[u]);
+          x[u].z = rescale4(x[u].z, r[u]);
+          x[u].w = rescale4(x[u].w, r[u]);
+        }
+        *at(j, v) = x[u];
+      }
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_cache_append(const CacheView& c, const SeqView& s, const void* k, int64_t k_ss, int64_t k_sh,
+                                const void* v, int64_t v_ss, int64_t v_sh, int f16, int* status, cudaStream_t st) {
+  const dim3 grid((unsigned)(s.T / c.page + 2 * (int64_t)s.B), c.Hkv, 2);
+  if (f16)
+    append_kernel<__half><<<grid, kAppendThreads, 0, st>>>(c, s, static_cast<const __half*>(k), k_ss, k_sh,
+                                                          static_cast<const __half*>(v), v_ss, v_sh, status);
+  else
+    append_kernel<__nv_bfloat16><<<grid, kAppendThreads, 0, st>>>(c, s, static_cast<const __nv_bfloat16*>(k), k_ss,
+                                                                 k_sh, static_cast<const __nv_bfloat16*>(v), v_ss,
+                                                                 v_sh, status);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_cache_gather(const CacheView& c, const SeqView& s, void* k, void* v, int32_t* cu_k,
+                                int64_t total_k, int f16, int* status, cudaStream_t st) {
+  gather_prefix_kernel<<<1, kPrefixThreads, 0, st>>>(s, c.page, cu_k, total_k, status);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || total_k == 0) return e;
+  const dim3 grid((unsigned)(total_k / c.page + s.B), c.Hkv, 2);
+  if (f16)
+    gather_kernel<__half><<<grid, kGatherThreads, 0, st>>>(c, s, cu_k, static_cast<__half*>(k),
+                                                          static_cast<__half*>(v), total_k, status);
+  else
+    gather_kernel<__nv_bfloat16><<<grid, kGatherThreads, 0, st>>>(c, s, cu_k, static_cast<__nv_bfloat16*>(k),
+                                                                 static_cast<__nv_bfloat16*>(v), total_k, status);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_cache_evict(const CacheView& c, const SeqView& s, int budget, int recent, int32_t* new_lens,
+                               const EvictWorkspace& ws, int sms, int* status, cudaStream_t st) {
+  const int smem_keys = (int)min(ws.cap, (int64_t)kEvictSmemKeys);
+  const int smem = smem_keys * 4;
+  cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       kEvictSmemKeys * 4);
+  if (e != cudaSuccess) return e;
+  evict_select_kernel<<<dim3(c.Hkv, s.B), kSelectThreads, smem, st>>>(c, s, budget, recent, new_lens, ws, smem_keys,
+                                                                     status);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  const int slices = 1;
+  evict_move_kernel<<<dim3(c.Hkv, s.B, 2 * slices), kMoveThreads, 0, st>>>(c, s, budget, ws, slices);
+  return cudaGetLastError();
+}
+
+}  // namespace psf

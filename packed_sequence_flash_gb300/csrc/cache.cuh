@@ -1,0 +1,110 @@
+// cache.cuh -- the 8-bit paged key/value cache as the kernels see it, and the
+// arithmetic of its blocks.
+//
+// A page holds `page` tokens (16, 32, 64 or 128) of every KV head: e4m3 codes
+// k [pages][Hkv][page][Dqk] and v [pages][Hkv][page][Dv] (any strides, the row
+// contiguous) with one fp32 scale per (page, head) for K and one for V; a code c
+// stands for c * scale. Token j of sequence b is row j % page of page
+// table[b][j / page]. weight [pages][Hkv][page] is the attention weight that
+// the token has received so far.
+#pragma once
+
+#include <math_constants.h>
+#include <stdint.h>
+
+#include "common.cuh"
+
+namespace psf {
+
+struct CacheView {
+  uint8_t *k, *v;
+  float *k_scale, *v_scale;  // [pages][Hkv]
+  float* weight;             // [pages][Hkv][page], nullable
+  int64_t k_sp, k_sh, k_sr, v_sp, v_sh, v_sr;  // strides (page, head, row) in bytes
+  int pages, page, page_lg, Hkv, Dqk, Dv;
+};
+
+// The sequences of a call. cu (nullable): exclusive prefix sums of the rows
+// (query rows, or new tokens) that each sequence has in a packed tensor of T
+// rows; without it every sequence has `each` rows.
+struct SeqView {
+  const int32_t* table;  // [B][max_pages]
+  const int32_t* lens;   // [B] tokens in the cache
+  const int32_t* cu;
+  int B, max_pages, T, each;
+  int max_rows;  // most rows of a sequence
+};
+
+// Sequence b: n tokens in the cache, m rows of the packed tensor from row q0.
+// A description that cannot be right (lengths past the page table, rows outside
+// the tensor) sets bad and leaves the sequence without tokens and rows.
+struct Seq {
+  int n, m, q0;
+  bool bad;
+};
+__device__ __forceinline__ Seq seq_at(const SeqView& s, int page, int b) {
+  Seq r;
+  r.n = s.lens[b];
+  r.q0 = s.cu ? s.cu[b] : b * s.each;
+  r.m = s.cu ? s.cu[b + 1] - r.q0 : s.each;
+  r.bad = r.n < 0 || (int64_t)r.n > (int64_t)s.max_pages * page || r.q0 < 0 || r.m < 0 || r.m > s.max_rows ||
+          (int64_t)r.q0 + r.m > s.T;
+  if (r.bad) {
+    r.n = 0;
+    r.m = 0;
+  }
+  return r;
+}
+
+// Scale of a block whose largest magnitude is a (finite, >= 0): the smallest
+// power of two s >= 2^-126 with a <= 448 s (448 = 1.75 * 2^8 is the largest e4m3
+// value). A power of two costs no precision in a floating format and keeps a
+// later change of scale exact down to the format's subnormals.
+__device__ __forceinline__ float block_scale(float a) {
+  const int bits = __float_as_int(a);
+  const int e = (bits >> 23) - 8 + ((bits & 0x7fffff) > 0x600000 ? 1 : 0);
+  return __int_as_float(min(max(e, 1), 254) << 23);
+}
+
+// Two fp32 values -> two e4m3 codes (round to nearest even), lo in the low byte.
+// |x| never exceeds 448 by more than a rounding here; what is not finite becomes NaN.
+__device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Two e4m3 codes -> two fp16 values (exact), low byte in the low half.
+__device__ __forceinline__ uint32_t e4m3_to_half2(uint32_t pair) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"((uint16_t)pair));
+  return d;
+}
+__device__ __forceinline__ float2 e4m3_to_float2(uint32_t pair) {
+  const uint32_t h = e4m3_to_half2(pair);
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+// Four codes times r, rounded to e4m3 again.
+__device__ __forceinline__ uint32_t rescale4(uint32_t codes, float r) {
+  const float2 a = e4m3_to_float2(codes & 0xffff), b = e4m3_to_float2(codes >> 16);
+  return e4m3_pair(a.x * r, a.y * r) | (e4m3_pair(b.x * r, b.y * r) << 16);
+}
+__device__ __forceinline__ float finite_or_nan(float x) { return fabsf(x) <= 3.402823466e38f ? x : CUDART_NAN_F; }
+
+// Largest b in [0, B) with start(b) <= x, start increasing with start(0) <= x;
+// every lane of the warp returns it. 32 probes a step: two dependent loads up
+// to 1024 sequences.
+template <typename F>
+__device__ __forceinline__ int warp_find(int B, int64_t x, F start) {
+  int lo = 0, hi = B;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) >> 5;
+    const int probe = lo + (int)(threadIdx.x & 31) * step;
+    const bool in = probe < hi && start(probe) <= x;
+    const int c = __popc(__ballot_sync(0xffffffffu, in));
+    lo += (c - 1) * step;
+    hi = min(hi, lo + step);
+  }
+  return lo;
+}
+
+}  // namespace psf

@@ -1,0 +1,52 @@
+// launch_cache.h -- host-side launchers of the 8-bit cache's kernels.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "cache.cuh"
+
+namespace psf {
+
+// Eviction workspace: per (sequence, head) whether it is evicted from, the kept
+// tokens in order, the ratios old / new scale of each (K, V), the new blocks'
+// scales and, for sequences whose keys do not fit in shared memory, the keys.
+constexpr int kEvictSmemKeys = 48 * 1024;
+struct EvictWorkspace {
+  int* live;       // [B][Hkv]
+  int32_t* src;    // [B][Hkv][budget]
+  float2* ratio;   // [B][Hkv][budget]
+  float2* scale;   // [B][Hkv][blocks]
+  uint32_t* keys;  // [B][Hkv][cap], used when cap > kEvictSmemKeys
+  int64_t cap;     // tokens a page table row can hold
+};
+
+// New rows k, v (strides in elements: row, head) into the cache.
+cudaError_t launch_cache_append(const CacheView& c, const SeqView& s, const void* k, int64_t k_ss, int64_t k_sh,
+                                const void* v, int64_t v_ss, int64_t v_sh, int f16, int* status, cudaStream_t st);
+// Cached rows as packed 16-bit [total_k, Hkv, D], and their prefix sums.
+cudaError_t launch_cache_gather(const CacheView& c, const SeqView& s, void* k, void* v, int32_t* cu_k,
+                                int64_t total_k, int f16, int* status, cudaStream_t st);
+// Selection of the kept tokens, then compaction in place.
+cudaError_t launch_cache_evict(const CacheView& c, const SeqView& s, int budget, int recent, int32_t* new_lens,
+                               const EvictWorkspace& ws, int sms, int* status, cudaStream_t st);
+
+struct CacheAttnParams {
+  CacheView c;
+  SeqView s;
+  const void* q;
+  int64_t q_ss, q_sh;  // strides in elements (row, head)
+  void* out;
+  int64_t o_ss, o_sh;
+  float* lse;  // [Hq][T]
+  int Hq, G;
+  float scale, softcap;
+  int causal, window;  // window > 0: left window counting the current token
+  int accumulate;      // add each key's probabilities to c.weight
+  int f16;
+  int* status;
+  uint64_t limit_ns;
+};
+cudaError_t launch_cache_attn(const CacheAttnParams& p, int sms, cudaStream_t st);
+
+}  // namespace psf
