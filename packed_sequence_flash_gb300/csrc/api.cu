@@ -656,8 +656,8 @@ int cache_view(const psf_kv_cache* cache, CacheView* v) {
 
 int seq_view(const int32_t* page_table, const int32_t* seq_lens, const int32_t* cu, int B, int max_pages,
              int page_size, int T, SeqView* s) {
-  if (B < 1 || B > 65535 || max_pages < 1 || T < 0)
-    return fail(PSF_EINVAL, "need 1 <= B <= 65535, max_pages >= 1 and T >= 0 (got B=%d max_pages=%d T=%d)", B, max_pages, T);
+  if (B < 1 || B > 65534 || max_pages < 1 || T < 0)
+    return fail(PSF_EINVAL, "need 1 <= B <= 65534, max_pages >= 1 and T >= 0 (got B=%d max_pages=%d T=%d)", B, max_pages, T);
   if ((int64_t)max_pages * page_size > 0x7fffffff) return fail(PSF_EINVAL, "max_pages * page_size exceeds 2^31 - 1");
   if (!page_table || !seq_lens) return fail(PSF_EINVAL, "null page_table or seq_lens");
   if (!cu && T % B != 0) return fail(PSF_EINVAL, "without prefix sums B=%d must divide T=%d", B, T);
@@ -669,6 +669,37 @@ int seq_view(const int32_t* page_table, const int32_t* seq_lens, const int32_t* 
   s->T = T;
   s->each = cu ? 0 : T / B;
   s->max_rows = T;
+  return PSF_OK;
+}
+
+// Partial results of two units per CTA, sized for the largest SM count this
+// library targets, and the scores when weights are accumulated.
+size_t cache_attn_ws_layout(int B, int max_pages, int page_size, int Hq, int Hkv, int Dqk, int Dv, int max_q,
+                            int accumulate, CacheAttnParams* p, void* base) {
+  const int64_t rows = (int64_t)max_q * (Hq / Hkv), cap = (int64_t)max_pages * page_size;
+  const int nt = cache_attn_nt(Dqk, rows);
+  const size_t slots = 2 * (size_t)kMaxSms * cache_attn_ctas(Dqk, nt) * 8 * nt;
+  const size_t l_off = align256(sizeof(float) * slots * Dv);
+  const size_t s_off = l_off + align256(sizeof(float) * slots);
+  if (p && base) {
+    char* b = static_cast<char*>(base);
+    p->part_o = reinterpret_cast<float*>(b);
+    p->part_l = reinterpret_cast<float*>(b + l_off);
+    p->scores = reinterpret_cast<float*>(b + s_off);
+    p->score_rows = rows;
+    p->score_cap = cap;
+  }
+  return s_off + (accumulate ? sizeof(float) * (size_t)(B * (int64_t)Hkv * rows * cap) : 0);
+}
+
+// TMA view (d, row, head, page) of cache codes: boxes of one plane of a page's
+// rows, at most 64 of them.
+int cache_map(CUtensorMap* m, const uint8_t* base, const CacheView& c, int D, int64_t sp, int64_t sh, int64_t sr) {
+  const int width = D == 64 ? 64 : 128;
+  int rc = make_tmap_4d(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, base, D, c.page, c.Hkv, c.pages, sr, sh, sp, width,
+                        c.page < 64 ? c.page : 64,
+                        D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
+  if (rc) return fail(PSF_ECUDA, "cuTensorMapEncodeTiled failed (%d) for a cache of %d pages", rc, c.pages);
   return PSF_OK;
 }
 
@@ -968,7 +999,8 @@ size_t psf_attn_cache_workspace_size(int B, int max_pages, int page_size, int Hq
                                      int max_q, int flags) {
   if (B < 1 || max_pages < 1 || page_size < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || Dqk < 1 || Dv < 1 || max_q < 0)
     return 0;
-  return 256;
+  return cache_attn_ws_layout(B, max_pages, page_size, Hq, Hkv, Dqk, Dv, max_q, flags & PSF_CACHE_ACCUMULATE, nullptr,
+                              nullptr);
 }
 
 int psf_attn_cache_fwd(const void* q, const psf_kv_cache* cache, void* out, float* lse, const int32_t* cu_q,
@@ -1017,7 +1049,12 @@ int psf_attn_cache_fwd(const void* q, const psf_kv_cache* cache, void* out, floa
   p.f16 = dtype == PSF_DTYPE_F16;
   p.status = dev->status;
   p.limit_ns = g_wait_limit_ns;
-  cudaError_t e = launch_cache_attn(p, dev->sms, static_cast<cudaStream_t>(stream));
+  p.min_tiles = 2;
+  cache_attn_ws_layout(B, max_pages, p.c.page, Hq, p.c.Hkv, p.c.Dqk, p.c.Dv, max_q, p.accumulate, &p, workspace);
+  if ((rc = cache_map(&p.tm_k, p.c.k, p.c, p.c.Dqk, p.c.k_sp, p.c.k_sh, p.c.k_sr)) ||
+      (rc = cache_map(&p.tm_v, p.c.v, p.c, p.c.Dv, p.c.v_sp, p.c.v_sh, p.c.v_sr)))
+    return rc;
+  cudaError_t e = launch_cache_attn(p, max_q, dev->sms, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? PSF_OK : cuda_fail(e, "cache attention launch");
 }
 

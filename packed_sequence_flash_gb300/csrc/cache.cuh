@@ -37,7 +37,7 @@ struct SeqView {
 
 // Sequence b: n tokens in the cache, m rows of the packed tensor from row q0.
 // A description that cannot be right (lengths past the page table, rows outside
-// the tensor) sets bad and leaves the sequence without tokens and rows.
+// the tensor) sets bad and leaves the sequence without tokens (and rows).
 struct Seq {
   int n, m, q0;
   bool bad;
@@ -47,12 +47,10 @@ __device__ __forceinline__ Seq seq_at(const SeqView& s, int page, int b) {
   r.n = s.lens[b];
   r.q0 = s.cu ? s.cu[b] : b * s.each;
   r.m = s.cu ? s.cu[b + 1] - r.q0 : s.each;
-  r.bad = r.n < 0 || (int64_t)r.n > (int64_t)s.max_pages * page || r.q0 < 0 || r.m < 0 || r.m > s.max_rows ||
-          (int64_t)r.q0 + r.m > s.T;
-  if (r.bad) {
-    r.n = 0;
-    r.m = 0;
-  }
+  const bool rows_bad = r.q0 < 0 || r.m < 0 || r.m > s.max_rows || (int64_t)r.q0 + r.m > s.T;
+  r.bad = rows_bad || r.n < 0 || (int64_t)r.n > (int64_t)s.max_pages * page;
+  if (r.bad) r.n = 0;
+  if (rows_bad) r.m = 0;
   return r;
 }
 

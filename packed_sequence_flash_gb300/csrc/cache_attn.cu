@@ -1,166 +1,90 @@
-// cache_attn.cu -- attention of a few query rows per sequence over the 8-bit
-// paged cache.
-#include "cache.cuh"
-#include "launch_cache.h"
+// cache_attn.cu -- launches of the cache attention: the main kernel, the join of
+// partial results, and the weights.
+#include "cache_attn.cuh"
 
 namespace psf {
 
 namespace {
 
-// Keys [lo, hi) that row i of a sequence with m rows and n cached tokens sees
-// (the last row sits at the last token).
-__device__ __forceinline__ void row_keys(const CacheAttnParams& p, int n, int m, int i, int& lo, int& hi) {
-  const int at = i + n - m;
-  hi = p.causal ? min(n, at + 1) : n;
-  lo = p.window > 0 ? max(0, at - p.window + 1) : 0;
-  if (hi < lo) hi = lo;
-}
-
-__device__ __forceinline__ float logit(const CacheAttnParams& p, float dot) {
-  const float z = dot * p.scale;
-  return p.softcap > 0.f ? p.softcap * tanhf(z / p.softcap) : z;
-}
-
-// One CTA per (query row, query head): the scores of all keys in two passes
-// (maximum and sum, then the weighted values), all in fp32.
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-template <typename T>
-__global__ void __launch_bounds__(kThreads) cache_attn_kernel(const CacheAttnParams p) {
-  __shared__ float qs[512], red[2][kWarps], acc[512];
+// Weights of the keys, from the stored scores and the finished lse: a thread per
+// key sums exp2(score - lse) over the rows that see it, in their order, and
+// adds the sum once (atomically: another sequence may share the page).
+constexpr int kWeightThreads = 256;
+__global__ void __launch_bounds__(kWeightThreads) cache_weight_kernel(const __grid_constant__ CacheAttnParams p) {
   const CacheView& c = p.c;
-  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-  const int t = blockIdx.x, hq = blockIdx.y, h = hq / p.G;
-  T* out = static_cast<T*>(p.out) + p.o_ss * t + p.o_sh * hq;
-  float* lse = p.lse + (int64_t)hq * p.s.T + t;
-  int b = 0;
-  if (p.s.cu)
-    b = warp_find(p.s.B, t, [&](int x) -> int64_t { return p.s.cu[x]; });
-  else
-    b = p.s.each ? t / p.s.each : 0;
-  Seq q = seq_at(p.s, c.page, b);
-  if (q.bad && tid == 0) record_status(p.status, kStatusDeviceArgs);
-  int lo = 0, hi = 0;
-  if (t >= q.q0 && t < q.q0 + q.m) row_keys(p, q.n, q.m, t - q.q0, lo, hi);
-  const T* qr = static_cast<const T*>(p.q) + p.q_ss * t + p.q_sh * hq;
-  for (int d = tid; d < c.Dqk; d += kThreads) qs[d] = (float)qr[d];
-  for (int d = tid; d < 512; d += kThreads) acc[d] = 0.f;
-  __syncthreads();
-  const int32_t* table = p.s.table + (int64_t)b * p.s.max_pages;
-  auto page_of = [&](int j) {
-    int pg = table[j >> c.page_lg];
-    if (pg < 0 || pg >= c.pages) {
-      record_status(p.status, kStatusDeviceArgs);
-      pg = 0;
-    }
-    return pg;
-  };
-  auto score = [&](int j) {
-    const int pg = page_of(j);
-    const uint8_t* k = c.k + c.k_sp * pg + c.k_sh * h + c.k_sr * (j & (c.page - 1));
-    float dot = 0.f;
-    for (int d = lane * 2; d < c.Dqk; d += 64) {
-      const float2 x = e4m3_to_float2(*reinterpret_cast<const uint16_t*>(k + d));
-      dot = fmaf(x.x, qs[d], fmaf(x.y, qs[d + 1], dot));
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-    return logit(p, dot * c.k_scale[(int64_t)pg * c.Hkv + h]);
-  };
-  float top = -CUDART_INF_F, sum = 0.f;
-  for (int j = lo + wid; j < hi; j += kWarps) {
-    const float z = score(j), m = fmaxf(top, z);
-    sum = sum * __expf(top - m) + expf(z - m);
-    top = m;
-  }
-  if (lane == 0) {
-    red[0][wid] = top;
-    red[1][wid] = sum;
-  }
-  __syncthreads();
-  float all = -CUDART_INF_F, total = 0.f;
-  for (int w = 0; w < kWarps; ++w) all = fmaxf(all, red[0][w]);
-  for (int w = 0; w < kWarps; ++w)
-    if (red[1][w] > 0.f || red[1][w] != red[1][w]) total += red[1][w] * expf(red[0][w] - all);
-  const float l = hi > lo ? all + logf(total) : -CUDART_INF_F;
-  float o[16];
-  for (int u = 0; u < 16; ++u) o[u] = 0.f;
-  for (int j = lo + wid; j < hi; j += kWarps) {
-    const float w = expf(score(j) - l);
-    const int pg = page_of(j);
-    const uint8_t* v = c.v + c.v_sp * pg + c.v_sh * h + c.v_sr * (j & (c.page - 1));
-    const float wv = w * c.v_scale[(int64_t)pg * c.Hkv + h];
-    for (int u = 0, d = lane * 2; d < c.Dv; d += 64, u += 2) {
-      const float2 x = e4m3_to_float2(*reinterpret_cast<const uint16_t*>(v + d));
-      o[u] = fmaf(x.x, wv, o[u]);
-      o[u + 1] = fmaf(x.y, wv, o[u + 1]);
-    }
-  }
-  for (int w = 0; w < kWarps; ++w) {
-    if (wid == w)
-      for (int u = 0, d = lane * 2; d < c.Dv; d += 64, u += 2) {
-        acc[d] += o[u];
-        acc[d + 1] += o[u + 1];
-      }
-    __syncthreads();
-  }
-  for (int d = tid * 2; d < c.Dv; d += kThreads * 2)
-    *reinterpret_cast<uint32_t*>(out + d) = pack2<T>(acc[d], acc[d + 1]);
-  if (tid == 0) *lse = l;
-}
-
-// Weights of the keys, from the finished lse: a warp per (sequence, KV head,
-// key) sums exp(z - lse) over the rows and heads that see the key, in their order,
-// and adds the sum once (atomically: another sequence may share the page).
-template <typename T>
-__global__ void __launch_bounds__(kThreads) cache_weight_kernel(const CacheAttnParams p) {
-  const CacheView& c = p.c;
-  const int lane = threadIdx.x & 31;
-  const int b = blockIdx.z, h = blockIdx.y;
+  const int b = blockIdx.z, h = blockIdx.y, j = blockIdx.x * kWeightThreads + threadIdx.x;
   const Seq q = seq_at(p.s, c.page, b);
-  for (int j = blockIdx.x * kWarps + (threadIdx.x >> 5); j < q.n; j += gridDim.x * kWarps) {
-    const int pg = p.s.table[(int64_t)b * p.s.max_pages + (j >> c.page_lg)];
-    if (pg < 0 || pg >= c.pages) continue;
-    const uint8_t* k = c.k + c.k_sp * pg + c.k_sh * h + c.k_sr * (j & (c.page - 1));
-    const float ks = c.k_scale[(int64_t)pg * c.Hkv + h];
-    float sum = 0.f;
-    for (int i = 0; i < q.m; ++i) {
-      int lo, hi;
-      row_keys(p, q.n, q.m, i, lo, hi);
-      if (j < lo || j >= hi) continue;
-      for (int g = 0; g < p.G; ++g) {
-        const T* qr = static_cast<const T*>(p.q) + p.q_ss * (q.q0 + i) + p.q_sh * (h * p.G + g);
-        float dot = 0.f;
-        for (int d = lane * 2; d < c.Dqk; d += 64) {
-          const float2 x = e4m3_to_float2(*reinterpret_cast<const uint16_t*>(k + d));
-          dot = fmaf(x.x, (float)qr[d], fmaf(x.y, (float)qr[d + 1], dot));
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-        sum += expf(logit(p, dot * ks) - p.lse[(int64_t)(h * p.G + g) * p.s.T + q.q0 + i]);
-      }
-    }
-    if (lane == 0) atomicAdd(c.weight + ((int64_t)pg * c.Hkv + h) * c.page + (j & (c.page - 1)), sum);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (j >= q.n) return;
+  const int pg = p.s.table[(int64_t)b * p.s.max_pages + (j >> c.page_lg)];
+  if (pg < 0 || pg >= c.pages) return;
+  const float* s = p.scores + (((int64_t)b * c.Hkv + h) * p.score_rows) * p.score_cap + j;
+  float sum = 0.f;
+  for (int i = 0; i < q.m; ++i) {
+    int lo, hi;
+    ca_row_keys(p, q.n, q.m, i, lo, hi);
+    if (j < lo || j >= hi) continue;
+    for (int g = 0; g < p.G; ++g)
+      sum += ex2_approx(s[(int64_t)(i * p.G + g) * p.score_cap] -
+                        p.lse[(int64_t)(h * p.G + g) * p.s.T + q.q0 + i] * 1.4426950408889634f);
   }
+  atomicAdd(c.weight + ((int64_t)pg * c.Hkv + h) * c.page + (j & (c.page - 1)), sum);
+}
+
+// A kernel that may start while the one before it still runs (it waits with griddepcontrol.wait).
+template <typename... A>
+cudaError_t launch_after(void (*kernel)(A...), dim3 grid, int threads, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = st;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <int DQK, int DV, int NT>
+cudaError_t run(CacheAttnParams& p, int max_q, int sms, cudaStream_t st) {
+  using C = CaCfg<DQK, DV, NT>;
+  cudaError_t e = cudaFuncSetAttribute(cache_attn_kernel<DQK, DV, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       C::SMEM);
+  if (e != cudaSuccess) return e;
+  const int grid = sms * C::CTAS;
+  p.row_tiles = max(1, (int)(((int64_t)max_q * p.G + C::R - 1) / C::R));
+  cache_attn_kernel<DQK, DV, NT><<<grid, kCaThreads, C::SMEM, st>>>(p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  return launch_after(cache_join_kernel<DQK, DV, NT>, dim3(p.c.Hkv * p.row_tiles, p.s.B + (p.s.cu ? 1 : 0)),
+                      kJoinThreads, st, (const CacheAttnParams)p, grid);
 }
 
 }  // namespace
 
-cudaError_t launch_cache_attn(const CacheAttnParams& p, int sms, cudaStream_t st) {
-  const dim3 grid(p.s.T, p.Hq);
-  if (p.f16)
-    cache_attn_kernel<__half><<<grid, kThreads, 0, st>>>(p);
+// Row tiles of 8 rows for one group of heads and one token, of 16 and 32 rows
+// where there are more rows; 8 at head dim 512, where O takes 128 registers.
+int cache_attn_nt(int Dqk, int64_t rows) { return Dqk == 512 || rows <= 8 ? 1 : (rows <= 16 ? 2 : 4); }
+
+cudaError_t launch_cache_attn(CacheAttnParams& p, int max_q, int sms, cudaStream_t st) {
+  const int nt = cache_attn_nt(p.c.Dqk, (int64_t)max_q * p.G);
+  cudaError_t e;
+#define PSF_RUN(DQK, DV)                                              \
+  e = nt == 1 ? run<DQK, DV, 1>(p, max_q, sms, st)                    \
+              : (nt == 2 ? run<DQK, DV, 2>(p, max_q, sms, st) : run<DQK, DV, 4>(p, max_q, sms, st))
+  if (p.c.Dqk == 64)
+    PSF_RUN(64, 64);
+  else if (p.c.Dqk == 128)
+    PSF_RUN(128, 128);
+  else if (p.c.Dqk == 192)
+    PSF_RUN(192, 128);
   else
-    cache_attn_kernel<__nv_bfloat16><<<grid, kThreads, 0, st>>>(p);
-  cudaError_t e = cudaGetLastError();
+    e = run<512, 512, 1>(p, max_q, sms, st);
+#undef PSF_RUN
   if (e != cudaSuccess || !p.accumulate) return e;
-  const int keys = p.s.max_pages << p.c.page_lg;
-  const dim3 wgrid((unsigned)(keys + kWarps - 1) / kWarps < 256 ? (keys + kWarps - 1) / kWarps : 256, p.c.Hkv, p.s.B);
-  if (p.f16)
-    cache_weight_kernel<__half><<<wgrid, kThreads, 0, st>>>(p);
-  else
-    cache_weight_kernel<__nv_bfloat16><<<wgrid, kThreads, 0, st>>>(p);
-  return cudaGetLastError();
+  const unsigned chunks = (unsigned)((p.score_cap + kWeightThreads - 1) / kWeightThreads);
+  return launch_after(cache_weight_kernel, dim3(chunks, p.c.Hkv, p.s.B), kWeightThreads, st,
+                      (const CacheAttnParams)p);
 }
 
 }  // namespace psf

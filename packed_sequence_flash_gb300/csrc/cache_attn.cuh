@@ -1,0 +1,834 @@
+// cache_attn.cuh -- attention of a few query rows per sequence over the 8-bit
+// paged cache (sm_103a).
+//
+//   out_i = sum_j p_ij V_j,  p_ij = exp(z_ij - lse_i),  z_ij = scale q_i . K_j (capped)
+//
+// What bounds it: every key and value byte is read once per group of query
+// heads and used for 8 to 32 rows, 2 flop per byte and row, so the kernel is a
+// stream of the cache: the floor is bytes / HBM bandwidth. A 128-row tensor
+// tile (tcgen05) would be nearly empty and would need the codes as 16-bit
+// operands in shared memory, that is every byte expanded and written back
+// once; warp-level products take their operands from registers, where the
+// codes are expanded in place, so the legacy instruction is the fitting one.
+//
+// Rows: the query rows of one KV head (m rows x G heads, token-major) in tiles
+// of R = 8 NT rows. Keys: tiles of 64. A CTA takes an equal share of all
+// (sequence, KV head, row tile, key tile) in that order, wherever it begins and
+// ends, so ragged batches and a single long sequence alike fill the device.
+// A share that covers all tiles of a (sequence, head, row tile) writes its
+// result; otherwise it leaves a partial result (o / l, lse) that the join kernel
+// adds up in the order of the CTAs. Nothing depends on the order of execution.
+//
+//   warp 4     producer: page numbers and scales one batch ahead, K and V pages
+//              by TMA into a ring of stages (128-byte rows, 128-byte swizzle;
+//              64-byte rows for head dim 64)
+//   warps 0-3  16 keys of each tile each, with a softmax state of their own
+//              (nothing but the ring's barriers between them); joined at the
+//              end of the unit
+//
+// S^T = K Q^T: 16 keys are the rows of the product, 8 query rows its columns,
+// so a group of up to 8 heads wastes nothing. The order in which the head dim
+// is contracted is free, so a lane reads 16 consecutive codes of its two key
+// rows and its Q operand is arranged to match. O^T += V^T P^T likewise: a lane
+// reads 16 consecutive codes of four keys, pairs up keys with byte permutes,
+// and owns those 16 head-dim rows of O^T. P^T is S^T's accumulator transposed
+// in registers (movmatrix). The map R from a position in the product to a key row is
+// chosen so that neither kind of read has a bank conflict under the swizzle.
+//
+// Numbers: codes are exact in fp16. Q rows are scaled by a power of two into
+// fp16's range (exact for what matters: 28 octaves below the row's largest).
+// Scores, sums and O are fp32. P enters the product with V in fp16, scaled to at
+// most 2^15 by a reference that includes the block's V scale, so that blocks of
+// very different scales stay in range; the row sum has a reference without it.
+// Both references move only when a score exceeds them by 2^8, which a warp vote
+// finds. bf16 would round P 8 times as coarsely for no gain in range.
+#pragma once
+
+#include "cache.cuh"
+#include "launch_cache.h"
+
+namespace psf {
+
+constexpr int kCaKeys = 64;       // keys per tile
+constexpr int kCaWarps = 4;       // consumer warps, 16 keys of a tile each
+constexpr int kCaThreads = 160;
+constexpr float kCaLazy = 8.f;    // a reference moves when a score is 2^8 above it
+constexpr float kCaHead = 7.f;    // the P reference sits 2^7 below the largest value
+
+template <int DQK, int DV, int NT>
+struct CaCfg {
+  static constexpr int R = 8 * NT;
+  static constexpr int KP = DQK <= 128 ? 1 : (DQK + 127) / 128;  // 128-byte planes of a K row
+  static constexpr int VP = DV <= 128 ? 1 : (DV + 127) / 128;
+  static constexpr int ROWB = DQK == 64 ? 64 : 128;  // bytes of a row in a plane
+  static constexpr int PLANE = kCaKeys * ROWB;
+  static constexpr int STAGE = (KP + VP) * PLANE;
+  static constexpr int CTAS = cache_attn_ctas(DQK, NT);
+  static constexpr int QPITCH = DQK + 8;  // fp16 elements
+  static constexpr int OPITCH = DV + 4;   // fp32 elements
+  static constexpr int FIXED = R * QPITCH * 2 + R * OPITCH * 4 + 1024;
+  // As many stages as fit beside 2 KB of static and 1 KB of reserved shared
+  // memory: 64 KB or more of the cache in flight per SM.
+  static constexpr int FIT = (233472 / CTAS - 3072 - FIXED) / STAGE;
+  static constexpr int STAGES = FIT > 8 ? 8 : FIT;
+  static constexpr int Q_OFF = STAGES * STAGE;
+  static constexpr int O_OFF = Q_OFF + R * QPITCH * 2;
+  static constexpr int SMEM = STAGES * STAGE + FIXED;
+  static_assert(CTAS * STAGES * STAGE >= 64 * 1024, "bytes in flight");
+  static constexpr bool QREGS = NT * DQK <= 256;  // Q operand kept in registers
+};
+
+// Share of the work: the (sequence, head, row tile, key tile) index space.
+struct CaSeq {
+  Seq q;
+  int rt, kt, t0;  // row tiles, key tiles, first key tile
+  __device__ __forceinline__ int64_t tiles(int Hkv) const { return (int64_t)Hkv * rt * kt; }
+};
+__device__ __forceinline__ CaSeq ca_seq(const CacheAttnParams& p, int R, int b) {
+  CaSeq s;
+  s.q = seq_at(p.s, p.c.page, b);
+  const int lo = p.window > 0 ? max(0, s.q.n - s.q.m - p.window + 1) : 0;
+  s.t0 = lo / kCaKeys;
+  s.kt = s.q.m > 0 ? max(0, (s.q.n + kCaKeys - 1) / kCaKeys - s.t0) : 0;
+  s.rt = (s.q.m * p.G + R - 1) / R;
+  return s;
+}
+// CTAs that share `total` tiles, and the first tile of CTA c (c = parts: total).
+__device__ __forceinline__ int ca_parts(int64_t total, int grid, int min_tiles) {
+  const int64_t most = (total + min_tiles - 1) / min_tiles;
+  return (int)(most < grid ? most : grid);
+}
+__device__ __forceinline__ int64_t ca_first(int64_t total, int parts, int c) { return total * c / parts; }
+// The CTA that tile x belongs to.
+__device__ __forceinline__ int ca_owner(int64_t total, int parts, int64_t x) {
+  return (int)(((x + 1) * parts - 1) / total);
+}
+
+// Keys [lo, hi) that row i of m sees of n cached tokens (the last row sits at the last token).
+__device__ __forceinline__ void ca_row_keys(const CacheAttnParams& p, int n, int m, int i, int& lo, int& hi) {
+  const int at = i + n - m;
+  hi = p.causal ? min(n, at + 1) : n;
+  lo = p.window > 0 ? max(0, at - p.window + 1) : 0;
+  if (hi < lo) hi = lo;
+}
+
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ float minus_inf_as_0(float x) { return x == -CUDART_INF_F ? 0.f : x; }
+
+// Walks a CTA's share unit by unit; every role walks it by itself.
+struct CaUnit {
+  int b, h, rt, n, m, q0;
+  int t0, t1;    // key tiles of this share
+  int whole;     // the share holds all key tiles of the unit
+  int slot;      // partial result: 1 = the unit begins in this share, 0 = it continues
+};
+struct CaWalk {
+  int64_t pos, end, base;
+  int b;
+  CaSeq s;
+  template <typename Cfg>
+  __device__ __forceinline__ bool next(const CacheAttnParams& p, CaUnit& u) {
+    if (pos >= end) return false;
+    int64_t n = s.tiles(p.c.Hkv);
+    while (pos >= base + n) {
+      base += n;
+      s = ca_seq(p, Cfg::R, ++b);
+      n = s.tiles(p.c.Hkv);
+    }
+    const int64_t rel = pos - base, x = rel / s.kt;
+    const int kt = (int)(rel - x * s.kt);
+    const int cnt = (int)min((int64_t)(s.kt - kt), end - pos);
+    u.b = b;
+    u.h = (int)(x / s.rt);
+    u.rt = (int)(x - (int64_t)u.h * s.rt);
+    u.n = s.q.n;
+    u.m = s.q.m;
+    u.q0 = s.q.q0;
+    u.t0 = s.t0 + kt;
+    u.t1 = u.t0 + cnt;
+    u.whole = cnt == s.kt;
+    u.slot = kt == 0;
+    pos += cnt;
+    return true;
+  }
+};
+// Keys [lo, hi) that some row of the unit's row tile sees, and the key tiles of the share that hold them.
+__device__ __forceinline__ void ca_unit_keys(const CacheAttnParams& p, int R, const CaUnit& u, int& lo, int& hi, int& ta,
+                                             int& tb) {
+  const int i0 = u.rt * R / p.G, i1 = (min((u.rt + 1) * R, u.m * p.G) - 1) / p.G;
+  int x;
+  ca_row_keys(p, u.n, u.m, i0, lo, x);
+  ca_row_keys(p, u.n, u.m, i1, x, hi);
+  ta = max(u.t0, lo / kCaKeys);
+  tb = min(u.t1, (hi + kCaKeys - 1) / kCaKeys);
+}
+
+template <int DQK, int DV, int NT>
+__global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV, NT>::CTAS)
+    cache_attn_kernel(const __grid_constant__ CacheAttnParams p) {
+  using C = CaCfg<DQK, DV, NT>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ uint64_t full[C::STAGES], empty[C::STAGES];
+  __shared__ float2 meta[C::STAGES][kCaWarps];  // K scale and log2 of the V scale of each warp's keys
+  __shared__ float row_fac[C::R];
+  __shared__ int2 row_lim[C::R];
+  __shared__ float st_mu[kCaWarps][C::R], st_l[kCaWarps][C::R], fin_l[C::R];
+  __shared__ int64_t scan[8], found_base;
+  __shared__ int found_b, abort_flag;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int i = 0; i < C::STAGES; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], kCaWarps);
+    }
+    abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&p.tm_k);
+    tma_prefetch_desc(&p.tm_v);
+  }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  // The whole work, then the sequence that this share begins in.
+  int64_t mine = 0, first_count = 0;
+  for (int b = tid; b < p.s.B; b += kCaThreads) {
+    const CaSeq s = ca_seq(p, C::R, b);
+    if (s.q.bad && blockIdx.x == 0) record_status(p.status, kStatusDeviceArgs);
+    const int64_t n = s.tiles(p.c.Hkv);
+    if (b == tid) first_count = n;
+    mine += n;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+  if (lane == 0) scan[warp] = mine;
+  __syncthreads();
+  int64_t total = 0;
+#pragma unroll
+  for (int w = 0; w < kCaThreads / 32; ++w) total += scan[w];
+  const int parts = ca_parts(total, gridDim.x, p.min_tiles);
+  if ((int)blockIdx.x >= parts) return;
+  CaWalk walk;
+  walk.pos = ca_first(total, parts, blockIdx.x);
+  walk.end = ca_first(total, parts, blockIdx.x + 1);
+  int64_t carry = 0;
+  for (int base = 0; base < p.s.B; base += kCaThreads) {
+    const int b = base + tid;
+    const int64_t n = base == 0 ? first_count : (b < p.s.B ? ca_seq(p, C::R, b).tiles(p.c.Hkv) : 0);
+    int64_t x = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) scan[warp] = x;
+    __syncthreads();
+    int64_t before = carry;
+    for (int w = 0; w < kCaThreads / 32; ++w) {
+      if (w < warp) before += scan[w];
+      carry += scan[w];
+    }
+    if (b < p.s.B && n > 0 && walk.pos >= before + x - n && walk.pos < before + x) {
+      found_b = b;
+      found_base = before + x - n;
+    }
+    if (carry > walk.pos) break;  // the same for every thread
+  }
+  __syncthreads();
+  walk.b = found_b;
+  walk.base = found_base;
+  walk.s = ca_seq(p, C::R, found_b);
+  const Ctl ctl{p.status, p.limit_ns, &abort_flag};
+  CaUnit u;
+
+  if (warp == kCaWarps) {
+    // ------------------------------------------------------------ producer
+    const int box = min(p.c.page, kCaKeys), per_box = box / 16, boxes = kCaKeys / box;
+    uint32_t it = 0;
+    bool ok = true;
+    while (ok && walk.next<C>(p, u)) {
+      int lo, hi, ta, tb;
+      ca_unit_keys(p, C::R, u, lo, hi, ta, tb);
+      const int32_t* table = p.s.table + (int64_t)u.b * p.s.max_pages;
+      // Lane l looks after 16-key slice l of the next eight tiles.
+      auto page_at = [&](int tile0) {
+        const int key = tile0 * kCaKeys + lane * 16, first = key & -box;
+        if (first >= hi || first + box <= lo || tile0 * 4 + lane >= tb * 4) return -1;
+        int pg = table[key >> p.c.page_lg];
+        if (pg < 0 || pg >= p.c.pages) {
+          record_status(p.status, kStatusDeviceArgs);
+          pg = 0;
+        }
+        return pg;
+      };
+      auto scales_at = [&](int pg) {
+        const int64_t a = (int64_t)pg * p.c.Hkv + u.h;
+        return pg < 0 ? make_float2(0.f, 1.f) : make_float2(p.c.k_scale[a], p.c.v_scale[a]);
+      };
+      int pg = page_at(ta);
+      float2 sc = scales_at(pg);
+      int pg_next = page_at(ta + 8);
+      for (int t8 = ta; ok && t8 < tb; t8 += 8) {
+        const float2 sc_next = scales_at(pg_next);
+        const int pg_after = page_at(t8 + 16);
+        const float lvs = log2f(sc.y);
+        for (int i = 0; i < 8 && t8 + i < tb; ++i, ++it) {
+          const int st = it % C::STAGES;
+          if (it >= C::STAGES && !wait_bar(&empty[st], ((it / C::STAGES) - 1) & 1, ctl)) {
+            ok = false;
+            break;
+          }
+          if ((lane >> 2) == i) meta[st][lane & 3] = make_float2(sc.x, lvs);
+          __syncwarp();
+          const int key0 = (t8 + i) * kCaKeys;
+          uint8_t* dst = smem + st * C::STAGE;
+          const int b0 = max(lo - key0, 0) / box, b1 = min((hi - key0 + box - 1) / box, boxes);
+          if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)(b1 - b0) * box * C::ROWB * (C::KP + C::VP));
+          for (int x = b0; x < b1; ++x) {
+            const int use = __shfl_sync(0xffffffffu, pg, i * 4 + x * per_box);
+            if (lane == 0) {
+              const int row = (key0 + x * box) & (p.c.page - 1);
+#pragma unroll
+              for (int k = 0; k < C::KP; ++k)
+                tma_load_4d(dst + k * C::PLANE + x * box * C::ROWB, &p.tm_k, &full[st], k * 128, row, u.h, use);
+#pragma unroll
+              for (int k = 0; k < C::VP; ++k)
+                tma_load_4d(dst + (C::KP + k) * C::PLANE + x * box * C::ROWB, &p.tm_v, &full[st], k * 128, row, u.h,
+                            use);
+            }
+          }
+        }
+        pg = pg_next;
+        sc = sc_next;
+        pg_next = pg_after;
+      }
+    }
+    // After an abort the copies in flight are waited for (with a limit) before the CTA ends.
+    if (abort_flag)
+      for (uint32_t k = it > C::STAGES ? it - C::STAGES : 0; k < it; ++k)
+        wait_bar_drain(&full[k % C::STAGES], (k / C::STAGES) & 1, p.limit_ns);
+    return;
+  }
+
+  // ------------------------------------------------------------ consumers
+  const int g = lane >> 2, t = lane & 3;
+  // Position in a product -> key row of the warp's 16 (bits 0-2; bit 3 stays).
+  auto row_at = [](int x) {
+    return DQK == 64 ? ((x & 1) * 3) ^ ((x >> 1) & 1) ^ (x & 4) : ((x & 1) * 5) ^ (x & 2) ^ (x & 4);
+  };
+  const int ka = warp * 16 + row_at(g);  // key rows of this lane's scores: ka, ka + 8
+  const int va = warp * 16 + row_at(2 * t), vb = warp * 16 + row_at(2 * t + 1);  // V rows: va, vb, + 8 each
+  const uint32_t ring = smem_u32(smem);
+  const uint32_t qs = smem_u32(smem + C::Q_OFF);
+  float* ob = reinterpret_cast<float*>(smem + C::O_OFF);
+  auto k_off = [&](int row, int j) -> uint32_t {
+    if (DQK == 64) return row * 64 + ((t ^ ((row >> 1) & 3)) << 4);
+    return (j >> 1) * C::PLANE + row * 128 + ((((j & 1) * 4 + t) ^ (row & 7)) << 4);
+  };
+  auto v_off = [&](int row, int j) -> uint32_t {
+    if (DV == 64) return C::PLANE + row * 64 + (((g >> 1) ^ ((row >> 1) & 3)) << 4) + (g & 1) * 8;
+    return (C::KP + j) * C::PLANE + row * 128 + ((g ^ (row & 7)) << 4);
+  };
+  constexpr int MT = DV / 16;            // products along the head dim of V
+  constexpr int VW = DV == 64 ? 2 : 4;   // 4-code words a lane reads of a key row and plane
+  uint32_t it = 0;
+  bool ok = true;
+
+  while (walk.next<C>(p, u)) {
+    int lo, hi, ta, tb;
+    ca_unit_keys(p, C::R, u, lo, hi, ta, tb);
+    const int rows = u.m * p.G, n0 = u.rt * C::R;
+    consumers_sync();  // the last unit's shared rows are read
+    for (int r = warp; r < C::R; r += kCaWarps) {
+      const int x = n0 + r, i = x / p.G, hq = u.h * p.G + (x - i * p.G);
+      constexpr int E = DQK / 32;  // elements per lane
+      float v[E];
+      float top = 0.f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] = 0.f;
+      if (x < rows) {
+        const int64_t at = p.q_ss * (u.q0 + i) + p.q_sh * hq + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+          const uint32_t w = *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p.q) + at + e);
+          const float2 f = p.f16 ? unpack2<__half>(w) : unpack2<__nv_bfloat16>(w);
+          v[e] = f.x;
+          v[e + 1] = f.y;
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < E; ++e) top = fmaxf(top, fabsf(v[e]));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const int field = min(268 - (__float_as_int(top) >> 23), 253);  // 2^14 <= top * 2^(field - 127) < 2^15
+      const float up = __int_as_float(field << 23), down = __int_as_float((254 - field) << 23);
+#pragma unroll
+      for (int e = 0; e < E; e += 2)
+        *reinterpret_cast<uint32_t*>(smem + C::Q_OFF + (r * C::QPITCH + lane * E + e) * 2) =
+            pack2<__half>(v[e] * up, v[e + 1] * up);
+      if (lane == 0) {
+        int2 lim = make_int2(0, 0);
+        if (x < rows) ca_row_keys(p, u.n, u.m, i, lim.x, lim.y);
+        row_lim[r] = lim;
+        row_fac[r] = down * (p.softcap > 0.f ? p.scale / p.softcap : p.scale * 1.4426950408889634f);
+      }
+    }
+    consumers_sync();
+    // Every row that exists sees keys [in_lo, in_hi): tiles inside need no mask.
+    int in_lo, in_hi;
+    {
+      const int i0 = n0 / p.G, i1 = (min(n0 + C::R, rows) - 1) / p.G;
+      int x;
+      ca_row_keys(p, u.n, u.m, i1, in_lo, x);
+      ca_row_keys(p, u.n, u.m, i0, x, in_hi);
+    }
+    uint32_t qf[C::QREGS ? NT : 1][C::QREGS ? DQK / 8 : 1];
+    if constexpr (C::QREGS) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < DQK / 64; ++j)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const uint4 a = lds128(qs + ((nt * 8 + g) * C::QPITCH + j * 64 + t * 16 + x * 8) * 2);
+            qf[nt][j * 8 + x * 4] = a.x;
+            qf[nt][j * 8 + x * 4 + 1] = a.y;
+            qf[nt][j * 8 + x * 4 + 2] = a.z;
+            qf[nt][j * 8 + x * 4 + 3] = a.w;
+          }
+    }
+    float fac[NT][2], mu[NT][2], ro[NT][2], l[NT][2];
+    float o[MT][NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        fac[nt][c] = row_fac[nt * 8 + 2 * t + c];
+        mu[nt][c] = ro[nt][c] = -CUDART_INF_F;
+        l[nt][c] = 0.f;
+      }
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[m][nt][c] = 0.f;
+
+    auto tile_step = [&](auto mask_tag, int tile) {
+      constexpr bool MASK = decltype(mask_tag)::value;
+      const int st = it % C::STAGES;
+      const uint32_t sb = ring + st * C::STAGE;
+      const int key = tile * kCaKeys + ka;
+      float s[NT][4], s2[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) s[nt][c] = s2[nt][c] = 0.f;
+#pragma unroll
+      for (int j = 0; j < DQK / 64; ++j) {
+        const uint4 xa = lds128(sb + k_off(ka, j)), xb = lds128(sb + k_off(ka + 8, j));
+        const uint32_t wa[4] = {xa.x, xa.y, xa.z, xa.w}, wb[4] = {xb.x, xb.y, xb.z, xb.w};
+        uint32_t qv[NT][8];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          if constexpr (C::QREGS) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) qv[nt][e] = qf[nt][j * 8 + e];
+          } else {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const uint4 a = lds128(qs + ((nt * 8 + g) * C::QPITCH + j * 64 + t * 16 + x * 8) * 2);
+              qv[nt][x * 4] = a.x;
+              qv[nt][x * 4 + 1] = a.y;
+              qv[nt][x * 4 + 2] = a.z;
+              qv[nt][x * 4 + 3] = a.w;
+            }
+          }
+        }
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const uint32_t a0 = e4m3_to_half2(wa[w] & 0xffff), a2 = e4m3_to_half2(wa[w] >> 16);
+          const uint32_t a1 = e4m3_to_half2(wb[w] & 0xffff), a3 = e4m3_to_half2(wb[w] >> 16);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            mma16816((w & 1) ? s2[nt] : s[nt], a0, a1, a2, a3, qv[nt][2 * w], qv[nt][2 * w + 1]);
+        }
+      }
+      // Scores in log2 units.
+      const float2 sc = meta[st][warp];
+      bool move = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const float f0 = fac[nt][0] * sc.x, f1 = fac[nt][1] * sc.x;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float x = (s[nt][c] + s2[nt][c]) * ((c & 1) ? f1 : f0);
+          if (p.softcap > 0.f) {
+            // c tanh(y) log2(e), tanh(y) = 1 - 2 / (e^(2y) + 1): off by some 2^-22 of the cap
+            const float e = ex2_approx(x * 2.8853900817779268f);
+            x = p.softcap * 1.4426950408889634f * fmaf(-2.f, rcp_approx(e + 1.f), 1.f);
+          }
+          s[nt][c] = x;
+        }
+        if (p.accumulate) {
+          const int64_t unit = (int64_t)u.b * p.c.Hkv + u.h;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int col = n0 + nt * 8 + 2 * t + (c & 1), k = key + (c >> 1) * 8;
+            if (col < rows && k < hi) p.scores[(unit * p.score_rows + col) * p.score_cap + k] = s[nt][c];
+          }
+        }
+        if constexpr (MASK) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int2 lim = row_lim[nt * 8 + 2 * t + (c & 1)];
+            const int k = key + (c >> 1) * 8;
+            if (k < lim.x || k >= lim.y) s[nt][c] = -CUDART_INF_F;
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          move |= s[nt][c] > mu[nt][c & 1] + kCaLazy || s[nt][c] + sc.y > ro[nt][c & 1] + (kCaHead + kCaLazy);
+      }
+      if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float of[2];
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float top = fmaxf(s[nt][c], s[nt][c + 2]);
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+            const float m1 = fmaxf(mu[nt][c], top), r1 = fmaxf(ro[nt][c], top + sc.y - kCaHead);
+            l[nt][c] *= ex2_approx(mu[nt][c] - minus_inf_as_0(m1));
+            of[c] = ex2_approx(ro[nt][c] - minus_inf_as_0(r1));
+            mu[nt][c] = m1;
+            ro[nt][c] = r1;
+          }
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) o[m][nt][c] *= of[c & 1];
+        }
+      }
+      uint32_t pb[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float w[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          l[nt][c & 1] += ex2_approx(s[nt][c] - minus_inf_as_0(mu[nt][c & 1]));
+          w[c] = ex2_approx(s[nt][c] + (sc.y - minus_inf_as_0(ro[nt][c & 1])));
+        }
+        pb[nt][0] = transpose8x8(pack2<__half>(w[0], w[1]));
+        pb[nt][1] = transpose8x8(pack2<__half>(w[2], w[3]));
+      }
+      uint32_t nan_seen = 0;
+#pragma unroll
+      for (int j = 0; j < C::VP; ++j) {
+        uint32_t x[4][4];
+        const int rows4[4] = {va, vb, va + 8, vb + 8};
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          if constexpr (DV == 64) {
+            const uint2 a = lds64(sb + v_off(rows4[r], j));
+            x[r][0] = a.x;
+            x[r][1] = a.y;
+          } else {
+            const uint4 a = lds128(sb + v_off(rows4[r], j));
+            x[r][0] = a.x;
+            x[r][1] = a.y;
+            x[r][2] = a.z;
+            x[r][3] = a.w;
+          }
+          if constexpr (MASK) {
+            // Rows that no query row sees count as 0 (stale codes may be NaN);
+            // a NaN that some row sees is put in below, for that row alone.
+            const int k = tile * kCaKeys + rows4[r];
+            const bool in = k >= lo && k < hi;
+#pragma unroll
+            for (int w = 0; w < VW; ++w) {
+              const uint32_t z = in ? x[r][w] : 0u;
+              const uint32_t nan = ((z & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+              nan_seen |= nan;
+              x[r][w] = z & ~((nan >> 7) * 0xffu);
+            }
+          }
+        }
+#pragma unroll
+        for (int w = 0; w < VW; ++w) {
+          const uint32_t y0 = __byte_perm(x[0][w], x[1][w], 0x5140), y1 = __byte_perm(x[0][w], x[1][w], 0x7362);
+          const uint32_t z0 = __byte_perm(x[2][w], x[3][w], 0x5140), z1 = __byte_perm(x[2][w], x[3][w], 0x7362);
+          const int m = j * 8 + w * 2;
+          const uint32_t a0 = e4m3_to_half2(y0 & 0xffff), a1 = e4m3_to_half2(y0 >> 16);
+          const uint32_t a2 = e4m3_to_half2(z0 & 0xffff), a3 = e4m3_to_half2(z0 >> 16);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma16816(o[m][nt], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+          const uint32_t b0 = e4m3_to_half2(y1 & 0xffff), b1 = e4m3_to_half2(y1 >> 16);
+          const uint32_t b2 = e4m3_to_half2(z1 & 0xffff), b3 = e4m3_to_half2(z1 >> 16);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma16816(o[m + 1][nt], b0, b1, b2, b3, pb[nt][0], pb[nt][1]);
+        }
+      }
+      if constexpr (MASK) {
+        if (__any_sync(0xffffffffu, nan_seen != 0)) {
+          for (int r = 0; r < 16; ++r) {
+            const int row = warp * 16 + r, k = tile * kCaKeys + row;
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const uint32_t code = lds8(sb + v_off(row, m >> 3) + (m & 7) * 2 + e);
+                if ((code & 0x7f) == 0x7f)
+#pragma unroll
+                  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                      const int2 lim = row_lim[nt * 8 + 2 * t + c];
+                      if (k >= lim.x && k < lim.y) o[m][nt][2 * e + c] = CUDART_NAN_F;
+                    }
+              }
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[st]);
+    };
+
+    for (int tile = ta; tile < tb; ++tile, ++it) {
+      if (ok && !wait_bar(&full[it % C::STAGES], (it / C::STAGES) & 1, ctl)) ok = false;
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) continue;
+      if (tile * kCaKeys >= in_lo && (tile + 1) * kCaKeys <= in_hi)
+        tile_step(MaskTag<false>(), tile);
+      else
+        tile_step(MaskTag<true>(), tile);
+    }
+
+    // ---------------------------------------------------------- end of the unit: the four warps' states into one
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], x);
+        if (g == 0) {
+          const int r = nt * 8 + 2 * t + c;
+          st_mu[warp][r] = mu[nt][c];
+          st_l[warp][r] = l[nt][c];
+        }
+      }
+    consumers_sync();
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float f[2];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int r = nt * 8 + 2 * t + c;
+        float top = -CUDART_INF_F, sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < kCaWarps; ++w) top = fmaxf(top, st_mu[w][r]);
+#pragma unroll
+        for (int w = 0; w < kCaWarps; ++w) sum += st_l[w][r] * ex2_approx(st_mu[w][r] - minus_inf_as_0(top));
+        // sum > 0 unless the row saw nothing; NaN stays NaN
+        f[c] = sum == 0.f ? 0.f : ex2_approx(ro[nt][c] - minus_inf_as_0(top)) / sum;
+        if (warp == 0 && g == 0) fin_l[r] = sum == 0.f ? -CUDART_INF_F : top + log2f(sum);
+      }
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[m][nt][c] *= f[c & 1];
+    }
+    for (int w = 0; w < kCaWarps; ++w) {
+      if (warp == w) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          const int d = DV == 64 ? g * 8 + m * 2 : (m >> 3) * 128 + g * 16 + (m & 7) * 2;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              float2* at = reinterpret_cast<float2*>(ob + (nt * 8 + 2 * t + c) * C::OPITCH + d);
+              float2 x = make_float2(o[m][nt][c], o[m][nt][2 + c]);
+              if (w) {
+                const float2 y = *at;
+                x.x += y.x;
+                x.y += y.y;
+              }
+              *at = x;
+            }
+        }
+      }
+      consumers_sync();
+    }
+    const int live = min(C::R, rows - n0);
+    if (u.whole) {
+      for (int x = tid; x < live * (DV / 8); x += 128) {
+        const int r = x / (DV / 8), d = (x - r * (DV / 8)) * 8, y = n0 + r, i = y / p.G;
+        const float* at = ob + r * C::OPITCH + d;
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          w[e] = p.f16 ? pack2<__half>(at[2 * e], at[2 * e + 1]) : pack2<__nv_bfloat16>(at[2 * e], at[2 * e + 1]);
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + p.o_ss * (u.q0 + i) +
+                                  p.o_sh * (u.h * p.G + y - i * p.G) + d) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      if (tid < live) {
+        const int y = n0 + tid, i = y / p.G;
+        p.lse[(int64_t)(u.h * p.G + y - i * p.G) * p.s.T + u.q0 + i] = fin_l[tid] * 0.69314718055994531f;
+      }
+    } else {
+      const int64_t slot = (int64_t)blockIdx.x * 2 + u.slot;
+      float* po = p.part_o + slot * C::R * DV;
+      for (int x = tid; x < live * (DV / 4); x += 128) {
+        const int r = x / (DV / 4), d = (x - r * (DV / 4)) * 4;
+        *reinterpret_cast<float4*>(po + r * DV + d) = *reinterpret_cast<const float4*>(ob + r * C::OPITCH + d);
+      }
+      if (tid < live) p.part_l[slot * C::R + tid] = fin_l[tid];
+    }
+  }
+}
+
+// Joins the partial results of units that several CTAs share, in the order of
+// the CTAs, and writes the rows that no CTA wrote: sequences without keys, and
+// (blockIdx.y = B) rows past the last sequence. One CTA per (head, row tile) and sequence.
+constexpr int kJoinThreads = 128;
+template <int DQK, int DV, int NT>
+__global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_constant__ CacheAttnParams p, int grid) {
+  using C = CaCfg<DQK, DV, NT>;
+  __shared__ int64_t sum_before[kJoinThreads / 32], sum_all[kJoinThreads / 32];
+  __shared__ float row_l[C::R];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int b = blockIdx.y;
+  auto write8 = [&](int64_t row, int hq, int d, const float* x) {
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      w[e] = p.f16 ? pack2<__half>(x[2 * e], x[2 * e + 1]) : pack2<__nv_bfloat16>(x[2 * e], x[2 * e + 1]);
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + p.o_ss * row + p.o_sh * hq + d) =
+        make_uint4(w[0], w[1], w[2], w[3]);
+  };
+  const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (b == p.s.B) {
+    const int first = min(max(p.s.cu[p.s.B], 0), p.s.T);
+    for (int64_t x = (int64_t)blockIdx.x * kJoinThreads + tid; x < (int64_t)(p.s.T - first) * p.Hq;
+         x += (int64_t)gridDim.x * kJoinThreads) {
+      const int64_t row = first + x / p.Hq;
+      const int hq = (int)(x % p.Hq);
+      for (int d = 0; d < DV; d += 8) write8(row, hq, d, zero);
+      p.lse[(int64_t)hq * p.s.T + row] = -CUDART_INF_F;
+    }
+    return;
+  }
+  const CaSeq s = ca_seq(p, C::R, b);
+  const int h = blockIdx.x / p.row_tiles, rt = blockIdx.x % p.row_tiles;
+  if (rt >= s.rt) return;
+  const int rows = s.q.m * p.G, n0 = rt * C::R, live = min(C::R, rows - n0);
+  if (s.kt == 0) {
+    for (int x = tid; x < live * (DV / 8); x += kJoinThreads) {
+      const int r = x / (DV / 8), y = n0 + r, i = y / p.G;
+      write8(s.q.q0 + i, h * p.G + y - i * p.G, (x - r * (DV / 8)) * 8, zero);
+    }
+    if (tid < live) {
+      const int y = n0 + tid, i = y / p.G;
+      p.lse[(int64_t)(h * p.G + y - i * p.G) * p.s.T + s.q.q0 + i] = -CUDART_INF_F;
+    }
+    return;
+  }
+  int64_t before = 0, total = 0;
+  for (int x = tid; x < p.s.B; x += kJoinThreads) {
+    const int64_t n = ca_seq(p, C::R, x).tiles(p.c.Hkv);
+    total += n;
+    before += x < b ? n : 0;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    total += __shfl_xor_sync(0xffffffffu, total, o);
+    before += __shfl_xor_sync(0xffffffffu, before, o);
+  }
+  if (lane == 0) {
+    sum_all[warp] = total;
+    sum_before[warp] = before;
+  }
+  __syncthreads();
+  total = before = 0;
+#pragma unroll
+  for (int w = 0; w < kJoinThreads / 32; ++w) {
+    total += sum_all[w];
+    before += sum_before[w];
+  }
+  const int parts = ca_parts(total, grid, p.min_tiles);
+  const int64_t x0 = before + ((int64_t)h * s.rt + rt) * s.kt;
+  const int c0 = ca_owner(total, parts, x0), c1 = ca_owner(total, parts, x0 + s.kt - 1);
+  if (c0 == c1) return;  // one CTA had it all and wrote it
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int np = c1 - c0 + 1;
+  auto slot = [&](int i) -> int64_t { return (int64_t)(c0 + i) * 2 + (i == 0); };
+  for (int r = warp; r < live; r += kJoinThreads / 32) {
+    float top = -CUDART_INF_F, sum = 0.f;
+    for (int i = lane; i < np; i += 32) top = fmaxf(top, p.part_l[slot(i) * C::R + r]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    top = minus_inf_as_0(top);
+    for (int i = lane; i < np; i += 32) sum += ex2_approx(p.part_l[slot(i) * C::R + r] - top);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) {
+      const float l = sum == 0.f ? -CUDART_INF_F : top + log2f(sum);
+      const int y = n0 + r, i = y / p.G;
+      row_l[r] = l;
+      p.lse[(int64_t)(h * p.G + y - i * p.G) * p.s.T + s.q.q0 + i] = l * 0.69314718055994531f;
+    }
+  }
+  __syncthreads();
+  for (int x = tid; x < live * (DV / 8); x += kJoinThreads) {
+    const int r = x / (DV / 8), d = (x - r * (DV / 8)) * 8, y = n0 + r, i = y / p.G;
+    const float l = minus_inf_as_0(row_l[r]);
+    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int k = 0; k < np; ++k) {
+      const float w = ex2_approx(p.part_l[slot(k) * C::R + r] - l);
+      const float4* at = reinterpret_cast<const float4*>(p.part_o + (slot(k) * C::R + r) * DV + d);
+      const float4 a = at[0], e = at[1];
+      acc[0] = fmaf(a.x, w, acc[0]);
+      acc[1] = fmaf(a.y, w, acc[1]);
+      acc[2] = fmaf(a.z, w, acc[2]);
+      acc[3] = fmaf(a.w, w, acc[3]);
+      acc[4] = fmaf(e.x, w, acc[4]);
+      acc[5] = fmaf(e.y, w, acc[5]);
+      acc[6] = fmaf(e.z, w, acc[6]);
+      acc[7] = fmaf(e.w, w, acc[7]);
+    }
+    write8(s.q.q0 + i, h * p.G + y - i * p.G, d, acc);
+  }
+}
+
+}  // namespace psf

@@ -1,6 +1,7 @@
 // launch_cache.h -- host-side launchers of the 8-bit cache's kernels.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -32,6 +33,7 @@ cudaError_t launch_cache_evict(const CacheView& c, const SeqView& s, int budget,
                                const EvictWorkspace& ws, int sms, int* status, cudaStream_t st);
 
 struct CacheAttnParams {
+  CUtensorMap tm_k, tm_v;  // (d, row, head, page) of the codes
   CacheView c;
   SeqView s;
   const void* q;
@@ -44,9 +46,18 @@ struct CacheAttnParams {
   int causal, window;  // window > 0: left window counting the current token
   int accumulate;      // add each key's probabilities to c.weight
   int f16;
+  int min_tiles;  // a CTA's share is at least this many key tiles
+  int row_tiles;  // of a sequence with the most rows
+  // Workspace: partial results [CTA][2][R][Dv] and their lse in log2 units
+  // [CTA][2][R]; scores [B * Hkv][score_rows][score_cap] in log2 units.
+  float *part_o, *part_l, *scores;
+  int64_t score_rows, score_cap;
   int* status;
   uint64_t limit_ns;
 };
-cudaError_t launch_cache_attn(const CacheAttnParams& p, int sms, cudaStream_t st);
+// Row tile (in units of 8 rows) and CTAs per SM that the launch uses.
+int cache_attn_nt(int Dqk, int64_t rows);
+constexpr int cache_attn_ctas(int Dqk, int nt) { return Dqk == 512 ? 1 : (nt == 1 && Dqk <= 128 ? 3 : 2); }
+cudaError_t launch_cache_attn(CacheAttnParams& p, int max_q, int sms, cudaStream_t st);
 
 }  // namespace psf
