@@ -1049,7 +1049,7 @@ int psf_attn_cache_fwd(const void* q, const psf_kv_cache* cache, void* out, floa
   p.f16 = dtype == PSF_DTYPE_F16;
   p.status = dev->status;
   p.limit_ns = g_wait_limit_ns;
-  p.min_tiles = 2;
+  p.min_share = 2;
   cache_attn_ws_layout(B, max_pages, p.c.page, Hq, p.c.Hkv, p.c.Dqk, p.c.Dv, max_q, p.accumulate, &p, workspace);
   if ((rc = cache_map(&p.tm_k, p.c.k, p.c, p.c.Dqk, p.c.k_sp, p.c.k_sh, p.c.k_sr)) ||
       (rc = cache_map(&p.tm_v, p.c.v, p.c, p.c.Dv, p.c.v_sp, p.c.v_sh, p.c.v_sr)))

@@ -19,9 +19,9 @@
 // result; otherwise it leaves a partial result (o / l, lse) that the join kernel
 // adds up in the order of the CTAs. Nothing depends on the order of execution.
 //
-//   warp 4     producer: page numbers and scales one batch ahead, K and V pages
-//              by TMA into a ring of stages (128-byte rows, 128-byte swizzle;
-//              64-byte rows for head dim 64)
+//   warp 4     producer: the next unit's queries (two buffers), page numbers and
+//              scales one batch ahead, K and V pages by TMA into a ring of stages
+//              (128-byte rows, 128-byte swizzle; 64-byte rows for head dim 64)
 //   warps 0-3  16 keys of each tile each, with a softmax state of their own
 //              (nothing but the ring's barriers between them); joined at the
 //              end of the unit
@@ -66,23 +66,31 @@ struct CaCfg {
   static constexpr int CTAS = cache_attn_ctas(DQK, NT);
   static constexpr int QPITCH = DQK + 8;  // fp16 elements
   static constexpr int OPITCH = DV + 4;   // fp32 elements
-  static constexpr int FIXED = R * QPITCH * 2 + R * OPITCH * 4 + 1024;
+  static constexpr int QBYTES = R * QPITCH * 2;  // one of two buffers
+  static constexpr int FIXED = 2 * QBYTES + R * OPITCH * 4 + 1024;
   // As many stages as fit beside 2 KB of static and 1 KB of reserved shared
   // memory: 64 KB or more of the cache in flight per SM.
   static constexpr int FIT = (233472 / CTAS - 3072 - FIXED) / STAGE;
   static constexpr int STAGES = FIT > 8 ? 8 : FIT;
   static constexpr int Q_OFF = STAGES * STAGE;
-  static constexpr int O_OFF = Q_OFF + R * QPITCH * 2;
+  static constexpr int O_OFF = Q_OFF + 2 * QBYTES;
   static constexpr int SMEM = STAGES * STAGE + FIXED;
   static_assert(CTAS * STAGES * STAGE >= 64 * 1024, "bytes in flight");
   static constexpr bool QREGS = NT * DQK <= 256;  // Q operand kept in registers
 };
 
-// Share of the work: the (sequence, head, row tile, key tile) index space.
+// Share of the work. A unit is a (sequence, head, row tile); it costs its key
+// tiles and kCaUnit more (queries in, four warps' states into one, result out),
+// laid out as kCaUnit places and then a place per tile. CTA c takes places
+// [ca_first(c), ca_first(c + 1)) of the units in order. Without the unit's cost a
+// share of many short sequences took five times as long as one of a long one
+// (16 sequences of 5 to 4099 tokens: 148 us).
+constexpr int kCaUnit = 2;
 struct CaSeq {
   Seq q;
   int rt, kt, t0;  // row tiles, key tiles, first key tile
-  __device__ __forceinline__ int64_t tiles(int Hkv) const { return (int64_t)Hkv * rt * kt; }
+  __device__ __forceinline__ int cost() const { return kt + kCaUnit; }
+  __device__ __forceinline__ int64_t places(int Hkv) const { return kt ? (int64_t)Hkv * rt * cost() : 0; }
 };
 __device__ __forceinline__ CaSeq ca_seq(const CacheAttnParams& p, int R, int b) {
   CaSeq s;
@@ -93,13 +101,13 @@ __device__ __forceinline__ CaSeq ca_seq(const CacheAttnParams& p, int R, int b) 
   s.rt = (s.q.m * p.G + R - 1) / R;
   return s;
 }
-// CTAs that share `total` tiles, and the first tile of CTA c (c = parts: total).
-__device__ __forceinline__ int ca_parts(int64_t total, int grid, int min_tiles) {
-  const int64_t most = (total + min_tiles - 1) / min_tiles;
+// CTAs that share `total` places, and the first place of CTA c (c = parts: total).
+__device__ __forceinline__ int ca_parts(int64_t total, int grid, int min_share) {
+  const int64_t most = (total + min_share - 1) / min_share;
   return (int)(most < grid ? most : grid);
 }
 __device__ __forceinline__ int64_t ca_first(int64_t total, int parts, int c) { return total * c / parts; }
-// The CTA that tile x belongs to.
+// The CTA that place x belongs to.
 __device__ __forceinline__ int ca_owner(int64_t total, int parts, int64_t x) {
   return (int)(((x + 1) * parts - 1) / total);
 }
@@ -140,55 +148,68 @@ __device__ __forceinline__ uint32_t lds8(uint32_t a) {
   return v;
 }
 __device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ bool consumers_all(bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %1, 0;\n\t"
+      "barrier.cta.red.and.pred q, 1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)x)
+      : "memory");
+  return r != 0;
+}
 __device__ __forceinline__ float minus_inf_as_0(float x) { return x == -CUDART_INF_F ? 0.f : x; }
 
-// Walks a CTA's share unit by unit; every role walks it by itself.
+// One unit of a share, and the keys and tiles it concerns.
 struct CaUnit {
   int b, h, rt, n, m, q0;
-  int t0, t1;    // key tiles of this share
-  int whole;     // the share holds all key tiles of the unit
-  int slot;      // partial result: 1 = the unit begins in this share, 0 = it continues
+  int t0, t1;        // key tiles of this share
+  int whole;         // the share holds all key tiles of the unit
+  int slot;          // partial result: 1 = the unit begins in this share, 0 = it continues
+  int lo, hi;        // keys that some row of the row tile sees
+  int in_lo, in_hi;  // keys that every row sees: tiles inside need no mask
+  int ta, tb;        // key tiles of the share with keys in [lo, hi)
 };
 struct CaWalk {
   int64_t pos, end, base;
   int b;
   CaSeq s;
-  template <typename Cfg>
-  __device__ __forceinline__ bool next(const CacheAttnParams& p, CaUnit& u) {
-    if (pos >= end) return false;
-    int64_t n = s.tiles(p.c.Hkv);
-    while (pos >= base + n) {
-      base += n;
-      s = ca_seq(p, Cfg::R, ++b);
-      n = s.tiles(p.c.Hkv);
+  __device__ __forceinline__ bool next(const CacheAttnParams& p, int R, CaUnit& u) {
+    while (pos < end) {
+      int64_t n = s.places(p.c.Hkv);
+      while (pos >= base + n) {
+        base += n;
+        s = ca_seq(p, R, ++b);
+        n = s.places(p.c.Hkv);
+      }
+      const int64_t rel = pos - base, x = rel / s.cost();
+      const int off = (int)(rel - x * s.cost());
+      const int stop = (int)min((int64_t)s.cost(), off + (end - pos));
+      pos += stop - off;
+      const int k0 = max(off - kCaUnit, 0), k1 = stop - kCaUnit;
+      if (k1 <= k0) continue;  // nothing but the places in front of the tiles
+      u.b = b;
+      u.h = (int)(x / s.rt);
+      u.rt = (int)(x - (int64_t)u.h * s.rt);
+      u.n = s.q.n;
+      u.m = s.q.m;
+      u.q0 = s.q.q0;
+      u.t0 = s.t0 + k0;
+      u.t1 = s.t0 + k1;
+      u.whole = k1 - k0 == s.kt;
+      u.slot = k0 == 0;
+      const int i0 = u.rt * R / p.G, i1 = (min((u.rt + 1) * R, u.m * p.G) - 1) / p.G;
+      ca_row_keys(p, u.n, u.m, i0, u.lo, u.in_hi);
+      ca_row_keys(p, u.n, u.m, i1, u.in_lo, u.hi);
+      u.ta = max(u.t0, u.lo / kCaKeys);
+      u.tb = min(u.t1, (u.hi + kCaKeys - 1) / kCaKeys);
+      return true;
     }
-    const int64_t rel = pos - base, x = rel / s.kt;
-    const int kt = (int)(rel - x * s.kt);
-    const int cnt = (int)min((int64_t)(s.kt - kt), end - pos);
-    u.b = b;
-    u.h = (int)(x / s.rt);
-    u.rt = (int)(x - (int64_t)u.h * s.rt);
-    u.n = s.q.n;
-    u.m = s.q.m;
-    u.q0 = s.q.q0;
-    u.t0 = s.t0 + kt;
-    u.t1 = u.t0 + cnt;
-    u.whole = cnt == s.kt;
-    u.slot = kt == 0;
-    pos += cnt;
-    return true;
+    return false;
   }
 };
-// Keys [lo, hi) that some row of the unit's row tile sees, and the key tiles of the share that hold them.
-__device__ __forceinline__ void ca_unit_keys(const CacheAttnParams& p, int R, const CaUnit& u, int& lo, int& hi, int& ta,
-                                             int& tb) {
-  const int i0 = u.rt * R / p.G, i1 = (min((u.rt + 1) * R, u.m * p.G) - 1) / p.G;
-  int x;
-  ca_row_keys(p, u.n, u.m, i0, lo, x);
-  ca_row_keys(p, u.n, u.m, i1, x, hi);
-  ta = max(u.t0, lo / kCaKeys);
-  tb = min(u.t1, (hi + kCaKeys - 1) / kCaKeys);
-}
 
 template <int DQK, int DV, int NT>
 __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV, NT>::CTAS)
@@ -198,8 +219,10 @@ __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV, NT>::CTAS)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ uint64_t full[C::STAGES], empty[C::STAGES];
   __shared__ float2 meta[C::STAGES][kCaWarps];  // K scale and log2 of the V scale of each warp's keys
-  __shared__ float row_fac[C::R];
-  __shared__ int2 row_lim[C::R];
+  __shared__ uint64_t q_full[2], q_empty[2];
+  __shared__ CaUnit unit_at[2];             // b < 0: no more units
+  __shared__ float row_fac_at[2][C::R];     // query scale times the logit scale
+  __shared__ int2 row_lim_at[2][C::R];      // keys that a row sees
   __shared__ float st_mu[kCaWarps][C::R], st_l[kCaWarps][C::R], fin_l[C::R];
   __shared__ int64_t scan[8], found_base;
   __shared__ int found_b, abort_flag;
@@ -209,6 +232,10 @@ __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV, NT>::CTAS)
     for (int i = 0; i < C::STAGES; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], kCaWarps);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_full[i], 1);
+      mbar_init(&q_empty[i], kCaWarps);
     }
     abort_flag = 0;
     fence_mbar_init();
@@ -222,7 +249,7 @@ __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV, NT>::CTAS)
   for (int b = tid; b < p.s.B; b += kCaThreads) {
     const CaSeq s = ca_seq(p, C::R, b);
     if (s.q.bad && blockIdx.x == 0) record_status(p.status, kStatusDeviceArgs);
-    const int64_t n = s.tiles(p.c.Hkv);
+    const int64_t n = s.places(p.c.Hkv);
     if (b == tid) first_count = n;
     mine += n;
   }
@@ -233,7 +260,7 @@ __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV, NT>::CTAS)
   int64_t total = 0;
 #pragma unroll
   for (int w = 0; w < kCaThreads / 32; ++w) total += scan[w];
-  const int parts = ca_parts(total, gridDim.x, p.min_tiles);
+  const int parts = ca_parts(total, gridDim.x, p.min_share);
   if ((int)blockIdx.x >= parts) return;
   CaWalk walk;
   walk.pos = ca_first(total, parts, blockIdx.x);
@@ -241,7 +268,7 @@ __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV, NT>::CTAS)
   int64_t carry = 0;
   for (int base = 0; base < p.s.B; base += kCaThreads) {
     const int b = base + tid;
-    const int64_t n = base == 0 ? first_count : (b < p.s.B ? ca_seq(p, C::R, b).tiles(p.c.Hkv) : 0);
+    const int64_t n = base == 0 ? first_count : (b < p.s.B ? ca_seq(p, C::R, b).places(p.c.Hkv) : 0);
     int64_t x = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -263,25 +290,63 @@ __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV, NT>::CTAS)
     if (carry > walk.pos) break;  // the same for every thread
   }
   __syncthreads();
-  walk.b = found_b;
-  walk.base = found_base;
-  walk.s = ca_seq(p, C::R, found_b);
   const Ctl ctl{p.status, p.limit_ns, &abort_flag};
-  CaUnit u;
 
   if (warp == kCaWarps) {
     // ------------------------------------------------------------ producer
+    walk.b = found_b;
+    walk.base = found_base;
+    walk.s = ca_seq(p, C::R, found_b);
     const int box = min(p.c.page, kCaKeys), per_box = box / 16, boxes = kCaKeys / box;
-    uint32_t it = 0;
+    constexpr int E = DQK / 32;  // query elements per lane and row
+    uint32_t it = 0, nu = 0;
     bool ok = true;
-    while (ok && walk.next<C>(p, u)) {
-      int lo, hi, ta, tb;
-      ca_unit_keys(p, C::R, u, lo, hi, ta, tb);
+    CaUnit u;
+    while (true) {
+      const bool more = walk.next(p, C::R, u);
+      const int qb = nu & 1;
+      if (nu >= 2 && !wait_bar(&q_empty[qb], ((nu >> 1) - 1) & 1, ctl)) break;
+      if (!more) {
+        if (lane == 0) {
+          unit_at[qb].b = -1;
+          mbar_arrive(&q_full[qb]);
+        }
+        break;
+      }
+      const int rows = u.m * p.G, n0 = u.rt * C::R;
+      // Queries on their way while the first pages are looked up.
+      uint32_t qw[C::R][E / 2];
+#pragma unroll
+      for (int r = 0; r < C::R; ++r) {
+        const int x = n0 + r, i = x / p.G, hq = u.h * p.G + (x - i * p.G);
+        const uint16_t* at = static_cast<const uint16_t*>(p.q) + p.q_ss * (u.q0 + i) + p.q_sh * hq + lane * E;
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) qw[r][e] = 0;
+        if (x < rows) {
+          if constexpr (E % 8 == 0) {
+#pragma unroll
+            for (int e = 0; e < E / 8; ++e) {
+              const uint4 w = reinterpret_cast<const uint4*>(at)[e];
+              qw[r][4 * e] = w.x;
+              qw[r][4 * e + 1] = w.y;
+              qw[r][4 * e + 2] = w.z;
+              qw[r][4 * e + 3] = w.w;
+            }
+          } else if constexpr (E == 4) {
+            const uint2 w = *reinterpret_cast<const uint2*>(at);
+            qw[r][0] = w.x;
+            qw[r][1] = w.y;
+          } else {
+#pragma unroll
+            for (int e = 0; e < E / 2; ++e) qw[r][e] = reinterpret_cast<const uint32_t*>(at)[e];
+          }
+        }
+      }
       const int32_t* table = p.s.table + (int64_t)u.b * p.s.max_pages;
       // Lane l looks after 16-key slice l of the next eight tiles.
       auto page_at = [&](int tile0) {
         const int key = tile0 * kCaKeys + lane * 16, first = key & -box;
-        if (first >= hi || first + box <= lo || tile0 * 4 + lane >= tb * 4) return -1;
+        if (first >= u.hi || first + box <= u.lo || tile0 * 4 + lane >= u.tb * 4) return -1;
         int pg = table[key >> p.c.page_lg];
         if (pg < 0 || pg >= p.c.pages) {
           record_status(p.status, kStatusDeviceArgs);
@@ -293,43 +358,89 @@ __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV, NT>::CTAS)
         const int64_t a = (int64_t)pg * p.c.Hkv + u.h;
         return pg < 0 ? make_float2(0.f, 1.f) : make_float2(p.c.k_scale[a], p.c.v_scale[a]);
       };
-      int pg = page_at(ta);
+      int pg = page_at(u.ta);
       float2 sc = scales_at(pg);
-      int pg_next = page_at(ta + 8);
-      for (int t8 = ta; ok && t8 < tb; t8 += 8) {
+      int pg_next = page_at(u.ta + 8);
+      // The codes of a tile into stage `it` (which is free).
+      auto load_tile = [&](int tile, int i) {
+        const int st = it % C::STAGES;
+        const int key0 = tile * kCaKeys;
+        uint8_t* dst = smem + st * C::STAGE;
+        const int b0 = max(u.lo - key0, 0) / box, b1 = min((u.hi - key0 + box - 1) / box, boxes);
+        if (lane == 0) mbar_expect_tx(&full[st], (uint32_t)(b1 - b0) * box * C::ROWB * (C::KP + C::VP));
+        for (int x = b0; x < b1; ++x) {
+          const int use = __shfl_sync(0xffffffffu, pg, i * 4 + x * per_box);
+          if (lane == 0) {
+            const int row = (key0 + x * box) & (p.c.page - 1);
+#pragma unroll
+            for (int k = 0; k < C::KP; ++k)
+              tma_load_4d(dst + k * C::PLANE + x * box * C::ROWB, &p.tm_k, &full[st], k * 128, row, u.h, use);
+#pragma unroll
+            for (int k = 0; k < C::VP; ++k)
+              tma_load_4d(dst + (C::KP + k) * C::PLANE + x * box * C::ROWB, &p.tm_v, &full[st], k * 128, row, u.h,
+                          use);
+          }
+        }
+      };
+      // The scales of the tile, and the arrival that completes the stage.
+      auto finish_tile = [&](int i, float lvs) {
+        const int st = it % C::STAGES;
+        if ((lane >> 2) == i) meta[st][lane & 3] = make_float2(sc.x, lvs);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[st]);
+        ++it;
+      };
+      // At the start of the share the first tile's codes go out before anything waits for the queries.
+      const bool early = it == 0 && u.ta < u.tb;
+      if (early) load_tile(u.ta, 0);
+
+#pragma unroll
+      for (int r = 0; r < C::R; ++r) {
+        const int x = n0 + r;
+        float v[E], top = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+          const float2 f = p.f16 ? unpack2<__half>(qw[r][e / 2]) : unpack2<__nv_bfloat16>(qw[r][e / 2]);
+          v[e] = f.x;
+          v[e + 1] = f.y;
+          top = fmax3(top, fabsf(f.x), fabsf(f.y));
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const int field = min(268 - (__float_as_int(top) >> 23), 253);  // 2^14 <= top * 2^(field - 127) < 2^15
+        const float up = __int_as_float(field << 23), down = __int_as_float((254 - field) << 23);
+        uint32_t* to = reinterpret_cast<uint32_t*>(smem + C::Q_OFF + qb * C::QBYTES + (r * C::QPITCH + lane * E) * 2);
+#pragma unroll
+        for (int e = 0; e < E; e += 2) to[e / 2] = pack2<__half>(v[e] * up, v[e + 1] * up);
+        if (lane == 0) {
+          int2 lim = make_int2(0, 0);
+          if (x < rows) ca_row_keys(p, u.n, u.m, x / p.G, lim.x, lim.y);
+          row_lim_at[qb][r] = lim;
+          row_fac_at[qb][r] = down * (p.softcap > 0.f ? p.scale / p.softcap : p.scale * 1.4426950408889634f);
+        }
+      }
+      if (lane == 0) unit_at[qb] = u;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_full[qb]);
+      ++nu;
+
+      for (int t8 = u.ta; ok && t8 < u.tb; t8 += 8) {
         const float2 sc_next = scales_at(pg_next);
         const int pg_after = page_at(t8 + 16);
         const float lvs = log2f(sc.y);
-        for (int i = 0; i < 8 && t8 + i < tb; ++i, ++it) {
-          const int st = it % C::STAGES;
-          if (it >= C::STAGES && !wait_bar(&empty[st], ((it / C::STAGES) - 1) & 1, ctl)) {
+        for (int i = 0; i < 8 && t8 + i < u.tb; ++i) {
+          if (it >= C::STAGES && !wait_bar(&empty[it % C::STAGES], ((it / C::STAGES) - 1) & 1, ctl)) {
             ok = false;
             break;
           }
-          if ((lane >> 2) == i) meta[st][lane & 3] = make_float2(sc.x, lvs);
-          __syncwarp();
-          const int key0 = (t8 + i) * kCaKeys;
-          uint8_t* dst = smem + st * C::STAGE;
-          const int b0 = max(lo - key0, 0) / box, b1 = min((hi - key0 + box - 1) / box, boxes);
-          if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)(b1 - b0) * box * C::ROWB * (C::KP + C::VP));
-          for (int x = b0; x < b1; ++x) {
-            const int use = __shfl_sync(0xffffffffu, pg, i * 4 + x * per_box);
-            if (lane == 0) {
-              const int row = (key0 + x * box) & (p.c.page - 1);
-#pragma unroll
-              for (int k = 0; k < C::KP; ++k)
-                tma_load_4d(dst + k * C::PLANE + x * box * C::ROWB, &p.tm_k, &full[st], k * 128, row, u.h, use);
-#pragma unroll
-              for (int k = 0; k < C::VP; ++k)
-                tma_load_4d(dst + (C::KP + k) * C::PLANE + x * box * C::ROWB, &p.tm_v, &full[st], k * 128, row, u.h,
-                            use);
-            }
-          }
+          if (!(early && t8 == u.ta && i == 0)) load_tile(t8 + i, i);
+          finish_tile(i, lvs);
         }
         pg = pg_next;
         sc = sc_next;
         pg_next = pg_after;
       }
+      if (!ok) break;
     }
     // After an abort the copies in flight are waited for (with a limit) before the CTA ends.
     if (abort_flag)
@@ -347,7 +458,6 @@ __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV, NT>::CTAS)
   const int ka = warp * 16 + row_at(g);  // key rows of this lane's scores: ka, ka + 8
   const int va = warp * 16 + row_at(2 * t), vb = warp * 16 + row_at(2 * t + 1);  // V rows: va, vb, + 8 each
   const uint32_t ring = smem_u32(smem);
-  const uint32_t qs = smem_u32(smem + C::Q_OFF);
   float* ob = reinterpret_cast<float*>(smem + C::O_OFF);
   auto k_off = [&](int row, int j) -> uint32_t {
     if (DQK == 64) return row * 64 + ((t ^ ((row >> 1) & 3)) << 4);
@@ -361,55 +471,17 @@ __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV, NT>::CTAS)
   constexpr int VW = DV == 64 ? 2 : 4;   // 4-code words a lane reads of a key row and plane
   uint32_t it = 0;
   bool ok = true;
-
-  while (walk.next<C>(p, u)) {
-    int lo, hi, ta, tb;
-    ca_unit_keys(p, C::R, u, lo, hi, ta, tb);
-    const int rows = u.m * p.G, n0 = u.rt * C::R;
-    consumers_sync();  // the last unit's shared rows are read
-    for (int r = warp; r < C::R; r += kCaWarps) {
-      const int x = n0 + r, i = x / p.G, hq = u.h * p.G + (x - i * p.G);
-      constexpr int E = DQK / 32;  // elements per lane
-      float v[E];
-      float top = 0.f;
-#pragma unroll
-      for (int e = 0; e < E; ++e) v[e] = 0.f;
-      if (x < rows) {
-        const int64_t at = p.q_ss * (u.q0 + i) + p.q_sh * hq + lane * E;
-#pragma unroll
-        for (int e = 0; e < E; e += 2) {
-          const uint32_t w = *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p.q) + at + e);
-          const float2 f = p.f16 ? unpack2<__half>(w) : unpack2<__nv_bfloat16>(w);
-          v[e] = f.x;
-          v[e + 1] = f.y;
-        }
-      }
-#pragma unroll
-      for (int e = 0; e < E; ++e) top = fmaxf(top, fabsf(v[e]));
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const int field = min(268 - (__float_as_int(top) >> 23), 253);  // 2^14 <= top * 2^(field - 127) < 2^15
-      const float up = __int_as_float(field << 23), down = __int_as_float((254 - field) << 23);
-#pragma unroll
-      for (int e = 0; e < E; e += 2)
-        *reinterpret_cast<uint32_t*>(smem + C::Q_OFF + (r * C::QPITCH + lane * E + e) * 2) =
-            pack2<__half>(v[e] * up, v[e + 1] * up);
-      if (lane == 0) {
-        int2 lim = make_int2(0, 0);
-        if (x < rows) ca_row_keys(p, u.n, u.m, i, lim.x, lim.y);
-        row_lim[r] = lim;
-        row_fac[r] = down * (p.softcap > 0.f ? p.scale / p.softcap : p.scale * 1.4426950408889634f);
-      }
-    }
-    consumers_sync();
-    // Every row that exists sees keys [in_lo, in_hi): tiles inside need no mask.
-    int in_lo, in_hi;
-    {
-      const int i0 = n0 / p.G, i1 = (min(n0 + C::R, rows) - 1) / p.G;
-      int x;
-      ca_row_keys(p, u.n, u.m, i1, in_lo, x);
-      ca_row_keys(p, u.n, u.m, i0, x, in_hi);
-    }
+  for (uint32_t nu = 0;; ++nu) {
+    const int qb = nu & 1;
+    // All four warps go on or none does: a wait that ran out in one of them must
+    // not leave the others at a barrier.
+    if (!consumers_all(wait_bar(&q_full[qb], (nu >> 1) & 1, ctl))) break;
+    const CaUnit& u = unit_at[qb];
+    if (u.b < 0) break;
+    const int rows = u.m * p.G, n0 = u.rt * C::R, lo = u.lo, hi = u.hi;
+    const float* row_fac = row_fac_at[qb];
+    const int2* row_lim = row_lim_at[qb];
+    const uint32_t qs = smem_u32(smem + C::Q_OFF + qb * C::QBYTES);
     uint32_t qf[C::QREGS ? NT : 1][C::QREGS ? DQK / 8 : 1];
     if constexpr (C::QREGS) {
 #pragma unroll
@@ -479,7 +551,7 @@ __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV, NT>::CTAS)
           const uint32_t a1 = e4m3_to_half2(wb[w] & 0xffff), a3 = e4m3_to_half2(wb[w] >> 16);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
-            mma16816((w & 1) ? s2[nt] : s[nt], a0, a1, a2, a3, qv[nt][2 * w], qv[nt][2 * w + 1]);
+            mma16816(NT == 1 && (w & 1) ? s2[nt] : s[nt], a0, a1, a2, a3, qv[nt][2 * w], qv[nt][2 * w + 1]);
         }
       }
       // Scores in log2 units.
@@ -490,7 +562,7 @@ __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV, NT>::CTAS)
         const float f0 = fac[nt][0] * sc.x, f1 = fac[nt][1] * sc.x;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          float x = (s[nt][c] + s2[nt][c]) * ((c & 1) ? f1 : f0);
+          float x = (NT == 1 ? s[nt][c] + s2[nt][c] : s[nt][c]) * ((c & 1) ? f1 : f0);
           if (p.softcap > 0.f) {
             // c tanh(y) log2(e), tanh(y) = 1 - 2 / (e^(2y) + 1): off by some 2^-22 of the cap
             const float e = ex2_approx(x * 2.8853900817779268f);
@@ -600,6 +672,7 @@ __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV, NT>::CTAS)
       }
       if constexpr (MASK) {
         if (__any_sync(0xffffffffu, nan_seen != 0)) {
+#pragma unroll 1
           for (int r = 0; r < 16; ++r) {
             const int row = warp * 16 + r, k = tile * kCaKeys + row;
 #pragma unroll
@@ -623,11 +696,11 @@ __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV, NT>::CTAS)
       if (lane == 0) mbar_arrive(&empty[st]);
     };
 
-    for (int tile = ta; tile < tb; ++tile, ++it) {
+    for (int tile = u.ta; tile < u.tb; ++tile, ++it) {
       if (ok && !wait_bar(&full[it % C::STAGES], (it / C::STAGES) & 1, ctl)) ok = false;
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) continue;
-      if (tile * kCaKeys >= in_lo && (tile + 1) * kCaKeys <= in_hi)
+      if (tile * kCaKeys >= u.in_lo && (tile + 1) * kCaKeys <= u.in_hi)
         tile_step(MaskTag<false>(), tile);
       else
         tile_step(MaskTag<true>(), tile);
@@ -667,21 +740,24 @@ __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV, NT>::CTAS)
 #pragma unroll
         for (int c = 0; c < 4; ++c) o[m][nt][c] *= f[c & 1];
     }
+#pragma unroll 1
     for (int w = 0; w < kCaWarps; ++w) {
       if (warp == w) {
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
+        for (int m = 0; m < MT; m += 2) {
           const int d = DV == 64 ? g * 8 + m * 2 : (m >> 3) * 128 + g * 16 + (m & 7) * 2;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              float2* at = reinterpret_cast<float2*>(ob + (nt * 8 + 2 * t + c) * C::OPITCH + d);
-              float2 x = make_float2(o[m][nt][c], o[m][nt][2 + c]);
+              float4* at = reinterpret_cast<float4*>(ob + (nt * 8 + 2 * t + c) * C::OPITCH + d);
+              float4 x = make_float4(o[m][nt][c], o[m][nt][2 + c], o[m + 1][nt][c], o[m + 1][nt][2 + c]);
               if (w) {
-                const float2 y = *at;
+                const float4 y = *at;
                 x.x += y.x;
                 x.y += y.y;
+                x.z += y.z;
+                x.w += y.w;
               }
               *at = x;
             }
@@ -714,18 +790,21 @@ __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV, NT>::CTAS)
       }
       if (tid < live) p.part_l[slot * C::R + tid] = fin_l[tid];
     }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&q_empty[qb]);
   }
 }
 
 // Joins the partial results of units that several CTAs share, in the order of
 // the CTAs, and writes the rows that no CTA wrote: sequences without keys, and
 // (blockIdx.y = B) rows past the last sequence. One CTA per (head, row tile) and sequence.
-constexpr int kJoinThreads = 128;
+constexpr int kJoinThreads = 512;
 template <int DQK, int DV, int NT>
 __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_constant__ CacheAttnParams p, int grid) {
   using C = CaCfg<DQK, DV, NT>;
   __shared__ int64_t sum_before[kJoinThreads / 32], sum_all[kJoinThreads / 32];
   __shared__ float row_l[C::R];
+  __shared__ float4 sums[kJoinThreads];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = blockIdx.y;
   auto write8 = [&](int64_t row, int hq, int d, const float* x) {
@@ -765,7 +844,7 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
   }
   int64_t before = 0, total = 0;
   for (int x = tid; x < p.s.B; x += kJoinThreads) {
-    const int64_t n = ca_seq(p, C::R, x).tiles(p.c.Hkv);
+    const int64_t n = ca_seq(p, C::R, x).places(p.c.Hkv);
     total += n;
     before += x < b ? n : 0;
   }
@@ -785,8 +864,8 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
     total += sum_all[w];
     before += sum_before[w];
   }
-  const int parts = ca_parts(total, grid, p.min_tiles);
-  const int64_t x0 = before + ((int64_t)h * s.rt + rt) * s.kt;
+  const int parts = ca_parts(total, grid, p.min_share);
+  const int64_t x0 = before + ((int64_t)h * s.rt + rt) * s.cost() + kCaUnit;  // the unit's first tile
   const int c0 = ca_owner(total, parts, x0), c1 = ca_owner(total, parts, x0 + s.kt - 1);
   if (c0 == c1) return;  // one CTA had it all and wrote it
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -809,25 +888,42 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
     }
   }
   __syncthreads();
-  for (int x = tid; x < live * (DV / 8); x += kJoinThreads) {
-    const int r = x / (DV / 8), d = (x - r * (DV / 8)) * 8, y = n0 + r, i = y / p.G;
+  // A thread takes four columns of a row over every GROUPS-th partial result;
+  // the groups' sums are added in their order.
+  constexpr int VEC = DV / 4, ROWS = kJoinThreads / VEC >= 8 ? 8 : kJoinThreads / VEC;
+  constexpr int GROUPS = kJoinThreads / (VEC * ROWS);
+  const int gr = tid / (VEC * ROWS), rr = tid / VEC % ROWS, d = (tid % VEC) * 4;
+  for (int r0 = 0; r0 < live; r0 += ROWS) {
+    const int r = min(r0 + rr, live - 1);
     const float l = minus_inf_as_0(row_l[r]);
-    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-    for (int k = 0; k < np; ++k) {
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int k = gr; k < np; k += GROUPS) {
       const float w = ex2_approx(p.part_l[slot(k) * C::R + r] - l);
-      const float4* at = reinterpret_cast<const float4*>(p.part_o + (slot(k) * C::R + r) * DV + d);
-      const float4 a = at[0], e = at[1];
-      acc[0] = fmaf(a.x, w, acc[0]);
-      acc[1] = fmaf(a.y, w, acc[1]);
-      acc[2] = fmaf(a.z, w, acc[2]);
-      acc[3] = fmaf(a.w, w, acc[3]);
-      acc[4] = fmaf(e.x, w, acc[4]);
-      acc[5] = fmaf(e.y, w, acc[5]);
-      acc[6] = fmaf(e.z, w, acc[6]);
-      acc[7] = fmaf(e.w, w, acc[7]);
+      const float4 a = *reinterpret_cast<const float4*>(p.part_o + (slot(k) * C::R + r) * DV + d);
+      acc.x = fmaf(a.x, w, acc.x);
+      acc.y = fmaf(a.y, w, acc.y);
+      acc.z = fmaf(a.z, w, acc.z);
+      acc.w = fmaf(a.w, w, acc.w);
     }
-    write8(s.q.q0 + i, h * p.G + y - i * p.G, d, acc);
+    __syncthreads();
+    sums[tid] = acc;
+    __syncthreads();
+    if (gr == 0 && r0 + rr < live) {
+#pragma unroll
+      for (int k = 1; k < GROUPS; ++k) {
+        const float4 a = sums[tid + k * VEC * ROWS];
+        acc.x += a.x;
+        acc.y += a.y;
+        acc.z += a.z;
+        acc.w += a.w;
+      }
+      const int y = n0 + r, i = y / p.G;
+      const uint2 w = p.f16 ? make_uint2(pack2<__half>(acc.x, acc.y), pack2<__half>(acc.z, acc.w))
+                            : make_uint2(pack2<__nv_bfloat16>(acc.x, acc.y), pack2<__nv_bfloat16>(acc.z, acc.w));
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + p.o_ss * (s.q.q0 + i) +
+                                p.o_sh * (h * p.G + y - i * p.G) + d) = w;
+    }
   }
 }
 

@@ -46,7 +46,7 @@ struct CacheAttnParams {
   int causal, window;  // window > 0: left window counting the current token
   int accumulate;      // add each key's probabilities to c.weight
   int f16;
-  int min_tiles;  // a CTA's share is at least this many key tiles
+  int min_share;  // a CTA's share is at least this many key tiles
   int row_tiles;  // of a sequence with the most rows
   // Workspace: partial results [CTA][2][R][Dv] and their lse in log2 units
   // [CTA][2][R]; scores [B * Hkv][score_rows][score_cap] in log2 units.
