@@ -19,6 +19,7 @@ Nothing here synchronises; every call can be captured into a CUDA graph.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -37,8 +38,8 @@ class KVCache:
     by ``attn_cache_fwd(accumulate=True)`` and used by ``kv_cache_evict``.
     """
 
-    __slots__ = ("k", "v", "k_scale", "v_scale", "weight", "num_pages", "Hkv", "page_size", "Dqk", "Dv", "_struct",
-                 "_ref")
+    __slots__ = ("k", "v", "k_scale", "v_scale", "weight", "num_pages", "Hkv", "page_size", "Dqk", "Dv", "device",
+                 "_struct", "_ref")
 
     def __init__(self, k, v, k_scale, v_scale, weight=None):
         _need_view(k, "cache k", torch.float8_e4m3fn)
@@ -46,25 +47,32 @@ class KVCache:
         if k.dim() != 4 or v.dim() != 4 or k.shape[:3] != v.shape[:3]:
             raise ValueError("cache k and v must be [num_pages, Hkv, page_size, D] with equal leading dims")
         num_pages, Hkv, page_size, Dqk = k.shape
-        for t, n, shape in ((k_scale, "k_scale", (num_pages, Hkv)), (v_scale, "v_scale", (num_pages, Hkv)),
-                            (weight, "weight", (num_pages, Hkv, page_size))):
-            if t is None and n == "weight":
-                continue
-            _need(t, n, torch.float32)
-            if tuple(t.shape) != shape:
-                raise ValueError(f"{n} must be {list(shape)}, got {list(t.shape)}")
-        for t in (v, k_scale, v_scale, weight):
-            if t is not None and t.device != k.device:
-                raise ValueError("the cache's tensors must be on one device")
+        Dv = v.shape[3]
+        device = k.device
+        _cache_f32(k_scale, "k_scale", (num_pages, Hkv), device)
+        _cache_f32(v_scale, "v_scale", (num_pages, Hkv), device)
+        if weight is not None:
+            _cache_f32(weight, "weight", (num_pages, Hkv, page_size), device)
+        if v.device != device:
+            raise ValueError("the cache's tensors must be on one device")
         self.k, self.v, self.k_scale, self.v_scale, self.weight = k, v, k_scale, v_scale, weight
-        self.num_pages, self.Hkv, self.page_size, self.Dqk, self.Dv = num_pages, Hkv, page_size, Dqk, v.shape[3]
+        self.num_pages, self.Hkv, self.page_size, self.Dqk, self.Dv = num_pages, Hkv, page_size, Dqk, Dv
+        self.device = device
         c = _lib.KVCacheStruct(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), _ptr(weight),
-                               num_pages, page_size, Hkv, Dqk, self.Dv)
+                               num_pages, page_size, Hkv, Dqk, Dv)
         if not (k.is_contiguous() and v.is_contiguous()):
             c.k_strides[:] = k.stride()[:3]
             c.v_strides[:] = v.stride()[:3]
         self._struct = c
         self._ref = ctypes.byref(c)
+
+
+def _cache_f32(t, name, shape, device):
+    _need(t, name, torch.float32)
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.device != device:
+        raise ValueError("the cache's tensors must be on one device")
 
 
 def kv_cache(num_pages, Hkv, Dqk, Dv, page_size=64, weights=False, device="cuda") -> KVCache:
@@ -76,35 +84,37 @@ def kv_cache(num_pages, Hkv, Dqk, Dv, page_size=64, weights=False, device="cuda"
     return KVCache(k, v, ks, torch.zeros_like(ks), w)
 
 
-class _on:
-    """The device of a call's tensors, made current for its launches (they may be on another than the current one)."""
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
-    __slots__ = ("index", "before")
 
-    def __init__(self, t):
-        self.index = t.device.index
-
-    def __enter__(self):
-        self.before = torch.cuda.current_device()
-        if self.before != self.index:
-            torch.cuda.set_device(self.index)
-        return torch.cuda.current_stream(self.index).cuda_stream
-
-    def __exit__(self, *exc):
-        if self.before != self.index:
-            torch.cuda.set_device(self.before)
+def _launch(device, call, *args) -> None:
+    """call(*args, stream) with `device` current (a call's tensors may be on another than the current one)."""
+    index = device.index
+    before = torch.cuda.current_device()
+    if before == index:
+        rc = call(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            rc = call(*args, _raw_stream(index))
+    if rc:
+        check(rc)
 
 
 def _sequences(cache, page_table, seq_lens, *others):
     """(B, max_pages) of a call's sequences; `others`: further tensors that must be on the cache's device."""
     _i32(page_table, "page_table")
     _i32(seq_lens, "seq_lens")
-    if page_table.dim() != 2 or seq_lens.dim() != 1 or page_table.shape[0] != seq_lens.shape[0]:
+    shape = page_table.shape
+    if len(shape) != 2 or seq_lens.shape != shape[:1]:
         raise ValueError("page_table must be [B, max_pages] and seq_lens [B]")
-    for t in (page_table, seq_lens, *others):
-        if t is not None and t.device != cache.k.device:
+    device = cache.device
+    if page_table.device != device or seq_lens.device != device:
+        raise ValueError("every tensor of a call must be on the cache's device")
+    for t in others:
+        if t is not None and t.device != device:
             raise ValueError("every tensor of a call must be on the cache's device")
-    return page_table.shape
+    return shape
 
 
 def _cu(cu, name, B):
@@ -140,16 +150,18 @@ def kv_cache_append(cache, k, v, page_table, seq_lens, cu_new=None) -> None:
         raise ValueError("k and v must have the same number of rows")
     B, max_pages = _sequences(cache, page_table, seq_lens, k, v, cu_new)
     _cu(cu_new, "cu_new", B)
-    with _on(k) as stream:
-        check(_lib.load().psf_kv_cache_append(cache._ref, k.data_ptr(), v.data_ptr(), _thd_strides(k, v), dt,
-                                              _ptr(cu_new), page_table.data_ptr(), seq_lens.data_ptr(), B, max_pages,
-                                              k.shape[0], stream))
+    _launch(cache.device, _lib.load().psf_kv_cache_append, cache._ref, k.data_ptr(), v.data_ptr(), _thd_strides(k, v),
+            dt, _ptr(cu_new), page_table.data_ptr(), seq_lens.data_ptr(), B, max_pages, k.shape[0])
+
+
+@functools.lru_cache(maxsize=256)
+def _attn_workspace(*sizes) -> int:
+    return int(_lib.load().psf_attn_cache_workspace_size(*sizes))
 
 
 def attn_cache_workspace_size(cache, B, max_pages, Hq, max_q=1, accumulate=False) -> int:
-    return int(_lib.load().psf_attn_cache_workspace_size(int(B), int(max_pages), cache.page_size, int(Hq), cache.Hkv,
-                                                         cache.Dqk, cache.Dv, int(max_q),
-                                                         PSF_CACHE_ACCUMULATE if accumulate else 0))
+    return _attn_workspace(int(B), int(max_pages), cache.page_size, int(Hq), cache.Hkv, cache.Dqk, cache.Dv, int(max_q),
+                           PSF_CACHE_ACCUMULATE if accumulate else 0)
 
 
 def attn_cache_fwd(q, cache, page_table, seq_lens, scale, cu_q=None, max_q=None, causal=True, window=None,
@@ -175,7 +187,7 @@ def attn_cache_fwd(q, cache, page_table, seq_lens, scale, cu_q=None, max_q=None,
             raise ValueError("cu_q needs max_q, the most query rows of a sequence")
         max_q = T // B if B else 0
     if out is None:
-        out = torch.empty(T, Hq, cache.Dv, dtype=q.dtype, device=q.device)
+        out = torch.empty((T, Hq, cache.Dv), dtype=q.dtype, device=q.device)
     else:
         _need_view(out, "out", q.dtype)
         _rows3(out, "out", Hq, cache.Dv)
@@ -189,18 +201,21 @@ def attn_cache_fwd(q, cache, page_table, seq_lens, scale, cu_q=None, max_q=None,
             raise ValueError(f"lse must be [{Hq}, {T}], got {list(lse.shape)}")
     if workspace is None:
         workspace = _workspace(attn_cache_workspace_size(cache, B, max_pages, Hq, max_q, accumulate), q.device)
-    with _on(q) as stream:
-        check(_lib.load().psf_attn_cache_fwd(
-            q.data_ptr(), cache._ref, out.data_ptr(), lse.data_ptr(), _ptr(cu_q), page_table.data_ptr(),
-            seq_lens.data_ptr(), B, max_pages, T, int(max_q), Hq, _thd_strides(q, out), _DTYPES[q.dtype], float(scale),
-            int(bool(causal)), _window(window), _cap(softcap), PSF_CACHE_ACCUMULATE if accumulate else 0,
-            workspace.data_ptr(), workspace.numel() * workspace.element_size(), stream))
+    _launch(cache.device, _lib.load().psf_attn_cache_fwd, q.data_ptr(), cache._ref, out.data_ptr(), lse.data_ptr(),
+            _ptr(cu_q), page_table.data_ptr(), seq_lens.data_ptr(), B, max_pages, T, int(max_q), Hq,
+            _thd_strides(q, out), _DTYPES[q.dtype], float(scale), int(bool(causal)), _window(window), _cap(softcap),
+            PSF_CACHE_ACCUMULATE if accumulate else 0, workspace.data_ptr(),
+            workspace.numel() * workspace.element_size())
     return out, lse
 
 
+@functools.lru_cache(maxsize=256)
+def _evict_workspace(*sizes) -> int:
+    return int(_lib.load().psf_kv_cache_evict_workspace_size(*sizes))
+
+
 def kv_cache_evict_workspace_size(cache, B, max_pages, budget) -> int:
-    return int(_lib.load().psf_kv_cache_evict_workspace_size(int(B), int(max_pages), cache.page_size, cache.Hkv,
-                                                             int(budget)))
+    return _evict_workspace(int(B), int(max_pages), cache.page_size, cache.Hkv, int(budget))
 
 
 def kv_cache_evict(cache, page_table, seq_lens, budget, recent, new_lens=None, workspace=None):
@@ -219,11 +234,9 @@ def kv_cache_evict(cache, page_table, seq_lens, budget, recent, new_lens=None, w
             raise ValueError("new_lens must be [B]")
     if workspace is None:
         workspace = _workspace(kv_cache_evict_workspace_size(cache, B, max_pages, budget), seq_lens.device)
-    with _on(seq_lens) as stream:
-        check(_lib.load().psf_kv_cache_evict(cache._ref, page_table.data_ptr(), seq_lens.data_ptr(),
-                                             new_lens.data_ptr(), B, max_pages, int(budget), int(recent),
-                                             workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                                             stream))
+    _launch(cache.device, _lib.load().psf_kv_cache_evict, cache._ref, page_table.data_ptr(), seq_lens.data_ptr(),
+            new_lens.data_ptr(), B, max_pages, int(budget), int(recent), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size())
     return new_lens
 
 
@@ -240,8 +253,6 @@ def kv_cache_gather(cache, page_table, seq_lens, total_k, dtype=torch.bfloat16):
     k = torch.empty(int(total_k), cache.Hkv, cache.Dqk, dtype=dtype, device=dev)
     v = torch.empty(int(total_k), cache.Hkv, cache.Dv, dtype=dtype, device=dev)
     cu_k = torch.empty(B + 1, dtype=torch.int32, device=dev)
-    with _on(seq_lens) as stream:
-        check(_lib.load().psf_kv_cache_gather(cache._ref, page_table.data_ptr(), seq_lens.data_ptr(), B, max_pages,
-                                              k.data_ptr(), v.data_ptr(), cu_k.data_ptr(), int(total_k),
-                                              _DTYPES[dtype], stream))
+    _launch(cache.device, _lib.load().psf_kv_cache_gather, cache._ref, page_table.data_ptr(), seq_lens.data_ptr(), B,
+            max_pages, k.data_ptr(), v.data_ptr(), cu_k.data_ptr(), int(total_k), _DTYPES[dtype])
     return k, v, cu_k

@@ -463,8 +463,8 @@ cudaError_t launch_cache_evict(const CacheView& c, const SeqView& s, int budget,
                                const EvictWorkspace& ws, int sms, int* status, cudaStream_t st) {
   const int smem_keys = (int)min(ws.cap, (int64_t)kEvictSmemKeys);
   const int smem = smem_keys * 4;
-  cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       kEvictSmemKeys * 4);
+  static std::atomic<uint64_t> smem_set{0};
+  cudaError_t e = smem_limit(evict_select_kernel, kEvictSmemKeys * 4, smem_set);
   if (e != cudaSuccess) return e;
   evict_select_kernel<<<dim3(c.Hkv, s.B), kSelectThreads, smem, st>>>(c, s, budget, recent, new_lens, ws, smem_keys,
                                                                      status);

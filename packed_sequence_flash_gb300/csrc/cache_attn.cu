@@ -13,9 +13,10 @@ constexpr int kWeightThreads = 256;
 __global__ void __launch_bounds__(kWeightThreads) cache_weight_kernel(const __grid_constant__ CacheAttnParams p) {
   const CacheView& c = p.c;
   const int b = blockIdx.z, h = blockIdx.y, j = blockIdx.x * kWeightThreads + threadIdx.x;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const Seq q = seq_at(p.s, c.page, b);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (j >= q.n) return;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int pg = p.s.table[(int64_t)b * p.s.max_pages + (j >> c.page_lg)];
   if (pg < 0 || pg >= c.pages) return;
   const float* s = p.scores + (((int64_t)b * c.Hkv + h) * p.score_rows) * p.score_cap + j;
@@ -31,12 +32,14 @@ __global__ void __launch_bounds__(kWeightThreads) cache_weight_kernel(const __gr
   atomicAdd(c.weight + ((int64_t)pg * c.Hkv + h) * c.page + (j & (c.page - 1)), sum);
 }
 
-// A kernel that may start while the one before it still runs (it waits with griddepcontrol.wait).
+// A launch that may begin while the kernel before it in the stream still runs
+// (its kernel waits with griddepcontrol.wait before it reads what that one writes).
 template <typename... A>
-cudaError_t launch_after(void (*kernel)(A...), dim3 grid, int threads, cudaStream_t st, A... args) {
+cudaError_t launch_early(void (*kernel)(A...), dim3 grid, int threads, int smem, cudaStream_t st, A... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -46,44 +49,35 @@ cudaError_t launch_after(void (*kernel)(A...), dim3 grid, int threads, cudaStrea
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <int DQK, int DV, int NT>
+template <int DQK, int DV>
 cudaError_t run(CacheAttnParams& p, int max_q, int sms, cudaStream_t st) {
-  using C = CaCfg<DQK, DV, NT>;
-  cudaError_t e = cudaFuncSetAttribute(cache_attn_kernel<DQK, DV, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       C::SMEM);
+  using C = CaCfg<DQK, DV>;
+  static std::atomic<uint64_t> smem_set{0};
+  cudaError_t e = smem_limit(cache_attn_kernel<DQK, DV>, C::SMEM, smem_set);
   if (e != cudaSuccess) return e;
   const int grid = sms * C::CTAS;
-  p.row_tiles = max(1, (int)(((int64_t)max_q * p.G + C::R - 1) / C::R));
-  cache_attn_kernel<DQK, DV, NT><<<grid, kCaThreads, C::SMEM, st>>>(p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  return launch_after(cache_join_kernel<DQK, DV, NT>, dim3(p.c.Hkv * p.row_tiles, p.s.B + (p.s.cu ? 1 : 0)),
-                      kJoinThreads, st, (const CacheAttnParams)p, grid);
+  p.row_tiles = max(1, (int)(((int64_t)max_q * p.G + kCaRows - 1) / kCaRows));
+  e = launch_early(cache_attn_kernel<DQK, DV>, dim3(grid), kCaThreads, C::SMEM, st, (const CacheAttnParams)p);
+  if (e != cudaSuccess) return e;
+  return launch_early(cache_join_kernel<DQK, DV>, dim3(p.c.Hkv * p.row_tiles, p.s.B + (p.s.cu ? 1 : 0)), kJoinThreads,
+                      0, st, (const CacheAttnParams)p, grid);
 }
 
 }  // namespace
 
-// Row tiles of 8 rows for one group of heads and one token, of 16 and 32 rows
-// where there are more rows; 8 at head dim 512, where O takes 128 registers.
-int cache_attn_nt(int Dqk, int64_t rows) { return Dqk == 512 || rows <= 8 ? 1 : (rows <= 16 ? 2 : 4); }
-
 cudaError_t launch_cache_attn(CacheAttnParams& p, int max_q, int sms, cudaStream_t st) {
-  const int nt = cache_attn_nt(p.c.Dqk, (int64_t)max_q * p.G);
   cudaError_t e;
-#define PSF_RUN(DQK, DV)                                              \
-  e = nt == 1 ? run<DQK, DV, 1>(p, max_q, sms, st)                    \
-              : (nt == 2 ? run<DQK, DV, 2>(p, max_q, sms, st) : run<DQK, DV, 4>(p, max_q, sms, st))
   if (p.c.Dqk == 64)
-    PSF_RUN(64, 64);
+    e = run<64, 64>(p, max_q, sms, st);
   else if (p.c.Dqk == 128)
-    PSF_RUN(128, 128);
+    e = run<128, 128>(p, max_q, sms, st);
   else if (p.c.Dqk == 192)
-    PSF_RUN(192, 128);
+    e = run<192, 128>(p, max_q, sms, st);
   else
-    e = run<512, 512, 1>(p, max_q, sms, st);
-#undef PSF_RUN
+    e = run<512, 512>(p, max_q, sms, st);
   if (e != cudaSuccess || !p.accumulate) return e;
   const unsigned chunks = (unsigned)((p.score_cap + kWeightThreads - 1) / kWeightThreads);
-  return launch_after(cache_weight_kernel, dim3(chunks, p.c.Hkv, p.s.B), kWeightThreads, st,
+  return launch_early(cache_weight_kernel, dim3(chunks, p.c.Hkv, p.s.B), kWeightThreads, 0, st,
                       (const CacheAttnParams)p);
 }
 

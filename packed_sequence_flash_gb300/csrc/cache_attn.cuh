@@ -12,14 +12,14 @@
 // codes are expanded in place, so the legacy instruction is the fitting one.
 //
 // Rows: the query rows of one KV head (m rows x G heads, token-major) in tiles
-// of R = 8 NT rows. Keys: tiles of 64. A CTA takes an equal share of all
+// of 8. Keys: tiles of 64. A CTA takes an equal share of all
 // (sequence, KV head, row tile, key tile) in that order, wherever it begins and
 // ends, so ragged batches and a single long sequence alike fill the device.
 // A share that covers all tiles of a (sequence, head, row tile) writes its
 // result; otherwise it leaves a partial result (o / l, lse) that the join kernel
 // adds up in the order of the CTAs. Nothing depends on the order of execution.
 //
-//   warp 4     producer: the next unit's queries (two buffers), page numbers and
+//   warp 4     producer: the next unit and its queries ahead of time, page numbers and
 //              scales one batch ahead, K and V pages by TMA into a ring of stages
 //              (128-byte rows, 128-byte swizzle; 64-byte rows for head dim 64)
 //   warps 0-3  16 keys of each tile each, with a softmax state of their own
@@ -50,67 +50,87 @@
 namespace psf {
 
 constexpr int kCaKeys = 64;       // keys per tile
+constexpr int kCaRows = kCacheAttnRows;
 constexpr int kCaWarps = 4;       // consumer warps, 16 keys of a tile each
-constexpr int kCaThreads = 160;
+constexpr int kCaConsumers = 32 * kCaWarps;
+constexpr int kCaThreads = kCaConsumers + 32;
+constexpr int kCaUnits = 3;       // units under way: finishing, current, next
 constexpr float kCaLazy = 8.f;    // a reference moves when a score is 2^8 above it
 constexpr float kCaHead = 7.f;    // the P reference sits 2^7 below the largest value
+constexpr float kCaFloor = -3e38f;  // references before the first score (finite: no inf - inf)
 
-template <int DQK, int DV, int NT>
+template <int DQK, int DV>
 struct CaCfg {
-  static constexpr int R = 8 * NT;
   static constexpr int KP = DQK <= 128 ? 1 : (DQK + 127) / 128;  // 128-byte planes of a K row
   static constexpr int VP = DV <= 128 ? 1 : (DV + 127) / 128;
   static constexpr int ROWB = DQK == 64 ? 64 : 128;  // bytes of a row in a plane
   static constexpr int PLANE = kCaKeys * ROWB;
   static constexpr int STAGE = (KP + VP) * PLANE;
-  static constexpr int CTAS = cache_attn_ctas(DQK, NT);
-  static constexpr int QPITCH = DQK + 8;  // fp16 elements
-  static constexpr int OPITCH = DV + 4;   // fp32 elements
-  static constexpr int QBYTES = R * QPITCH * 2;  // one of two buffers
-  static constexpr int FIXED = 2 * QBYTES + R * OPITCH * 4 + 1024;
+  static constexpr int CTAS = cache_attn_ctas(DQK);
+  static constexpr int RAW = kCaRows * DQK * 2;        // queries as they come, one of kCaUnits buffers
+  static constexpr int QPITCH = DQK + 8;         // fp16 elements of a query row
+  static constexpr int OPITCH = DV + 4;          // fp32 elements
+  static constexpr int OBYTES = kCaWarps * kCaRows * OPITCH * 4;
+  static constexpr int FIXED = kCaUnits * RAW + OBYTES + 1024;
   // As many stages as fit beside 2 KB of static and 1 KB of reserved shared
   // memory: 64 KB or more of the cache in flight per SM.
   static constexpr int FIT = (233472 / CTAS - 3072 - FIXED) / STAGE;
   static constexpr int STAGES = FIT > 8 ? 8 : FIT;
-  static constexpr int Q_OFF = STAGES * STAGE;
-  static constexpr int O_OFF = Q_OFF + 2 * QBYTES;
+  static constexpr int RAW_OFF = STAGES * STAGE;
+  static constexpr int O_OFF = RAW_OFF + kCaUnits * RAW;
+  static constexpr int Q_OFF = O_OFF;  // the queries are done with before O is written
   static constexpr int SMEM = STAGES * STAGE + FIXED;
-  static_assert(CTAS * STAGES * STAGE >= 64 * 1024, "bytes in flight");
-  static constexpr bool QREGS = NT * DQK <= 256;  // Q operand kept in registers
+  static_assert(STAGES >= 2 && CTAS * STAGES * STAGE >= 64 * 1024, "bytes in flight");
+  static_assert(kCaRows * QPITCH * 2 <= OBYTES, "queries fit where O goes");
+  static constexpr bool QREGS = DQK <= 192;  // Q operand kept in registers
 };
+
+// a / b, in 32 bits when both fit (most of the time).
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return (int64_t)((uint32_t)a / (uint32_t)b);
+  return a / b;
+}
 
 // Share of the work. A unit is a (sequence, head, row tile); it costs its key
 // tiles and kCaUnit more (queries in, four warps' states into one, result out),
-// laid out as kCaUnit places and then a place per tile. CTA c takes places
-// [ca_first(c), ca_first(c + 1)) of the units in order. Without the unit's cost a
+// laid out as kCaUnit places and then a place per tile. Each CTA takes an equal
+// run of the places of the units in order. Without the unit's cost a
 // share of many short sequences took five times as long as one of a long one
 // (16 sequences of 5 to 4099 tokens: 148 us).
-constexpr int kCaUnit = 2;
+constexpr int kCaUnit = 6;
 struct CaSeq {
   Seq q;
   int rt, kt, t0;  // row tiles, key tiles, first key tile
   __device__ __forceinline__ int cost() const { return kt + kCaUnit; }
   __device__ __forceinline__ int64_t places(int Hkv) const { return kt ? (int64_t)Hkv * rt * cost() : 0; }
 };
-__device__ __forceinline__ CaSeq ca_seq(const CacheAttnParams& p, int R, int b) {
+__device__ __forceinline__ CaSeq ca_seq(const CacheAttnParams& p, int b) {
   CaSeq s;
   s.q = seq_at(p.s, p.c.page, b);
   const int lo = p.window > 0 ? max(0, s.q.n - s.q.m - p.window + 1) : 0;
   s.t0 = lo / kCaKeys;
   s.kt = s.q.m > 0 ? max(0, (s.q.n + kCaKeys - 1) / kCaKeys - s.t0) : 0;
-  s.rt = (s.q.m * p.G + R - 1) / R;
+  s.rt = (s.q.m * p.G + kCaRows - 1) / kCaRows;
   return s;
 }
-// CTAs that share `total` places, and the first place of CTA c (c = parts: total).
+// CTAs that share `total` places, and how they do.
 __device__ __forceinline__ int ca_parts(int64_t total, int grid, int min_share) {
   const int64_t most = (total + min_share - 1) / min_share;
   return (int)(most < grid ? most : grid);
 }
-__device__ __forceinline__ int64_t ca_first(int64_t total, int parts, int c) { return total * c / parts; }
-// The CTA that place x belongs to.
-__device__ __forceinline__ int ca_owner(int64_t total, int parts, int64_t x) {
-  return (int)(((x + 1) * parts - 1) / total);
-}
+struct CaShares {
+  int64_t each, more;  // the first `more` CTAs take each + 1 places, the others each
+  __device__ __forceinline__ CaShares(int64_t total, int parts) {
+    each = parts ? quotient(total, parts) : 0;
+    more = total - each * parts;
+  }
+  __device__ __forceinline__ int64_t first(int c) const { return each * c + min((int64_t)c, more); }
+  // The CTA that place x belongs to.
+  __device__ __forceinline__ int owner(int64_t x) const {
+    const int64_t cut = more * (each + 1);
+    return (int)(x < cut ? quotient(x, each + 1) : more + quotient(x - cut, each));
+  }
+};
 
 // Keys [lo, hi) that row i of m sees of n cached tokens (the last row sits at the last token).
 __device__ __forceinline__ void ca_row_keys(const CacheAttnParams& p, int n, int m, int i, int& lo, int& hi) {
@@ -122,8 +142,7 @@ __device__ __forceinline__ void ca_row_keys(const CacheAttnParams& p, int n, int
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -132,22 +151,10 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint32_t lds8(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
-  return v;
-}
+__device__ __forceinline__ uint4 lds128(const uint8_t* a) { return *reinterpret_cast<const uint4*>(a); }
+__device__ __forceinline__ uint2 lds64(const uint8_t* a) { return *reinterpret_cast<const uint2*>(a); }
 __device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+// Whether x holds for all consumer threads.
 __device__ __forceinline__ bool consumers_all(bool x) {
   uint32_t r;
   asm volatile(
@@ -159,6 +166,13 @@ __device__ __forceinline__ bool consumers_all(bool x) {
       : "r"((uint32_t)x)
       : "memory");
   return r != 0;
+}
+// Contiguous copy of `bytes` (a multiple of 16) into shared memory, counted on bar.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
 }
 __device__ __forceinline__ float minus_inf_as_0(float x) { return x == -CUDART_INF_F ? 0.f : x; }
 
@@ -176,15 +190,15 @@ struct CaWalk {
   int64_t pos, end, base;
   int b;
   CaSeq s;
-  __device__ __forceinline__ bool next(const CacheAttnParams& p, int R, CaUnit& u) {
+  __device__ __forceinline__ bool next(const CacheAttnParams& p, CaUnit& u) {
     while (pos < end) {
       int64_t n = s.places(p.c.Hkv);
       while (pos >= base + n) {
         base += n;
-        s = ca_seq(p, R, ++b);
+        s = ca_seq(p, ++b);
         n = s.places(p.c.Hkv);
       }
-      const int64_t rel = pos - base, x = rel / s.cost();
+      const int64_t rel = pos - base, x = quotient(rel, s.cost());
       const int off = (int)(rel - x * s.cost());
       const int stop = (int)min((int64_t)s.cost(), off + (end - pos));
       pos += stop - off;
@@ -200,7 +214,7 @@ struct CaWalk {
       u.t1 = s.t0 + k1;
       u.whole = k1 - k0 == s.kt;
       u.slot = k0 == 0;
-      const int i0 = u.rt * R / p.G, i1 = (min((u.rt + 1) * R, u.m * p.G) - 1) / p.G;
+      const int i0 = u.rt * kCaRows / p.G, i1 = (min((u.rt + 1) * kCaRows, u.m * p.G) - 1) / p.G;
       ca_row_keys(p, u.n, u.m, i0, u.lo, u.in_hi);
       ca_row_keys(p, u.n, u.m, i1, u.in_lo, u.hi);
       u.ta = max(u.t0, u.lo / kCaKeys);
@@ -211,20 +225,20 @@ struct CaWalk {
   }
 };
 
-template <int DQK, int DV, int NT>
-__global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV, NT>::CTAS)
+template <int DQK, int DV>
+__global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV>::CTAS)
     cache_attn_kernel(const __grid_constant__ CacheAttnParams p) {
-  using C = CaCfg<DQK, DV, NT>;
+  using C = CaCfg<DQK, DV>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ uint64_t full[C::STAGES], empty[C::STAGES];
-  __shared__ float2 meta[C::STAGES][kCaWarps];  // K scale and log2 of the V scale of each warp's keys
-  __shared__ uint64_t q_full[2], q_empty[2];
-  __shared__ CaUnit unit_at[2];             // b < 0: no more units
-  __shared__ float row_fac_at[2][C::R];     // query scale times the logit scale
-  __shared__ int2 row_lim_at[2][C::R];      // keys that a row sees
-  __shared__ float st_mu[kCaWarps][C::R], st_l[kCaWarps][C::R], fin_l[C::R];
-  __shared__ int64_t scan[8], found_base;
+  __shared__ float2 meta[C::STAGES][kCaWarps];  // K scale and log2 of the V scale of 16 keys
+  __shared__ uint64_t q_full[kCaUnits], q_empty[kCaUnits];
+  __shared__ CaUnit unit_at[kCaUnits];  // b < 0: no more units
+  __shared__ float row_fac[kCaRows];  // query scale times the logit scale
+  __shared__ int2 row_lim[kCaRows];   // keys that a row sees
+  __shared__ float st_mu[kCaWarps][kCaRows], st_l[kCaWarps][kCaRows], fin_l[kCaRows];
+  __shared__ int64_t scan[kCaThreads / 32], found_base;
   __shared__ int found_b, abort_flag;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -233,7 +247,7 @@ __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV, NT>::CTAS)
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], kCaWarps);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kCaUnits; ++i) {
       mbar_init(&q_full[i], 1);
       mbar_init(&q_empty[i], kCaWarps);
     }
@@ -242,52 +256,72 @@ __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV, NT>::CTAS)
     tma_prefetch_desc(&p.tm_k);
     tma_prefetch_desc(&p.tm_v);
   }
+  // Nothing above touches memory that the kernel before this one may still
+  // write; the join may start once every CTA is past this point.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  // The whole work, then the sequence that this share begins in.
-  int64_t mine = 0, first_count = 0;
-  for (int b = tid; b < p.s.B; b += kCaThreads) {
-    const CaSeq s = ca_seq(p, C::R, b);
-    if (s.q.bad && blockIdx.x == 0) record_status(p.status, kStatusDeviceArgs);
-    const int64_t n = s.places(p.c.Hkv);
-    if (b == tid) first_count = n;
-    mine += n;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-  if (lane == 0) scan[warp] = mine;
-  __syncthreads();
-  int64_t total = 0;
-#pragma unroll
-  for (int w = 0; w < kCaThreads / 32; ++w) total += scan[w];
-  const int parts = ca_parts(total, gridDim.x, p.min_share);
-  if ((int)blockIdx.x >= parts) return;
-  CaWalk walk;
-  walk.pos = ca_first(total, parts, blockIdx.x);
-  walk.end = ca_first(total, parts, blockIdx.x + 1);
-  int64_t carry = 0;
+  // The whole work, and the sequence that this share begins in.
+  int64_t total = 0, before = 0, count = 0;  // places before and of this thread's sequence
   for (int base = 0; base < p.s.B; base += kCaThreads) {
     const int b = base + tid;
-    const int64_t n = base == 0 ? first_count : (b < p.s.B ? ca_seq(p, C::R, b).places(p.c.Hkv) : 0);
-    int64_t x = n;
+    count = 0;
+    if (b < p.s.B) {
+      const CaSeq s = ca_seq(p, b);
+      if (s.q.bad && blockIdx.x == 0) record_status(p.status, kStatusDeviceArgs);
+      count = s.places(p.c.Hkv);
+    }
+    int64_t x = count;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
       if (lane >= o) x += y;
     }
-    __syncthreads();
+    if (base) __syncthreads();
     if (lane == 31) scan[warp] = x;
     __syncthreads();
-    int64_t before = carry;
+    before = total + x - count;
     for (int w = 0; w < kCaThreads / 32; ++w) {
       if (w < warp) before += scan[w];
-      carry += scan[w];
+      total += scan[w];
     }
-    if (b < p.s.B && n > 0 && walk.pos >= before + x - n && walk.pos < before + x) {
-      found_b = b;
-      found_base = before + x - n;
+  }
+  const int parts = ca_parts(total, gridDim.x, p.min_share);
+  if ((int)blockIdx.x >= parts) return;
+  const CaShares shares(total, parts);
+  CaWalk walk;
+  walk.pos = shares.first(blockIdx.x);
+  walk.end = shares.first(blockIdx.x + 1);
+  if (p.s.B <= kCaThreads) {
+    if (count > 0 && walk.pos >= before && walk.pos < before + count) {
+      found_b = tid;
+      found_base = before;
     }
-    if (carry > walk.pos) break;  // the same for every thread
+  } else {
+    int64_t carry = 0;
+    for (int base = 0; base < p.s.B; base += kCaThreads) {
+      const int b = base + tid;
+      const int64_t n = b < p.s.B ? ca_seq(p, b).places(p.c.Hkv) : 0;
+      int64_t x = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      __syncthreads();
+      if (lane == 31) scan[warp] = x;
+      __syncthreads();
+      int64_t at = carry;
+      for (int w = 0; w < kCaThreads / 32; ++w) {
+        if (w < warp) at += scan[w];
+        carry += scan[w];
+      }
+      if (n > 0 && walk.pos >= at + x - n && walk.pos < at + x) {
+        found_b = b;
+        found_base = at + x - n;
+      }
+      if (carry > walk.pos) break;  // the same for every thread
+    }
   }
   __syncthreads();
   const Ctl ctl{p.status, p.limit_ns, &abort_flag};
@@ -296,156 +330,117 @@ __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV, NT>::CTAS)
     // ------------------------------------------------------------ producer
     walk.b = found_b;
     walk.base = found_base;
-    walk.s = ca_seq(p, C::R, found_b);
+    walk.s = ca_seq(p, found_b);
     const int box = min(p.c.page, kCaKeys), per_box = box / 16, boxes = kCaKeys / box;
-    constexpr int E = DQK / 32;  // query elements per lane and row
     uint32_t it = 0, nu = 0;
     bool ok = true;
-    CaUnit u;
-    while (true) {
-      const bool more = walk.next(p, C::R, u);
-      const int qb = nu & 1;
-      if (nu >= 2 && !wait_bar(&q_empty[qb], ((nu >> 1) - 1) & 1, ctl)) break;
-      if (!more) {
-        if (lane == 0) {
+    // Lane l looks after 16-key slice l of the next eight tiles.
+    auto page_at = [&](const CaUnit& u, int tile0) {
+      const int key = tile0 * kCaKeys + lane * 16, first = key & -box;
+      if (first >= u.hi || first + box <= u.lo || tile0 * 4 + lane >= u.tb * 4) return -1;
+      int pg = p.s.table[(int64_t)u.b * p.s.max_pages + (key >> p.c.page_lg)];
+      if (pg < 0 || pg >= p.c.pages) {
+        record_status(p.status, kStatusDeviceArgs);
+        pg = 0;
+      }
+      return pg;
+    };
+    auto scales_at = [&](int h, int pg) {
+      const int64_t a = (int64_t)pg * p.c.Hkv + h;
+      return pg < 0 ? make_float2(0.f, 1.f) : make_float2(p.c.k_scale[a], p.c.v_scale[a]);
+    };
+    // Hands the next unit to the consumers with its queries, as they are: a row
+    // each of the first eight lanes. Without one, tells them so.
+    auto announce = [&](bool more, const CaUnit& u) {
+      const int qb = nu % kCaUnits;
+      if (nu >= kCaUnits && !wait_bar(&q_empty[qb], (nu / kCaUnits - 1) & 1, ctl)) return false;
+      const int n0 = u.rt * kCaRows, rows = more ? min(u.m * p.G - n0, kCaRows) : 0;
+      if (lane == 0) {
+        if (more)
+          unit_at[qb] = u;
+        else
           unit_at[qb].b = -1;
-          mbar_arrive(&q_full[qb]);
-        }
-        break;
+        mbar_arrive_expect_tx(&q_full[qb], (uint32_t)rows * DQK * 2);
       }
-      const int rows = u.m * p.G, n0 = u.rt * C::R;
-      // Queries on their way while the first pages are looked up.
-      uint32_t qw[C::R][E / 2];
-#pragma unroll
-      for (int r = 0; r < C::R; ++r) {
-        const int x = n0 + r, i = x / p.G, hq = u.h * p.G + (x - i * p.G);
-        const uint16_t* at = static_cast<const uint16_t*>(p.q) + p.q_ss * (u.q0 + i) + p.q_sh * hq + lane * E;
-#pragma unroll
-        for (int e = 0; e < E / 2; ++e) qw[r][e] = 0;
-        if (x < rows) {
-          if constexpr (E % 8 == 0) {
-#pragma unroll
-            for (int e = 0; e < E / 8; ++e) {
-              const uint4 w = reinterpret_cast<const uint4*>(at)[e];
-              qw[r][4 * e] = w.x;
-              qw[r][4 * e + 1] = w.y;
-              qw[r][4 * e + 2] = w.z;
-              qw[r][4 * e + 3] = w.w;
-            }
-          } else if constexpr (E == 4) {
-            const uint2 w = *reinterpret_cast<const uint2*>(at);
-            qw[r][0] = w.x;
-            qw[r][1] = w.y;
-          } else {
-#pragma unroll
-            for (int e = 0; e < E / 2; ++e) qw[r][e] = reinterpret_cast<const uint32_t*>(at)[e];
-          }
-        }
-      }
-      const int32_t* table = p.s.table + (int64_t)u.b * p.s.max_pages;
-      // Lane l looks after 16-key slice l of the next eight tiles.
-      auto page_at = [&](int tile0) {
-        const int key = tile0 * kCaKeys + lane * 16, first = key & -box;
-        if (first >= u.hi || first + box <= u.lo || tile0 * 4 + lane >= u.tb * 4) return -1;
-        int pg = table[key >> p.c.page_lg];
-        if (pg < 0 || pg >= p.c.pages) {
-          record_status(p.status, kStatusDeviceArgs);
-          pg = 0;
-        }
-        return pg;
-      };
-      auto scales_at = [&](int pg) {
-        const int64_t a = (int64_t)pg * p.c.Hkv + u.h;
-        return pg < 0 ? make_float2(0.f, 1.f) : make_float2(p.c.k_scale[a], p.c.v_scale[a]);
-      };
-      int pg = page_at(u.ta);
-      float2 sc = scales_at(pg);
-      int pg_next = page_at(u.ta + 8);
-      // The codes of a tile into stage `it` (which is free).
-      auto load_tile = [&](int tile, int i) {
-        const int st = it % C::STAGES;
-        const int key0 = tile * kCaKeys;
-        uint8_t* dst = smem + st * C::STAGE;
-        const int b0 = max(u.lo - key0, 0) / box, b1 = min((u.hi - key0 + box - 1) / box, boxes);
-        if (lane == 0) mbar_expect_tx(&full[st], (uint32_t)(b1 - b0) * box * C::ROWB * (C::KP + C::VP));
-        for (int x = b0; x < b1; ++x) {
-          const int use = __shfl_sync(0xffffffffu, pg, i * 4 + x * per_box);
-          if (lane == 0) {
-            const int row = (key0 + x * box) & (p.c.page - 1);
-#pragma unroll
-            for (int k = 0; k < C::KP; ++k)
-              tma_load_4d(dst + k * C::PLANE + x * box * C::ROWB, &p.tm_k, &full[st], k * 128, row, u.h, use);
-#pragma unroll
-            for (int k = 0; k < C::VP; ++k)
-              tma_load_4d(dst + (C::KP + k) * C::PLANE + x * box * C::ROWB, &p.tm_v, &full[st], k * 128, row, u.h,
-                          use);
-          }
-        }
-      };
-      // The scales of the tile, and the arrival that completes the stage.
-      auto finish_tile = [&](int i, float lvs) {
-        const int st = it % C::STAGES;
-        if ((lane >> 2) == i) meta[st][lane & 3] = make_float2(sc.x, lvs);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&full[st]);
-        ++it;
-      };
-      // At the start of the share the first tile's codes go out before anything waits for the queries.
-      const bool early = it == 0 && u.ta < u.tb;
-      if (early) load_tile(u.ta, 0);
-
-#pragma unroll
-      for (int r = 0; r < C::R; ++r) {
-        const int x = n0 + r;
-        float v[E], top = 0.f;
-#pragma unroll
-        for (int e = 0; e < E; e += 2) {
-          const float2 f = p.f16 ? unpack2<__half>(qw[r][e / 2]) : unpack2<__nv_bfloat16>(qw[r][e / 2]);
-          v[e] = f.x;
-          v[e + 1] = f.y;
-          top = fmax3(top, fabsf(f.x), fabsf(f.y));
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const int field = min(268 - (__float_as_int(top) >> 23), 253);  // 2^14 <= top * 2^(field - 127) < 2^15
-        const float up = __int_as_float(field << 23), down = __int_as_float((254 - field) << 23);
-        uint32_t* to = reinterpret_cast<uint32_t*>(smem + C::Q_OFF + qb * C::QBYTES + (r * C::QPITCH + lane * E) * 2);
-#pragma unroll
-        for (int e = 0; e < E; e += 2) to[e / 2] = pack2<__half>(v[e] * up, v[e + 1] * up);
-        if (lane == 0) {
-          int2 lim = make_int2(0, 0);
-          if (x < rows) ca_row_keys(p, u.n, u.m, x / p.G, lim.x, lim.y);
-          row_lim_at[qb][r] = lim;
-          row_fac_at[qb][r] = down * (p.softcap > 0.f ? p.scale / p.softcap : p.scale * 1.4426950408889634f);
-        }
-      }
-      if (lane == 0) unit_at[qb] = u;
       __syncwarp();
-      if (lane == 0) mbar_arrive(&q_full[qb]);
+      if (lane < rows) {
+        const int x = n0 + lane, i = x / p.G, hq = u.h * p.G + (x - i * p.G);
+        bulk_load(smem + C::RAW_OFF + qb * C::RAW + lane * DQK * 2,
+                  static_cast<const uint16_t*>(p.q) + p.q_ss * (u.q0 + i) + p.q_sh * hq, DQK * 2, &q_full[qb]);
+      }
       ++nu;
-
+      return true;
+    };
+    CaUnit u, next;
+    bool more = walk.next(p, u);
+    int pg = more ? page_at(u, u.ta) : -1;
+    ok = announce(more, u);
+    while (ok && more) {
+      float2 sc = scales_at(u.h, pg);
+      int pg_next = page_at(u, u.ta + 8), pg_unit = -1;
+      bool looked = false, more_next = false;
       for (int t8 = u.ta; ok && t8 < u.tb; t8 += 8) {
-        const float2 sc_next = scales_at(pg_next);
-        const int pg_after = page_at(t8 + 16);
-        const float lvs = log2f(sc.y);
-        for (int i = 0; i < 8 && t8 + i < u.tb; ++i) {
-          if (it >= C::STAGES && !wait_bar(&empty[it % C::STAGES], ((it / C::STAGES) - 1) & 1, ctl)) {
+        float2 sc_next = make_float2(0.f, 1.f);
+        int pg_after = -1;
+        for (int i = 0; i < 8 && t8 + i < u.tb; ++i, ++it) {
+          const int st = it % C::STAGES;
+          if (it >= C::STAGES && !wait_bar(&empty[st], ((it / C::STAGES) - 1) & 1, ctl)) {
             ok = false;
             break;
           }
-          if (!(early && t8 == u.ta && i == 0)) load_tile(t8 + i, i);
-          finish_tile(i, lvs);
+          const int key0 = (t8 + i) * kCaKeys;
+          uint8_t* dst = smem + st * C::STAGE;
+          const int b0 = max(u.lo - key0, 0) / box, b1 = min((u.hi - key0 + box - 1) / box, boxes);
+          if (lane == 0) mbar_expect_tx(&full[st], (uint32_t)(b1 - b0) * box * C::ROWB * (C::KP + C::VP));
+          for (int x = b0; x < b1; ++x) {
+            const int use = __shfl_sync(0xffffffffu, pg, i * 4 + x * per_box);
+            if (lane == 0) {
+              const int row = (key0 + x * box) & (p.c.page - 1);
+#pragma unroll
+              for (int k = 0; k < C::KP; ++k)
+                tma_load_4d(dst + k * C::PLANE + x * box * C::ROWB, &p.tm_k, &full[st], k * 128, row, u.h, use);
+#pragma unroll
+              for (int k = 0; k < C::VP; ++k)
+                tma_load_4d(dst + (C::KP + k) * C::PLANE + x * box * C::ROWB, &p.tm_v, &full[st], k * 128, row, u.h,
+                            use);
+            }
+          }
+          // The scales are waited for only here, with the codes on their way.
+          if ((lane >> 2) == i) meta[st][lane & 3] = make_float2(sc.x, log2f(sc.y));
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&full[st]);
+          if (i == 0) {
+            sc_next = scales_at(u.h, pg_next);
+            pg_after = page_at(u, t8 + 16);
+            if (!looked) {
+              // With the first tile out: which unit comes next, its queries and first pages.
+              looked = true;
+              more_next = walk.next(p, next);
+              if (more_next) pg_unit = page_at(next, next.ta);
+              if (!announce(more_next, next)) ok = false;
+            }
+          }
         }
         pg = pg_next;
         sc = sc_next;
         pg_next = pg_after;
       }
-      if (!ok) break;
+      if (!looked) {  // a unit whose rows see no key
+        more_next = walk.next(p, next);
+        if (more_next) pg_unit = page_at(next, next.ta);
+        ok = announce(more_next, next);
+      }
+      more = more_next;
+      u = next;
+      pg = pg_unit;
     }
     // After an abort the copies in flight are waited for (with a limit) before the CTA ends.
-    if (abort_flag)
+    if (abort_flag) {
       for (uint32_t k = it > C::STAGES ? it - C::STAGES : 0; k < it; ++k)
         wait_bar_drain(&full[k % C::STAGES], (k / C::STAGES) & 1, p.limit_ns);
+      for (uint32_t k = nu > kCaUnits ? nu - kCaUnits : 0; k < nu; ++k)
+        wait_bar_drain(&q_full[k % kCaUnits], (k / kCaUnits) & 1, p.limit_ns);
+    }
     return;
   }
 
@@ -457,7 +452,6 @@ __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV, NT>::CTAS)
   };
   const int ka = warp * 16 + row_at(g);  // key rows of this lane's scores: ka, ka + 8
   const int va = warp * 16 + row_at(2 * t), vb = warp * 16 + row_at(2 * t + 1);  // V rows: va, vb, + 8 each
-  const uint32_t ring = smem_u32(smem);
   float* ob = reinterpret_cast<float*>(smem + C::O_OFF);
   auto k_off = [&](int row, int j) -> uint32_t {
     if (DQK == 64) return row * 64 + ((t ^ ((row >> 1) & 3)) << 4);
@@ -467,179 +461,197 @@ __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV, NT>::CTAS)
     if (DV == 64) return C::PLANE + row * 64 + (((g >> 1) ^ ((row >> 1) & 3)) << 4) + (g & 1) * 8;
     return (C::KP + j) * C::PLANE + row * 128 + ((g ^ (row & 7)) << 4);
   };
-  constexpr int MT = DV / 16;            // products along the head dim of V
-  constexpr int VW = DV == 64 ? 2 : 4;   // 4-code words a lane reads of a key row and plane
-  uint32_t it = 0;
+  const uint8_t* qs = smem + C::Q_OFF + g * C::QPITCH * 2 + t * 32;  // Q operand: 16 fp16 of each 64
+  constexpr int MT = DV / 16;           // products along the head dim of V
+  constexpr int VW = DV == 64 ? 2 : 4;  // 4-code words a lane reads of a key row and plane
+  int st = 0;         // stage of the ring
+  uint32_t ring = 0;  // its phase
   bool ok = true;
   for (uint32_t nu = 0;; ++nu) {
-    const int qb = nu & 1;
-    // All four warps go on or none does: a wait that ran out in one of them must
-    // not leave the others at a barrier.
-    if (!consumers_all(wait_bar(&q_full[qb], (nu >> 1) & 1, ctl))) break;
+    const int qb = nu % kCaUnits;
+    // All warps go on or none does: a wait that ran out in one of them must not
+    // leave the others at a barrier.
+    if (!consumers_all(wait_bar(&q_full[qb], (nu / kCaUnits) & 1, ctl))) break;
     const CaUnit& u = unit_at[qb];
     if (u.b < 0) break;
-    const int rows = u.m * p.G, n0 = u.rt * C::R, lo = u.lo, hi = u.hi;
-    const float* row_fac = row_fac_at[qb];
-    const int2* row_lim = row_lim_at[qb];
-    const uint32_t qs = smem_u32(smem + C::Q_OFF + qb * C::QBYTES);
-    uint32_t qf[C::QREGS ? NT : 1][C::QREGS ? DQK / 8 : 1];
+    const int rows = u.m * p.G, n0 = u.rt * kCaRows, lo = u.lo, hi = u.hi;
+    // Queries to fp16, each row scaled by a power of two: a warp two rows.
+#pragma unroll
+    for (int e2 = 0; e2 < 2; ++e2) {
+      constexpr int E = DQK / 32;  // elements per lane and row
+      const int r = warp + e2 * kCaWarps;
+      const uint32_t* from = reinterpret_cast<const uint32_t*>(smem + C::RAW_OFF + qb * C::RAW + r * DQK * 2) + lane * (E / 2);
+      float v[E], top = 0.f;
+#pragma unroll
+      for (int e = 0; e < E; e += 2) {
+        const uint32_t w = n0 + r < rows ? from[e / 2] : 0u;
+        const float2 f = p.f16 ? unpack2<__half>(w) : unpack2<__nv_bfloat16>(w);
+        v[e] = f.x;
+        v[e + 1] = f.y;
+        top = fmax3(top, fabsf(f.x), fabsf(f.y));
+      }
+#pragma unroll
+      for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+      const int field = min(268 - (__float_as_int(top) >> 23), 253);  // 2^14 <= top * 2^(field - 127) < 2^15
+      const float up = __int_as_float(field << 23), down = __int_as_float((254 - field) << 23);
+      uint32_t* to = reinterpret_cast<uint32_t*>(smem + C::Q_OFF + r * C::QPITCH * 2) + lane * (E / 2);
+#pragma unroll
+      for (int e = 0; e < E; e += 2) to[e / 2] = pack2<__half>(v[e] * up, v[e + 1] * up);
+      if (lane == 0) {
+        int2 lim = make_int2(0, 0);
+        if (n0 + r < rows) ca_row_keys(p, u.n, u.m, (n0 + r) / p.G, lim.x, lim.y);
+        row_lim[r] = lim;
+        row_fac[r] = down * (p.softcap > 0.f ? p.scale / p.softcap : p.scale * 1.4426950408889634f);
+      }
+    }
+    consumers_sync();
+    uint32_t qf[C::QREGS ? DQK / 8 : 1];
     if constexpr (C::QREGS) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int j = 0; j < DQK / 64; ++j)
 #pragma unroll
-        for (int j = 0; j < DQK / 64; ++j)
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const uint4 a = lds128(qs + ((nt * 8 + g) * C::QPITCH + j * 64 + t * 16 + x * 8) * 2);
-            qf[nt][j * 8 + x * 4] = a.x;
-            qf[nt][j * 8 + x * 4 + 1] = a.y;
-            qf[nt][j * 8 + x * 4 + 2] = a.z;
-            qf[nt][j * 8 + x * 4 + 3] = a.w;
-          }
+        for (int x = 0; x < 2; ++x) {
+          const uint4 a = lds128(qs + j * 128 + x * 16);
+          qf[j * 8 + x * 4] = a.x;
+          qf[j * 8 + x * 4 + 1] = a.y;
+          qf[j * 8 + x * 4 + 2] = a.z;
+          qf[j * 8 + x * 4 + 3] = a.w;
+        }
     }
-    float fac[NT][2], mu[NT][2], ro[NT][2], l[NT][2];
-    float o[MT][NT][4];
+    // Columns of this lane: rows r0 + 2 t and + 1 of the tile.
+    const float fac[2] = {row_fac[2 * t], row_fac[2 * t + 1]};
+    float mu[2], ro[2], l[2];
+    float o[MT][4];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        fac[nt][c] = row_fac[nt * 8 + 2 * t + c];
-        mu[nt][c] = ro[nt][c] = -CUDART_INF_F;
-        l[nt][c] = 0.f;
-      }
+    for (int c = 0; c < 2; ++c) {
+      mu[c] = ro[c] = kCaFloor;
+      l[c] = 0.f;
+    }
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) o[m][nt][c] = 0.f;
+      for (int c = 0; c < 4; ++c) o[m][c] = 0.f;
 
     auto tile_step = [&](auto mask_tag, int tile) {
       constexpr bool MASK = decltype(mask_tag)::value;
-      const int st = it % C::STAGES;
-      const uint32_t sb = ring + st * C::STAGE;
+      const uint8_t* sb = smem + st * C::STAGE;
       const int key = tile * kCaKeys + ka;
-      float s[NT][4], s2[NT][4];
+      float s[4], s2[4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) s[nt][c] = s2[nt][c] = 0.f;
+      for (int c = 0; c < 4; ++c) s[c] = s2[c] = 0.f;
 #pragma unroll
       for (int j = 0; j < DQK / 64; ++j) {
         const uint4 xa = lds128(sb + k_off(ka, j)), xb = lds128(sb + k_off(ka + 8, j));
         const uint32_t wa[4] = {xa.x, xa.y, xa.z, xa.w}, wb[4] = {xb.x, xb.y, xb.z, xb.w};
-        uint32_t qv[NT][8];
+        uint32_t qv[8];
+        if constexpr (C::QREGS) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          if constexpr (C::QREGS) {
+          for (int e = 0; e < 8; ++e) qv[e] = qf[j * 8 + e];
+        } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) qv[nt][e] = qf[nt][j * 8 + e];
-          } else {
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const uint4 a = lds128(qs + ((nt * 8 + g) * C::QPITCH + j * 64 + t * 16 + x * 8) * 2);
-              qv[nt][x * 4] = a.x;
-              qv[nt][x * 4 + 1] = a.y;
-              qv[nt][x * 4 + 2] = a.z;
-              qv[nt][x * 4 + 3] = a.w;
-            }
+          for (int x = 0; x < 2; ++x) {
+            const uint4 a = lds128(qs + j * 128 + x * 16);
+            qv[x * 4] = a.x;
+            qv[x * 4 + 1] = a.y;
+            qv[x * 4 + 2] = a.z;
+            qv[x * 4 + 3] = a.w;
           }
         }
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
           const uint32_t a0 = e4m3_to_half2(wa[w] & 0xffff), a2 = e4m3_to_half2(wa[w] >> 16);
           const uint32_t a1 = e4m3_to_half2(wb[w] & 0xffff), a3 = e4m3_to_half2(wb[w] >> 16);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            mma16816(NT == 1 && (w & 1) ? s2[nt] : s[nt], a0, a1, a2, a3, qv[nt][2 * w], qv[nt][2 * w + 1]);
+          mma16816((w & 1) ? s2 : s, a0, a1, a2, a3, qv[2 * w], qv[2 * w + 1]);
         }
       }
-      // Scores in log2 units.
+      // Exponents of the row sum's terms (x) and of P (y) against the references:
+      // x = z - mu, y = z + log2 v_scale - ro, z the score in log2 units.
       const float2 sc = meta[st][warp];
-      bool move = false;
+      float x[4], y[4];
+      float f[2] = {fac[0] * sc.x, fac[1] * sc.x};
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const float f0 = fac[nt][0] * sc.x, f1 = fac[nt][1] * sc.x;
+      for (int c = 0; c < 4; ++c) s[c] += s2[c];
+      if (p.softcap > 0.f) {
+        // c tanh(a) log2(e), tanh(a) = 1 - 2 / (e^(2a) + 1): off by some 2^-22 of the cap
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          float x = (NT == 1 ? s[nt][c] + s2[nt][c] : s[nt][c]) * ((c & 1) ? f1 : f0);
-          if (p.softcap > 0.f) {
-            // c tanh(y) log2(e), tanh(y) = 1 - 2 / (e^(2y) + 1): off by some 2^-22 of the cap
-            const float e = ex2_approx(x * 2.8853900817779268f);
-            x = p.softcap * 1.4426950408889634f * fmaf(-2.f, rcp_approx(e + 1.f), 1.f);
-          }
-          s[nt][c] = x;
+          const float e = ex2_approx(s[c] * f[c & 1] * 2.8853900817779268f);
+          s[c] = p.softcap * 1.4426950408889634f * fmaf(-2.f, rcp_approx(e + 1.f), 1.f);
         }
-        if (p.accumulate) {
-          const int64_t unit = (int64_t)u.b * p.c.Hkv + u.h;
+        f[0] = f[1] = 1.f;
+      }
+      if (p.accumulate) {
+        const int64_t unit = (int64_t)u.b * p.c.Hkv + u.h;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int col = n0 + nt * 8 + 2 * t + (c & 1), k = key + (c >> 1) * 8;
-            if (col < rows && k < hi) p.scores[(unit * p.score_rows + col) * p.score_cap + k] = s[nt][c];
-          }
+        for (int c = 0; c < 4; ++c) {
+          const int col = n0 + 2 * t + (c & 1), k = key + (c >> 1) * 8;
+          if (col < rows && k < hi) p.scores[(unit * p.score_rows + col) * p.score_cap + k] = s[c] * f[c & 1];
         }
+      }
+      const float dy[2] = {sc.y - ro[0], sc.y - ro[1]};
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        x[c] = fmaf(s[c], f[c & 1], -mu[c & 1]);
+        y[c] = fmaf(s[c], f[c & 1], dy[c & 1]);
         if constexpr (MASK) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int2 lim = row_lim[nt * 8 + 2 * t + (c & 1)];
-            const int k = key + (c >> 1) * 8;
-            if (k < lim.x || k >= lim.y) s[nt][c] = -CUDART_INF_F;
-          }
+          const int2 lim = row_lim[2 * t + (c & 1)];
+          const int k = key + (c >> 1) * 8;
+          if (k < lim.x || k >= lim.y) s[c] = x[c] = y[c] = -CUDART_INF_F;
         }
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          move |= s[nt][c] > mu[nt][c & 1] + kCaLazy || s[nt][c] + sc.y > ro[nt][c & 1] + (kCaHead + kCaLazy);
       }
+      const bool move = fmaxf(fmax3(x[0], x[1], x[2]), x[3]) > kCaLazy ||
+                        fmaxf(fmax3(y[0], y[1], y[2]), y[3]) > kCaHead + kCaLazy;
       if (__any_sync(0xffffffffu, move)) {
+        float of[2];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float of[2];
+        for (int c = 0; c < 2; ++c) {
+          float z[2];
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            float top = fmaxf(s[nt][c], s[nt][c + 2]);
+          for (int e = 0; e < 2; ++e)
+            z[e] = MASK && s[c + 2 * e] == -CUDART_INF_F ? -CUDART_INF_F : s[c + 2 * e] * f[c];
+          float top = fmaxf(z[0], z[1]);
 #pragma unroll
-            for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-            const float m1 = fmaxf(mu[nt][c], top), r1 = fmaxf(ro[nt][c], top + sc.y - kCaHead);
-            l[nt][c] *= ex2_approx(mu[nt][c] - minus_inf_as_0(m1));
-            of[c] = ex2_approx(ro[nt][c] - minus_inf_as_0(r1));
-            mu[nt][c] = m1;
-            ro[nt][c] = r1;
+          for (int e = 4; e < 32; e <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, e));
+          const float m1 = fmaxf(mu[c], top), r1 = fmaxf(ro[c], top + sc.y - kCaHead);
+          l[c] *= ex2_approx(mu[c] - m1);
+          of[c] = ex2_approx(ro[c] - r1);
+          mu[c] = m1;
+          ro[c] = r1;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            x[c + 2 * e] = z[e] - m1;
+            y[c + 2 * e] = z[e] + (sc.y - r1);
           }
-#pragma unroll
-          for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) o[m][nt][c] *= of[c & 1];
         }
-      }
-      uint32_t pb[NT][2];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float w[4];
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          l[nt][c & 1] += ex2_approx(s[nt][c] - minus_inf_as_0(mu[nt][c & 1]));
-          w[c] = ex2_approx(s[nt][c] + (sc.y - minus_inf_as_0(ro[nt][c & 1])));
-        }
-        pb[nt][0] = transpose8x8(pack2<__half>(w[0], w[1]));
-        pb[nt][1] = transpose8x8(pack2<__half>(w[2], w[3]));
+          for (int c = 0; c < 4; ++c) o[m][c] *= of[c & 1];
       }
+      float w[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        l[c & 1] += ex2_approx(x[c]);
+        w[c] = ex2_approx(y[c]);
+      }
+      const uint32_t p0 = transpose8x8(pack2<__half>(w[0], w[1])), p1 = transpose8x8(pack2<__half>(w[2], w[3]));
       uint32_t nan_seen = 0;
 #pragma unroll
       for (int j = 0; j < C::VP; ++j) {
-        uint32_t x[4][4];
+        uint32_t v[4][4];
         const int rows4[4] = {va, vb, va + 8, vb + 8};
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           if constexpr (DV == 64) {
             const uint2 a = lds64(sb + v_off(rows4[r], j));
-            x[r][0] = a.x;
-            x[r][1] = a.y;
+            v[r][0] = a.x;
+            v[r][1] = a.y;
           } else {
             const uint4 a = lds128(sb + v_off(rows4[r], j));
-            x[r][0] = a.x;
-            x[r][1] = a.y;
-            x[r][2] = a.z;
-            x[r][3] = a.w;
+            v[r][0] = a.x;
+            v[r][1] = a.y;
+            v[r][2] = a.z;
+            v[r][3] = a.w;
           }
           if constexpr (MASK) {
             // Rows that no query row sees count as 0 (stale codes may be NaN);
@@ -647,27 +659,23 @@ __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV, NT>::CTAS)
             const int k = tile * kCaKeys + rows4[r];
             const bool in = k >= lo && k < hi;
 #pragma unroll
-            for (int w = 0; w < VW; ++w) {
-              const uint32_t z = in ? x[r][w] : 0u;
+            for (int e = 0; e < VW; ++e) {
+              const uint32_t z = in ? v[r][e] : 0u;
               const uint32_t nan = ((z & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
               nan_seen |= nan;
-              x[r][w] = z & ~((nan >> 7) * 0xffu);
+              v[r][e] = z & ~((nan >> 7) * 0xffu);
             }
           }
         }
 #pragma unroll
-        for (int w = 0; w < VW; ++w) {
-          const uint32_t y0 = __byte_perm(x[0][w], x[1][w], 0x5140), y1 = __byte_perm(x[0][w], x[1][w], 0x7362);
-          const uint32_t z0 = __byte_perm(x[2][w], x[3][w], 0x5140), z1 = __byte_perm(x[2][w], x[3][w], 0x7362);
-          const int m = j * 8 + w * 2;
-          const uint32_t a0 = e4m3_to_half2(y0 & 0xffff), a1 = e4m3_to_half2(y0 >> 16);
-          const uint32_t a2 = e4m3_to_half2(z0 & 0xffff), a3 = e4m3_to_half2(z0 >> 16);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma16816(o[m][nt], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
-          const uint32_t b0 = e4m3_to_half2(y1 & 0xffff), b1 = e4m3_to_half2(y1 >> 16);
-          const uint32_t b2 = e4m3_to_half2(z1 & 0xffff), b3 = e4m3_to_half2(z1 >> 16);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma16816(o[m + 1][nt], b0, b1, b2, b3, pb[nt][0], pb[nt][1]);
+        for (int e = 0; e < VW; ++e) {
+          const uint32_t y0 = __byte_perm(v[0][e], v[1][e], 0x5140), y1 = __byte_perm(v[0][e], v[1][e], 0x7362);
+          const uint32_t z0 = __byte_perm(v[2][e], v[3][e], 0x5140), z1 = __byte_perm(v[2][e], v[3][e], 0x7362);
+          const int m = j * 8 + e * 2;
+          mma16816(o[m], e4m3_to_half2(y0 & 0xffff), e4m3_to_half2(y0 >> 16), e4m3_to_half2(z0 & 0xffff),
+                   e4m3_to_half2(z0 >> 16), p0, p1);
+          mma16816(o[m + 1], e4m3_to_half2(y1 & 0xffff), e4m3_to_half2(y1 >> 16), e4m3_to_half2(z1 & 0xffff),
+                   e4m3_to_half2(z1 >> 16), p0, p1);
         }
       }
       if constexpr (MASK) {
@@ -679,15 +687,13 @@ __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV, NT>::CTAS)
             for (int m = 0; m < MT; ++m)
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                const uint32_t code = lds8(sb + v_off(row, m >> 3) + (m & 7) * 2 + e);
+                const uint32_t code = sb[v_off(row, m >> 3) + (m & 7) * 2 + e];
                 if ((code & 0x7f) == 0x7f)
 #pragma unroll
-                  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                      const int2 lim = row_lim[nt * 8 + 2 * t + c];
-                      if (k >= lim.x && k < lim.y) o[m][nt][2 * e + c] = CUDART_NAN_F;
-                    }
+                  for (int c = 0; c < 2; ++c) {
+                    const int2 lim = row_lim[2 * t + c];
+                    if (k >= lim.x && k < lim.y) o[m][2 * e + c] = CUDART_NAN_F;
+                  }
               }
           }
         }
@@ -696,99 +702,83 @@ __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV, NT>::CTAS)
       if (lane == 0) mbar_arrive(&empty[st]);
     };
 
-    for (int tile = u.ta; tile < u.tb; ++tile, ++it) {
-      if (ok && !wait_bar(&full[it % C::STAGES], (it / C::STAGES) & 1, ctl)) ok = false;
+    const int ta = u.ta, tb = u.tb, in_lo = u.in_lo, in_hi = u.in_hi;
+    for (int tile = ta; tile < tb; ++tile) {
+      if (ok && !wait_bar(&full[st], ring, ctl)) ok = false;
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) continue;
-      if (tile * kCaKeys >= u.in_lo && (tile + 1) * kCaKeys <= u.in_hi)
+      if (tile * kCaKeys >= in_lo && (tile + 1) * kCaKeys <= in_hi)
         tile_step(MaskTag<false>(), tile);
       else
         tile_step(MaskTag<true>(), tile);
+      if (++st == C::STAGES) {
+        st = 0;
+        ring ^= 1;
+      }
     }
 
-    // ---------------------------------------------------------- end of the unit: the four warps' states into one
+    // ---------------------------------------------------------- end of the unit: four states into one
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int c = 0; c < 2; ++c) {
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-#pragma unroll
-        for (int x = 4; x < 32; x <<= 1) l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], x);
-        if (g == 0) {
-          const int r = nt * 8 + 2 * t + c;
-          st_mu[warp][r] = mu[nt][c];
-          st_l[warp][r] = l[nt][c];
-        }
+      for (int x = 4; x < 32; x <<= 1) l[c] += __shfl_xor_sync(0xffffffffu, l[c], x);
+      if (g == 0) {
+        st_mu[warp][2 * t + c] = mu[c];
+        st_l[warp][2 * t + c] = l[c];
       }
+    }
     consumers_sync();
+    float f[2];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      float f[2];
+    for (int c = 0; c < 2; ++c) {
+      const int r = 2 * t + c;
+      float top = kCaFloor, sum = 0.f;
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int r = nt * 8 + 2 * t + c;
-        float top = -CUDART_INF_F, sum = 0.f;
+      for (int w = 0; w < kCaWarps; ++w) top = fmaxf(top, st_mu[w][r]);
 #pragma unroll
-        for (int w = 0; w < kCaWarps; ++w) top = fmaxf(top, st_mu[w][r]);
-#pragma unroll
-        for (int w = 0; w < kCaWarps; ++w) sum += st_l[w][r] * ex2_approx(st_mu[w][r] - minus_inf_as_0(top));
-        // sum > 0 unless the row saw nothing; NaN stays NaN
-        f[c] = sum == 0.f ? 0.f : ex2_approx(ro[nt][c] - minus_inf_as_0(top)) / sum;
-        if (warp == 0 && g == 0) fin_l[r] = sum == 0.f ? -CUDART_INF_F : top + log2f(sum);
-      }
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) o[m][nt][c] *= f[c & 1];
+      for (int w = 0; w < kCaWarps; ++w) sum += st_l[w][r] * ex2_approx(st_mu[w][r] - top);
+      // sum > 0 unless the row saw nothing; NaN stays NaN
+      f[c] = sum == 0.f ? 0.f : ex2_approx(ro[c] - top) / sum;
+      if (warp == 0 && g == 0) fin_l[r] = sum == 0.f ? -CUDART_INF_F : top + log2f(sum);
     }
-#pragma unroll 1
-    for (int w = 0; w < kCaWarps; ++w) {
-      if (warp == w) {
+    // O into shared memory, a buffer per warp, added up on the way out.
 #pragma unroll
-        for (int m = 0; m < MT; m += 2) {
-          const int d = DV == 64 ? g * 8 + m * 2 : (m >> 3) * 128 + g * 16 + (m & 7) * 2;
+    for (int m = 0; m < MT; m += 2) {
+      const int d = DV == 64 ? g * 8 + m * 2 : (m >> 3) * 128 + g * 16 + (m & 7) * 2;
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              float4* at = reinterpret_cast<float4*>(ob + (nt * 8 + 2 * t + c) * C::OPITCH + d);
-              float4 x = make_float4(o[m][nt][c], o[m][nt][2 + c], o[m + 1][nt][c], o[m + 1][nt][2 + c]);
-              if (w) {
-                const float4 y = *at;
-                x.x += y.x;
-                x.y += y.y;
-                x.z += y.z;
-                x.w += y.w;
-              }
-              *at = x;
-            }
-        }
-      }
-      consumers_sync();
+      for (int c = 0; c < 2; ++c)
+        *reinterpret_cast<float4*>(ob + (warp * kCaRows + 2 * t + c) * C::OPITCH + d) =
+            make_float4(o[m][c] * f[c], o[m][2 + c] * f[c], o[m + 1][c] * f[c], o[m + 1][2 + c] * f[c]);
     }
-    const int live = min(C::R, rows - n0);
-    if (u.whole) {
-      for (int x = tid; x < live * (DV / 8); x += 128) {
-        const int r = x / (DV / 8), d = (x - r * (DV / 8)) * 8, y = n0 + r, i = y / p.G;
-        const float* at = ob + r * C::OPITCH + d;
-        uint32_t w[4];
+    consumers_sync();
+    const int live = min(kCaRows, rows - n0);
+    const int64_t slot = (int64_t)blockIdx.x * 2 + u.slot;
+    for (int x = tid; x < live * (DV / 4); x += kCaConsumers) {
+      const int r = x / (DV / 4), d = (x - r * (DV / 4)) * 4, z = n0 + r, i = z / p.G;
+      float4 a = *reinterpret_cast<const float4*>(ob + r * C::OPITCH + d);
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          w[e] = p.f16 ? pack2<__half>(at[2 * e], at[2 * e + 1]) : pack2<__nv_bfloat16>(at[2 * e], at[2 * e + 1]);
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + p.o_ss * (u.q0 + i) +
-                                  p.o_sh * (u.h * p.G + y - i * p.G) + d) = make_uint4(w[0], w[1], w[2], w[3]);
+      for (int w = 1; w < kCaWarps; ++w) {
+        const float4 b = *reinterpret_cast<const float4*>(ob + (w * kCaRows + r) * C::OPITCH + d);
+        a.x += b.x;
+        a.y += b.y;
+        a.z += b.z;
+        a.w += b.w;
       }
-      if (tid < live) {
-        const int y = n0 + tid, i = y / p.G;
-        p.lse[(int64_t)(u.h * p.G + y - i * p.G) * p.s.T + u.q0 + i] = fin_l[tid] * 0.69314718055994531f;
+      if (u.whole) {
+        const uint2 w = p.f16 ? make_uint2(pack2<__half>(a.x, a.y), pack2<__half>(a.z, a.w))
+                              : make_uint2(pack2<__nv_bfloat16>(a.x, a.y), pack2<__nv_bfloat16>(a.z, a.w));
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + p.o_ss * (u.q0 + i) +
+                                  p.o_sh * (u.h * p.G + z - i * p.G) + d) = w;
+      } else {
+        *reinterpret_cast<float4*>(p.part_o + (slot * kCaRows + r) * DV + d) = a;
       }
-    } else {
-      const int64_t slot = (int64_t)blockIdx.x * 2 + u.slot;
-      float* po = p.part_o + slot * C::R * DV;
-      for (int x = tid; x < live * (DV / 4); x += 128) {
-        const int r = x / (DV / 4), d = (x - r * (DV / 4)) * 4;
-        *reinterpret_cast<float4*>(po + r * DV + d) = *reinterpret_cast<const float4*>(ob + r * C::OPITCH + d);
-      }
-      if (tid < live) p.part_l[slot * C::R + tid] = fin_l[tid];
+    }
+    if (tid < live) {
+      const int z = n0 + tid, i = z / p.G;
+      if (u.whole)
+        p.lse[(int64_t)(u.h * p.G + z - i * p.G) * p.s.T + u.q0 + i] = fin_l[tid] * 0.69314718055994531f;
+      else
+        p.part_l[slot * kCaRows + tid] = fin_l[tid];
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&q_empty[qb]);
@@ -799,14 +789,15 @@ __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV, NT>::CTAS)
 // the CTAs, and writes the rows that no CTA wrote: sequences without keys, and
 // (blockIdx.y = B) rows past the last sequence. One CTA per (head, row tile) and sequence.
 constexpr int kJoinThreads = 512;
-template <int DQK, int DV, int NT>
+template <int DQK, int DV>
 __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_constant__ CacheAttnParams p, int grid) {
-  using C = CaCfg<DQK, DV, NT>;
+  using C = CaCfg<DQK, DV>;
   __shared__ int64_t sum_before[kJoinThreads / 32], sum_all[kJoinThreads / 32];
-  __shared__ float row_l[C::R];
+  __shared__ float row_l[kCaRows];
   __shared__ float4 sums[kJoinThreads];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = blockIdx.y;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   auto write8 = [&](int64_t row, int hq, int d, const float* x) {
     uint32_t w[4];
 #pragma unroll
@@ -827,10 +818,10 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
     }
     return;
   }
-  const CaSeq s = ca_seq(p, C::R, b);
+  const CaSeq s = ca_seq(p, b);
   const int h = blockIdx.x / p.row_tiles, rt = blockIdx.x % p.row_tiles;
   if (rt >= s.rt) return;
-  const int rows = s.q.m * p.G, n0 = rt * C::R, live = min(C::R, rows - n0);
+  const int rows = s.q.m * p.G, n0 = rt * kCaRows, live = min(kCaRows, rows - n0);
   if (s.kt == 0) {
     for (int x = tid; x < live * (DV / 8); x += kJoinThreads) {
       const int r = x / (DV / 8), y = n0 + r, i = y / p.G;
@@ -844,7 +835,7 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
   }
   int64_t before = 0, total = 0;
   for (int x = tid; x < p.s.B; x += kJoinThreads) {
-    const int64_t n = ca_seq(p, C::R, x).places(p.c.Hkv);
+    const int64_t n = ca_seq(p, x).places(p.c.Hkv);
     total += n;
     before += x < b ? n : 0;
   }
@@ -866,18 +857,19 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
   }
   const int parts = ca_parts(total, grid, p.min_share);
   const int64_t x0 = before + ((int64_t)h * s.rt + rt) * s.cost() + kCaUnit;  // the unit's first tile
-  const int c0 = ca_owner(total, parts, x0), c1 = ca_owner(total, parts, x0 + s.kt - 1);
+  const CaShares shares(total, parts);
+  const int c0 = shares.owner(x0), c1 = shares.owner(x0 + s.kt - 1);
   if (c0 == c1) return;  // one CTA had it all and wrote it
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int np = c1 - c0 + 1;
   auto slot = [&](int i) -> int64_t { return (int64_t)(c0 + i) * 2 + (i == 0); };
   for (int r = warp; r < live; r += kJoinThreads / 32) {
     float top = -CUDART_INF_F, sum = 0.f;
-    for (int i = lane; i < np; i += 32) top = fmaxf(top, p.part_l[slot(i) * C::R + r]);
+    for (int i = lane; i < np; i += 32) top = fmaxf(top, p.part_l[slot(i) * kCaRows + r]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     top = minus_inf_as_0(top);
-    for (int i = lane; i < np; i += 32) sum += ex2_approx(p.part_l[slot(i) * C::R + r] - top);
+    for (int i = lane; i < np; i += 32) sum += ex2_approx(p.part_l[slot(i) * kCaRows + r] - top);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (lane == 0) {
@@ -899,8 +891,8 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
     for (int k = gr; k < np; k += GROUPS) {
-      const float w = ex2_approx(p.part_l[slot(k) * C::R + r] - l);
-      const float4 a = *reinterpret_cast<const float4*>(p.part_o + (slot(k) * C::R + r) * DV + d);
+      const float w = ex2_approx(p.part_l[slot(k) * kCaRows + r] - l);
+      const float4 a = *reinterpret_cast<const float4*>(p.part_o + (slot(k) * kCaRows + r) * DV + d);
       acc.x = fmaf(a.x, w, acc.x);
       acc.y = fmaf(a.y, w, acc.y);
       acc.z = fmaf(a.z, w, acc.z);

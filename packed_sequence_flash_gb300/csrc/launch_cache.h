@@ -5,9 +5,24 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "cache.cuh"
 
 namespace psf {
+
+// Sets a kernel's dynamic shared memory limit once per device (done: a bit per device index).
+template <typename K>
+inline cudaError_t smem_limit(K kernel, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
 
 // Eviction workspace: per (sequence, head) whether it is evicted from, the kept
 // tokens in order, the ratios old / new scale of each (K, V), the new blocks'
@@ -55,9 +70,9 @@ struct CacheAttnParams {
   int* status;
   uint64_t limit_ns;
 };
-// Row tile (in units of 8 rows) and CTAs per SM that the launch uses.
-int cache_attn_nt(int Dqk, int64_t rows);
-constexpr int cache_attn_ctas(int Dqk, int nt) { return Dqk == 512 ? 1 : (nt == 1 && Dqk <= 128 ? 3 : 2); }
+constexpr int kCacheAttnRows = 8;  // query rows per tile
+// CTAs per SM: as many as shared memory and registers hold.
+constexpr int cache_attn_ctas(int Dqk) { return Dqk == 512 ? 1 : (Dqk == 192 ? 2 : 3); }
 cudaError_t launch_cache_attn(CacheAttnParams& p, int max_q, int sms, cudaStream_t st);
 
 }  // namespace psf
