@@ -25,7 +25,59 @@ import torch
 
 from . import _lib
 from ._lib import PSF_CACHE_ACCUMULATE, check
-from .attention import _cap, _DTYPES, _dtype_code, _i32, _need, _need_view, _ptr, _window, _workspace
+from .attention import _cap, _DTYPES, _ptr, _window
+
+_E4M3 = torch.float8_e4m3fn
+# The call behind torch.cuda.current_stream(index).cuda_stream, without the Stream object around it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _tensor(t, name, dtype, device):
+    """A contiguous tensor of a call, on the cache's device (an index)."""
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != device:
+        _wrong_device(t, name)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _view(t, name, dtype, device):
+    """A strided tensor whose last dim is contiguous and whose data starts on a 16-byte boundary; its address."""
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != device:
+        _wrong_device(t, name)
+    if not t.is_contiguous() and t.size(-1) > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: the last (head) dim must be contiguous")
+    ptr = t.data_ptr()
+    if ptr % 16:
+        raise ValueError(f"{name}: data must start on a 16-byte boundary")
+    return ptr
+
+
+def _wrong_device(t, name):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    raise ValueError(f"{name} must be on the cache's device, like every tensor of a call")
+
+
+def _dtype16(t, name):
+    if t.dtype not in _DTYPES:
+        raise ValueError(f"{name} must be bfloat16 or float16, got {t.dtype}")
+    return t.dtype
+
+
+def _launch(device, call, *args) -> None:
+    """call(*args, stream) with `device` current (a call's tensors may be on another than the current one)."""
+    if torch.cuda.current_device() == device:
+        rc = call(*args, _raw_stream(device))
+    else:
+        with torch.cuda.device(device):
+            rc = call(*args, _raw_stream(device))
+    if rc:
+        check(rc)
 
 
 class KVCache:
@@ -42,37 +94,33 @@ class KVCache:
                  "_struct", "_ref")
 
     def __init__(self, k, v, k_scale, v_scale, weight=None):
-        _need_view(k, "cache k", torch.float8_e4m3fn)
-        _need_view(v, "cache v", torch.float8_e4m3fn)
-        if k.dim() != 4 or v.dim() != 4 or k.shape[:3] != v.shape[:3]:
+        device = k.get_device()
+        if device < 0:
+            _wrong_device(k, "cache k")
+        kp, vp = _view(k, "cache k", _E4M3, device), _view(v, "cache v", _E4M3, device)
+        shape = k.shape
+        if len(shape) != 4 or v.shape[:3] != shape[:3] or v.dim() != 4:
             raise ValueError("cache k and v must be [num_pages, Hkv, page_size, D] with equal leading dims")
-        num_pages, Hkv, page_size, Dqk = k.shape
-        Dv = v.shape[3]
-        device = k.device
-        _cache_f32(k_scale, "k_scale", (num_pages, Hkv), device)
-        _cache_f32(v_scale, "v_scale", (num_pages, Hkv), device)
+        num_pages, Hkv, page_size, Dqk = shape
+        Dv = v.size(3)
+        _tensor(k_scale, "k_scale", torch.float32, device)
+        _tensor(v_scale, "v_scale", torch.float32, device)
+        if k_scale.shape != shape[:2] or v_scale.shape != shape[:2]:
+            raise ValueError(f"k_scale and v_scale must be {list(shape[:2])}")
         if weight is not None:
-            _cache_f32(weight, "weight", (num_pages, Hkv, page_size), device)
-        if v.device != device:
-            raise ValueError("the cache's tensors must be on one device")
+            _tensor(weight, "weight", torch.float32, device)
+            if weight.shape != shape[:3]:
+                raise ValueError(f"weight must be {list(shape[:3])}, got {list(weight.shape)}")
         self.k, self.v, self.k_scale, self.v_scale, self.weight = k, v, k_scale, v_scale, weight
         self.num_pages, self.Hkv, self.page_size, self.Dqk, self.Dv = num_pages, Hkv, page_size, Dqk, Dv
         self.device = device
-        c = _lib.KVCacheStruct(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), _ptr(weight),
-                               num_pages, page_size, Hkv, Dqk, Dv)
+        c = _lib.KVCacheStruct(kp, vp, k_scale.data_ptr(), v_scale.data_ptr(), _ptr(weight), num_pages, page_size, Hkv,
+                               Dqk, Dv)
         if not (k.is_contiguous() and v.is_contiguous()):
             c.k_strides[:] = k.stride()[:3]
             c.v_strides[:] = v.stride()[:3]
         self._struct = c
         self._ref = ctypes.byref(c)
-
-
-def _cache_f32(t, name, shape, device):
-    _need(t, name, torch.float32)
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    if t.device != device:
-        raise ValueError("the cache's tensors must be on one device")
 
 
 def kv_cache(num_pages, Hkv, Dqk, Dv, page_size=64, weights=False, device="cuda") -> KVCache:
@@ -84,45 +132,19 @@ def kv_cache(num_pages, Hkv, Dqk, Dv, page_size=64, weights=False, device="cuda"
     return KVCache(k, v, ks, torch.zeros_like(ks), w)
 
 
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-    lambda index: torch.cuda.current_stream(index).cuda_stream)
-
-
-def _launch(device, call, *args) -> None:
-    """call(*args, stream) with `device` current (a call's tensors may be on another than the current one)."""
-    index = device.index
-    before = torch.cuda.current_device()
-    if before == index:
-        rc = call(*args, _raw_stream(index))
-    else:
-        with torch.cuda.device(index):
-            rc = call(*args, _raw_stream(index))
-    if rc:
-        check(rc)
-
-
-def _sequences(cache, page_table, seq_lens, *others):
-    """(B, max_pages) of a call's sequences; `others`: further tensors that must be on the cache's device."""
-    _i32(page_table, "page_table")
-    _i32(seq_lens, "seq_lens")
-    shape = page_table.shape
-    if len(shape) != 2 or seq_lens.shape != shape[:1]:
-        raise ValueError("page_table must be [B, max_pages] and seq_lens [B]")
+def _sequences(cache, page_table, seq_lens, cu=None, name=""):
+    """(B, max_pages) of a call's sequences."""
     device = cache.device
-    if page_table.device != device or seq_lens.device != device:
-        raise ValueError("every tensor of a call must be on the cache's device")
-    for t in others:
-        if t is not None and t.device != device:
-            raise ValueError("every tensor of a call must be on the cache's device")
-    return shape
-
-
-def _cu(cu, name, B):
+    _tensor(page_table, "page_table", torch.int32, device)
+    _tensor(seq_lens, "seq_lens", torch.int32, device)
+    if page_table.dim() != 2 or seq_lens.dim() != 1 or seq_lens.size(0) != page_table.size(0):
+        raise ValueError("page_table must be [B, max_pages] and seq_lens [B]")
+    B, max_pages = page_table.shape
     if cu is not None:
-        _i32(cu, name)
-        if cu.dim() != 1 or cu.shape[0] != B + 1:
+        _tensor(cu, name, torch.int32, device)
+        if cu.dim() != 1 or cu.size(0) != B + 1:
             raise ValueError(f"{name} must be [B + 1]")
-    return cu
+    return B, max_pages
 
 
 def _thd_strides(a, b):
@@ -143,15 +165,16 @@ def kv_cache_append(cache, k, v, page_table, seq_lens, cu_new=None) -> None:
     Sequence b's new tokens are rows [cu_new[b], cu_new[b + 1]) (T / B each without cu_new) and go to its last
     positions: seq_lens (int32 [B], on the device) counts them already. See psf_kv_cache_append for the scales.
     """
-    dt = _dtype_code([(k, "k"), (v, "v")], strided=True)
+    dtype = _dtype16(k, "k")
+    kp, vp = _view(k, "k", dtype, cache.device), _view(v, "v", dtype, cache.device)
     _rows3(k, "k", cache.Hkv, cache.Dqk)
     _rows3(v, "v", cache.Hkv, cache.Dv)
-    if k.shape[0] != v.shape[0]:
+    T = k.size(0)
+    if v.size(0) != T:
         raise ValueError("k and v must have the same number of rows")
-    B, max_pages = _sequences(cache, page_table, seq_lens, k, v, cu_new)
-    _cu(cu_new, "cu_new", B)
-    _launch(cache.device, _lib.load().psf_kv_cache_append, cache._ref, k.data_ptr(), v.data_ptr(), _thd_strides(k, v),
-            dt, _ptr(cu_new), page_table.data_ptr(), seq_lens.data_ptr(), B, max_pages, k.shape[0])
+    B, max_pages = _sequences(cache, page_table, seq_lens, cu_new, "cu_new")
+    _launch(cache.device, _lib.load().psf_kv_cache_append, cache._ref, kp, vp, _thd_strides(k, v), _DTYPES[dtype],
+            _ptr(cu_new), page_table.data_ptr(), seq_lens.data_ptr(), B, max_pages, T)
 
 
 @functools.lru_cache(maxsize=256)
@@ -160,7 +183,7 @@ def _attn_workspace(*sizes) -> int:
 
 
 def attn_cache_workspace_size(cache, B, max_pages, Hq, max_q=1, accumulate=False) -> int:
-    return _attn_workspace(int(B), int(max_pages), cache.page_size, int(Hq), cache.Hkv, cache.Dqk, cache.Dv, int(max_q),
+    return _attn_workspace(B, max_pages, cache.page_size, Hq, cache.Hkv, cache.Dqk, cache.Dv, max_q,
                            PSF_CACHE_ACCUMULATE if accumulate else 0)
 
 
@@ -174,38 +197,40 @@ def attn_cache_fwd(q, cache, page_table, seq_lens, scale, cu_q=None, max_q=None,
     accumulate: add every token's attention weight, over the rows and the heads of its KV head, to cache.weight.
     Long prompt chunks run faster through ``kv_cache_gather`` and ``attn_varlen_fwd``.
     """
-    if q.dtype not in _DTYPES:
-        raise ValueError(f"q must be bfloat16 or float16, got {q.dtype}")
-    _need_view(q, "q")
-    if q.dim() != 3 or q.shape[2] != cache.Dqk:
+    dtype, device = _dtype16(q, "q"), cache.device
+    qp = _view(q, "q", dtype, device)
+    if q.dim() != 3 or q.size(2) != cache.Dqk:
         raise ValueError(f"q must be [T, Hq, {cache.Dqk}], got {list(q.shape)}")
     T, Hq, _ = q.shape
-    B, max_pages = _sequences(cache, page_table, seq_lens, q, cu_q, out, lse, workspace)
-    _cu(cu_q, "cu_q", B)
+    B, max_pages = _sequences(cache, page_table, seq_lens, cu_q, "cu_q")
     if max_q is None:
         if cu_q is not None:
             raise ValueError("cu_q needs max_q, the most query rows of a sequence")
         max_q = T // B if B else 0
     if out is None:
-        out = torch.empty((T, Hq, cache.Dv), dtype=q.dtype, device=q.device)
+        out = torch.empty((T, Hq, cache.Dv), dtype=dtype, device=q.device)
+        op = out.data_ptr()
     else:
-        _need_view(out, "out", q.dtype)
+        op = _view(out, "out", dtype, device)
         _rows3(out, "out", Hq, cache.Dv)
-        if out.shape[0] != T:
+        if out.size(0) != T:
             raise ValueError("out must have q's rows")
     if lse is None:
-        lse = torch.empty(Hq, T, dtype=torch.float32, device=q.device)
+        lse = torch.empty((Hq, T), dtype=torch.float32, device=q.device)
     else:
-        _need(lse, "lse", torch.float32)
-        if tuple(lse.shape) != (Hq, T):
+        _tensor(lse, "lse", torch.float32, device)
+        if lse.shape != (Hq, T):
             raise ValueError(f"lse must be [{Hq}, {T}], got {list(lse.shape)}")
     if workspace is None:
-        workspace = _workspace(attn_cache_workspace_size(cache, B, max_pages, Hq, max_q, accumulate), q.device)
-    _launch(cache.device, _lib.load().psf_attn_cache_fwd, q.data_ptr(), cache._ref, out.data_ptr(), lse.data_ptr(),
-            _ptr(cu_q), page_table.data_ptr(), seq_lens.data_ptr(), B, max_pages, T, int(max_q), Hq,
-            _thd_strides(q, out), _DTYPES[q.dtype], float(scale), int(bool(causal)), _window(window), _cap(softcap),
-            PSF_CACHE_ACCUMULATE if accumulate else 0, workspace.data_ptr(),
-            workspace.numel() * workspace.element_size())
+        size = attn_cache_workspace_size(cache, B, max_pages, Hq, max_q, accumulate)
+        workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
+    else:
+        _tensor(workspace, "workspace", workspace.dtype, device)
+        size = workspace.numel() * workspace.element_size()
+    _launch(device, _lib.load().psf_attn_cache_fwd, qp, cache._ref, op, lse.data_ptr(), _ptr(cu_q),
+            page_table.data_ptr(), seq_lens.data_ptr(), B, max_pages, T, max_q, Hq, _thd_strides(q, out),
+            _DTYPES[dtype], scale, 1 if causal else 0, _window(window), _cap(softcap),
+            PSF_CACHE_ACCUMULATE if accumulate else 0, workspace.data_ptr(), size)
     return out, lse
 
 
@@ -215,7 +240,7 @@ def _evict_workspace(*sizes) -> int:
 
 
 def kv_cache_evict_workspace_size(cache, B, max_pages, budget) -> int:
-    return _evict_workspace(int(B), int(max_pages), cache.page_size, cache.Hkv, int(budget))
+    return _evict_workspace(B, max_pages, cache.page_size, cache.Hkv, budget)
 
 
 def kv_cache_evict(cache, page_table, seq_lens, budget, recent, new_lens=None, workspace=None):
@@ -225,18 +250,21 @@ def kv_cache_evict(cache, page_table, seq_lens, budget, recent, new_lens=None, w
     accumulated weight (of equal ones the earliest), in their order. Pages past ceil(budget / page_size) are free
     afterwards. See psf_kv_cache_evict for the scales.
     """
-    B, max_pages = _sequences(cache, page_table, seq_lens, new_lens, workspace)
+    B, max_pages = _sequences(cache, page_table, seq_lens)
     if new_lens is None:
-        new_lens = torch.empty(B, dtype=torch.int32, device=seq_lens.device)
+        new_lens = torch.empty_like(seq_lens)
     else:
-        _i32(new_lens, "new_lens")
-        if tuple(new_lens.shape) != (B,):
+        _tensor(new_lens, "new_lens", torch.int32, cache.device)
+        if new_lens.shape != (B,):
             raise ValueError("new_lens must be [B]")
     if workspace is None:
-        workspace = _workspace(kv_cache_evict_workspace_size(cache, B, max_pages, budget), seq_lens.device)
+        size = kv_cache_evict_workspace_size(cache, B, max_pages, budget)
+        workspace = torch.empty(size, dtype=torch.uint8, device=seq_lens.device)
+    else:
+        _tensor(workspace, "workspace", workspace.dtype, cache.device)
+        size = workspace.numel() * workspace.element_size()
     _launch(cache.device, _lib.load().psf_kv_cache_evict, cache._ref, page_table.data_ptr(), seq_lens.data_ptr(),
-            new_lens.data_ptr(), B, max_pages, int(budget), int(recent), workspace.data_ptr(),
-            workspace.numel() * workspace.element_size())
+            new_lens.data_ptr(), B, max_pages, budget, recent, workspace.data_ptr(), size)
     return new_lens
 
 
@@ -248,11 +276,13 @@ def kv_cache_gather(cache, page_table, seq_lens, total_k, dtype=torch.bfloat16):
     """
     if dtype not in _DTYPES:
         raise ValueError(f"dtype must be bfloat16 or float16, got {dtype}")
+    if total_k < 0:
+        raise ValueError("total_k must not be negative")
     B, max_pages = _sequences(cache, page_table, seq_lens)
     dev = seq_lens.device
-    k = torch.empty(int(total_k), cache.Hkv, cache.Dqk, dtype=dtype, device=dev)
-    v = torch.empty(int(total_k), cache.Hkv, cache.Dv, dtype=dtype, device=dev)
+    k = torch.empty((total_k, cache.Hkv, cache.Dqk), dtype=dtype, device=dev)
+    v = torch.empty((total_k, cache.Hkv, cache.Dv), dtype=dtype, device=dev)
     cu_k = torch.empty(B + 1, dtype=torch.int32, device=dev)
     _launch(cache.device, _lib.load().psf_kv_cache_gather, cache._ref, page_table.data_ptr(), seq_lens.data_ptr(), B,
-            max_pages, k.data_ptr(), v.data_ptr(), cu_k.data_ptr(), int(total_k), _DTYPES[dtype])
+            max_pages, k.data_ptr(), v.data_ptr(), cu_k.data_ptr(), total_k, _DTYPES[dtype])
     return k, v, cu_k

@@ -709,10 +709,8 @@ size_t evict_ws_layout(int B, int max_pages, int page_size, int Hkv, int budget,
   size_t off = 0;
   const size_t live = off;
   off += align256(sizeof(int) * (size_t)units);
-  const size_t src = off;
-  off += align256(sizeof(int32_t) * (size_t)(units * kept));
-  const size_t ratio = off;
-  off += align256(sizeof(float2) * (size_t)(units * kept));
+  const size_t items = off;
+  off += align256(sizeof(int4) * (size_t)(units * kept));
   const size_t scale = off;
   off += align256(sizeof(float2) * (size_t)(units * blocks));
   const size_t keys = off;
@@ -720,8 +718,7 @@ size_t evict_ws_layout(int B, int max_pages, int page_size, int Hkv, int budget,
   if (w && base) {
     char* b = static_cast<char*>(base);
     w->live = reinterpret_cast<int*>(b + live);
-    w->src = reinterpret_cast<int32_t*>(b + src);
-    w->ratio = reinterpret_cast<float2*>(b + ratio);
+    w->items = reinterpret_cast<int4*>(b + items);
     w->scale = reinterpret_cast<float2*>(b + scale);
     w->keys = reinterpret_cast<uint32_t*>(b + keys);
     w->cap = cap;

@@ -12,11 +12,16 @@ namespace {
 // ---------------------------------------------------------------- append
 // One CTA per (sequence, page it enters, head, K or V): the largest new
 // magnitude, the block's scale, the older codes of the page if the scale grew,
-// the new codes. Sequence b's pages are tasks start(b) .. in an index space that
+// the new codes. Bound by memory: 2 bytes read and 1 written per element. The
+// largest magnitude is taken on packed 16-bit patterns (their order without the
+// sign is that of the values) and codes are made with a product by the scale's
+// reciprocal, exact for a power of two: with a division and a test of every
+// element for being finite 16 Ki prompt tokens took 30 us. Sequence b's pages are tasks start(b) .. in an index space that
 // leaves floor(cu / page) + 2 b tasks before it, room enough for the
 // floor((n - 2) / page) + 2 pages that n rows can touch, so a CTA finds its
 // page from cu alone.
 constexpr int kAppendThreads = 128;
+constexpr float kMaxFloat = 3.402823466e38f;
 constexpr int kAppendHeld = 8;  // 16-byte vectors a thread keeps between its two looks at the rows
 
 template <typename T>
@@ -27,6 +32,7 @@ __global__ void __launch_bounds__(kAppendThreads)
   const int tid = threadIdx.x, h = blockIdx.y;
   const bool is_v = blockIdx.z;
   auto start = [&](int b) -> int64_t { return (s.cu ? s.cu[b] : b * s.each) / c.page + 2 * (int64_t)b; };
+  after_previous_kernel();
   const int b = warp_find(s.B, blockIdx.x, start);
   const Seq q = seq_at(s, c.page, b);
   if (q.bad || q.m > q.n) {
@@ -57,16 +63,10 @@ __global__ void __launch_bounds__(kAppendThreads)
   auto row_of = [&](int i) { return D == 192 ? i / 24 : i >> lg; };
 
   uint4 held[kAppendHeld];
-  float top = 0.f;
+  uint32_t most = 0;  // largest patterns without sign, of the low and of the high halves
   auto look = [&](const uint4& x) {
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 f = unpack2<T>(w[j]);
-      const float a = fabsf(f.x), d = fabsf(f.y);
-      top = fmaxf(top, a <= 3.402823466e38f ? a : 0.f);
-      top = fmaxf(top, d <= 3.402823466e38f ? d : 0.f);
-    }
+    most = __vmaxu2(most, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
+                                   __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
   };
   auto load = [&](int i) {
     const int r = row_of(i);
@@ -80,6 +80,22 @@ __global__ void __launch_bounds__(kAppendThreads)
 #pragma unroll
   for (int u = 0; u < kAppendHeld; ++u) look(held[u]);
   for (int i = kAppendHeld * kAppendThreads + tid; i < items; i += kAppendThreads) look(load(i));
+  const float2 pair = unpack2<T>(most);
+  const bool odd = __syncthreads_or(!(pair.x <= kMaxFloat) || !(pair.y <= kMaxFloat));  // inf or NaN among the rows
+  float top = fmaxf(pair.x, pair.y);
+  if (odd) {  // once more, over the finite values alone
+    top = 0.f;
+    for (int i = tid; i < items; i += kAppendThreads) {
+      const uint4 x = load(i);
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 f = unpack2<T>(w[j]);
+        if (fabsf(f.x) <= kMaxFloat) top = fmaxf(top, fabsf(f.x));
+        if (fabsf(f.y) <= kMaxFloat) top = fmaxf(top, fabsf(f.y));
+      }
+    }
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   if ((tid & 31) == 0) warp_top[tid >> 5] = top;
@@ -104,6 +120,9 @@ __global__ void __launch_bounds__(kAppendThreads)
       *at = x;
     }
   }
+  // A scale that the append chose is a power of two; one that was there may not be.
+  const bool plain = !odd && (__float_as_int(scale) & 0x7fffff) == 0 && scale > 0.f;
+  const float inv = 1.f / scale;
   auto put = [&](int i, const uint4& x) {
     const int row = row_of(i);
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
@@ -111,7 +130,8 @@ __global__ void __launch_bounds__(kAppendThreads)
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const float2 f = unpack2<T>(w[j]);
-      e[j] = e4m3_pair(finite_or_nan(f.x) / scale, finite_or_nan(f.y) / scale);
+      e[j] = plain ? e4m3_pair(f.x * inv, f.y * inv)
+                   : e4m3_pair(finite_or_nan(f.x) / scale, finite_or_nan(f.y) / scale);
     }
     *reinterpret_cast<uint2*>(out + sr * (r0 + row) + (i - row * vecs) * 8) =
         make_uint2(e[0] | (e[1] << 16), e[2] | (e[3] << 16));
@@ -133,6 +153,7 @@ __global__ void __launch_bounds__(kPrefixThreads)
     gather_prefix_kernel(SeqView s, int page, int32_t* cu_k, int64_t total_k, int* status) {
   __shared__ int64_t tot[32];
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  after_previous_kernel();
   int64_t carry = 0;
   for (int base = 0; base < s.B; base += kPrefixThreads) {
     const int b = base + tid;
@@ -177,6 +198,7 @@ __global__ void __launch_bounds__(kGatherThreads)
   const int tid = threadIdx.x, h = blockIdx.y;
   const bool is_v = blockIdx.z;
   auto start = [&](int b) -> int64_t { return cu_k[b] / c.page + (int64_t)b; };
+  after_previous_kernel();
   const int b = warp_find(s.B, blockIdx.x, start);
   const int64_t pi = (int64_t)blockIdx.x - start(b);
   const int row0 = cu_k[b], n = cu_k[b + 1] - row0;
@@ -219,6 +241,10 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
+__device__ __forceinline__ float key_weight(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? k & 0x7fffffffu : ~k);
+}
+
 constexpr int kSelectThreads = 1024;
 
 // Exclusive block-wide prefix sum.
@@ -232,8 +258,7 @@ __device__ int select_scan(int v, int* warp_tot) {
   }
   if (lane == 31) warp_tot[wid] = x;
   __syncthreads();
-  int before = 0;
-  for (int w = 0; w < wid; ++w) before += warp_tot[w];
+  const int before = __reduce_add_sync(0xffffffffu, lane < wid ? warp_tot[lane] : 0);
   __syncthreads();
   return before + x - v;
 }
@@ -241,43 +266,45 @@ __device__ int select_scan(int v, int* warp_tot) {
 // One CTA per (head, sequence). The smallest kept weight is found bit by bit
 // over the integer keys (two bits a step, counted in parallel: no atomics, no
 // order), then the kept tokens are listed in their order, the new blocks'
-// scales set and the weights moved. Keys live in shared memory when they fit,
-// else in the workspace.
+// scales set and the weights written. Latency bounds it: a few passes over one
+// head's weights, which stay in shared memory (in the workspace when they are too many).
 __global__ void __launch_bounds__(kSelectThreads)
     evict_select_kernel(CacheView c, SeqView s, int budget, int recent, int32_t* new_lens, EvictWorkspace ws,
                         int smem_keys, int* status) {
   extern __shared__ uint32_t key_smem[];
-  __shared__ int warp_tot[32], cnt[3][32], bad_page;
+  __shared__ int warp_tot[32], cnt[2][3][32];
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   const int h = blockIdx.x, b = blockIdx.y;
+  after_previous_kernel();
   const int n = s.lens[b];
   const int32_t* table = s.table + (int64_t)b * s.max_pages;
   const int64_t unit = (int64_t)b * c.Hkv + h;
-  if (tid == 0) bad_page = n < 0 || (int64_t)n > (int64_t)s.max_pages * c.page;
-  __syncthreads();
-  if (!bad_page && n > budget)
-    for (int i = tid; i < (n + c.page - 1) >> c.page_lg; i += kSelectThreads)
-      if (table[i] < 0 || table[i] >= c.pages) bad_page = 1;
-  __syncthreads();
-  const bool skip = bad_page || n <= budget;
+  bool bad = n < 0 || (int64_t)n > (int64_t)s.max_pages * c.page;
+  if (!bad && n > budget)
+    for (int i = tid; i < (n + c.page - 1) >> c.page_lg; i += kSelectThreads) bad |= table[i] < 0 || table[i] >= c.pages;
+  bad = __syncthreads_or(bad);
+  const bool skip = bad || n <= budget;
   if (tid == 0) {
-    if (bad_page) record_status(status, kStatusDeviceArgs);
+    if (bad) record_status(status, kStatusDeviceArgs);
     if (h == 0) new_lens[b] = skip ? n : budget;
     ws.live[unit] = skip ? 0 : 1;
   }
   if (skip) return;
 
   const int old = n - recent, need = budget - recent;
-  uint32_t* keys = old <= smem_keys ? key_smem : ws.keys + unit * ws.cap;
+  uint32_t* keys = n <= smem_keys ? key_smem : ws.keys + unit * ws.cap;
   auto weight_at = [&](int j) -> float* {
     return c.weight + ((int64_t)table[j >> c.page_lg] * c.Hkv + h) * c.page + (j & (c.page - 1));
   };
-  for (int j = tid; j < old; j += kSelectThreads) keys[j] = weight_key(*weight_at(j));
+#pragma unroll 4
+  for (int j = tid; j < n; j += kSelectThreads) keys[j] = weight_key(*weight_at(j));
   __syncthreads();
   uint32_t thr = 0;
-  for (int bit = 30; bit >= 0; bit -= 2) {
+  int flip = 0;
+  for (int bit = 30; bit >= 0; bit -= 2, flip ^= 1) {
     const uint32_t one = 1u << bit;
     int n1 = 0, n2 = 0, n3 = 0;
+#pragma unroll 4
     for (int j = tid; j < old; j += kSelectThreads) {
       const uint32_t k = keys[j];
       n1 += k >= thr + one;
@@ -288,16 +315,15 @@ __global__ void __launch_bounds__(kSelectThreads)
     n2 = __reduce_add_sync(0xffffffffu, n2);
     n3 = __reduce_add_sync(0xffffffffu, n3);
     if (lane == 0) {
-      cnt[0][wid] = n1;
-      cnt[1][wid] = n2;
-      cnt[2][wid] = n3;
+      cnt[flip][0][wid] = n1;
+      cnt[flip][1][wid] = n2;
+      cnt[flip][2][wid] = n3;
     }
-    __syncthreads();
-    n1 = __reduce_add_sync(0xffffffffu, cnt[0][lane]);
-    n2 = __reduce_add_sync(0xffffffffu, cnt[1][lane]);
-    n3 = __reduce_add_sync(0xffffffffu, cnt[2][lane]);
+    __syncthreads();  // one a step: the next step counts in the other buffer
+    n1 = __reduce_add_sync(0xffffffffu, cnt[flip][0][lane]);
+    n2 = __reduce_add_sync(0xffffffffu, cnt[flip][1][lane]);
+    n3 = __reduce_add_sync(0xffffffffu, cnt[flip][2][lane]);
     thr += n3 >= need ? 3 * one : (n2 >= need ? 2 * one : (n1 >= need ? one : 0));
-    __syncthreads();
   }
   // Thread t lists tokens [t per, (t + 1) per); an odd `per` spreads the shared-memory reads.
   const int per = ((n + kSelectThreads - 1) / kSelectThreads) | 1;
@@ -308,122 +334,133 @@ __global__ void __launch_bounds__(kSelectThreads)
     equal += keys[j] == thr;
   }
   int all_above = __reduce_add_sync(0xffffffffu, above);
-  if (lane == 0) cnt[0][wid] = all_above;
+  if (lane == 0) cnt[flip][0][wid] = all_above;
   __syncthreads();
-  all_above = __reduce_add_sync(0xffffffffu, cnt[0][lane]);
+  all_above = __reduce_add_sync(0xffffffffu, cnt[flip][0][lane]);
   const int quota = need - all_above;  // tokens with exactly the smallest kept weight: the first ones
   const int eq_before = select_scan(equal, warp_tot);
   const int eq_kept = min(max(quota - eq_before, 0), equal);
   const int mine = above + eq_kept + max(j1 - max(j0, old), 0);
   int at = select_scan(mine, warp_tot);
-  int32_t* src = ws.src + unit * budget;
+  int4* items = ws.items + unit * budget;
   for (int j = j0, left = eq_kept; j < j1; ++j) {
     bool keep = j >= old || keys[j] > thr;
     if (!keep && keys[j] == thr && left > 0) {
       keep = true;
       --left;
     }
-    if (keep) src[at++] = j;
+    if (keep) items[at++].x = j;
   }
   __syncthreads();
 
-  // New blocks: a warp each. scale = the largest of its tokens' scales; the
-  // ratios go to the kernel that moves the codes.
+  // Blocks: a warp takes 128 kept tokens, four per lane. A new block's scale is
+  // the largest of its tokens' scales; where each token comes from and the
+  // ratios of the scales go to the kernel that moves the codes.
   const int blocks = (budget + c.page - 1) >> c.page_lg;
-  for (int blk = wid; blk < blocks; blk += kSelectThreads / 32) {
-    float sk[4], sv[4], tk = 0.f, tv = 0.f;
+  for (int base = wid * 128; base < budget; base += kSelectThreads / 32 * 128) {
+    int from[4], pg[4];
+    float sk[4], sv[4], tk[4], tv[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const int r = u * 32 + lane, j = (blk << c.page_lg) + r;
-      sk[u] = sv[u] = 0.f;
-      if (r < c.page && j < budget) {
-        const int64_t a = (int64_t)table[src[j] >> c.page_lg] * c.Hkv + h;
-        sk[u] = c.k_scale[a];
-        sv[u] = c.v_scale[a];
+      const int j = base + u * 32 + lane;
+      from[u] = j < budget ? items[j].x : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) pg[u] = from[u] >= 0 ? table[from[u] >> c.page_lg] : 0;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int64_t a = (int64_t)pg[u] * c.Hkv + h;
+      tk[u] = sk[u] = from[u] >= 0 ? c.k_scale[a] : 0.f;
+      tv[u] = sv[u] = from[u] >= 0 ? c.v_scale[a] : 0.f;
+    }
+    const int width = min(c.page, 32);
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      for (int o = 1; o < width; o <<= 1) {
+        tk[u] = fmaxf(tk[u], __shfl_xor_sync(0xffffffffu, tk[u], o));
+        tv[u] = fmaxf(tv[u], __shfl_xor_sync(0xffffffffu, tv[u], o));
       }
-      tk = fmaxf(tk, sk[u]);
-      tv = fmaxf(tv, sv[u]);
+    if (c.page >= 64) {
+      tk[0] = tk[1] = fmaxf(tk[0], tk[1]);
+      tk[2] = tk[3] = fmaxf(tk[2], tk[3]);
+      tv[0] = tv[1] = fmaxf(tv[0], tv[1]);
+      tv[2] = tv[3] = fmaxf(tv[2], tv[3]);
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      tk = fmaxf(tk, __shfl_xor_sync(0xffffffffu, tk, o));
-      tv = fmaxf(tv, __shfl_xor_sync(0xffffffffu, tv, o));
+    if (c.page == 128) {
+      tk[0] = tk[1] = tk[2] = tk[3] = fmaxf(tk[0], tk[2]);
+      tv[0] = tv[1] = tv[2] = tv[3] = fmaxf(tv[0], tv[2]);
     }
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const int r = u * 32 + lane, j = (blk << c.page_lg) + r;
-      if (r < c.page && j < budget)
-        ws.ratio[unit * budget + j] = make_float2(tk > 0.f ? sk[u] / tk : 1.f, tv > 0.f ? sv[u] / tv : 1.f);
+      const int j = base + u * 32 + lane;
+      if (j < budget) {
+        const float rk = tk[u] > 0.f ? sk[u] / tk[u] : 1.f, rv = tv[u] > 0.f ? sv[u] / tv[u] : 1.f;
+        items[j] = make_int4(pg[u], from[u] & (c.page - 1), __float_as_int(rk), __float_as_int(rv));
+        *weight_at(j) = key_weight(keys[from[u]]);
+        if ((j & (c.page - 1)) == 0) ws.scale[unit * blocks + (j >> c.page_lg)] = make_float2(tk[u], tv[u]);
+      }
     }
-    if (lane == 0) ws.scale[unit * blocks + blk] = make_float2(tk, tv);
   }
-  __syncthreads();
+  __syncthreads();  // every old scale has been read
   for (int blk = tid; blk < blocks; blk += kSelectThreads) {
     const float2 t = ws.scale[unit * blocks + blk];
     const int64_t a = (int64_t)table[blk] * c.Hkv + h;
     c.k_scale[a] = t.x;
     c.v_scale[a] = t.y;
   }
-  // Weights, a batch at a time: a token never moves up, so a batch's writes
-  // touch nothing that a later batch still has to read.
-  for (int base = 0; base < budget; base += kSelectThreads) {
-    const int j = base + tid;
-    const float w = j < budget ? *weight_at(src[j]) : 0.f;
-    __syncthreads();
-    if (j < budget) *weight_at(j) = w;
-  }
 }
 
 // Moves the codes: one CTA per (head, sequence, K or V, column slice), the kept
-// tokens in order and in batches (as for the weights: read a batch, wait, write
-// it). Slices of a row go to CTAs of their own when (head, sequence) pairs alone
-// would not fill the device.
+// tokens in order and in batches. A token never moves up, so a batch's writes
+// touch nothing that a later batch still has to read: read a batch, wait, write
+// it. Slices of a row go to CTAs of their own when (head, sequence) pairs alone
+// would not fill the device. Bound by memory: every kept code is read and written once.
 constexpr int kMoveThreads = 256;
-constexpr int kMoveVecs = 4;
-__global__ void __launch_bounds__(kMoveThreads)
+constexpr int kMoveVecs = 8;
+__global__ void __launch_bounds__(kMoveThreads, 3)
     evict_move_kernel(CacheView c, SeqView s, int budget, EvictWorkspace ws, int slices) {
   const int tid = threadIdx.x, h = blockIdx.x, b = blockIdx.y;
   const bool is_v = blockIdx.z & 1;
   const int slice = blockIdx.z >> 1;
   const int64_t unit = (int64_t)b * c.Hkv + h;
-  if (!ws.live[unit]) return;
   const int D = is_v ? c.Dv : c.Dqk;
   const int vecs = (D >> 4) / slices;  // 16-byte vectors of this CTA's part of a row
-  const int col = slice * vecs * 16;
   const int32_t* table = s.table + (int64_t)b * s.max_pages;
-  uint8_t* base = (is_v ? c.v + c.v_sh * h : c.k + c.k_sh * h) + col;
+  uint8_t* base = (is_v ? c.v + c.v_sh * h : c.k + c.k_sh * h) + slice * vecs * 16;
   const int64_t sp = is_v ? c.v_sp : c.k_sp, sr = is_v ? c.v_sr : c.k_sr;
-  const int32_t* src = ws.src + unit * budget;
-  const float2* ratio = ws.ratio + unit * budget;
-  const int64_t items = (int64_t)budget * vecs;
-  auto at = [&](int j, int v) {
-    return reinterpret_cast<uint4*>(base + sp * table[j >> c.page_lg] + sr * (j & (c.page - 1)) + v * 16);
-  };
-  for (int64_t i0 = 0; i0 < items; i0 += kMoveThreads * kMoveVecs) {
+  const int4* items = ws.items + unit * budget;
+  after_previous_kernel();
+  if (!ws.live[unit]) return;
+  const int64_t total = (int64_t)budget * vecs;
+  const int lg = (vecs & (vecs - 1)) == 0 ? 31 - __clz(vecs) : -1;
+  auto row_of = [&](int64_t i) { return lg >= 0 ? (int)(i >> lg) : (int)(i / vecs); };
+  for (int64_t i0 = 0; i0 < total; i0 += kMoveThreads * kMoveVecs) {
     uint4 x[kMoveVecs];
     float r[kMoveVecs];
 #pragma unroll
     for (int u = 0; u < kMoveVecs; ++u) {
       const int64_t i = i0 + u * kMoveThreads + tid;
-      if (i < items) {
-        const int j = (int)(i / vecs), v = (int)(i - (int64_t)j * vecs);
-        x[u] = *at(src[j], v);
-        r[u] = is_v ? ratio[j].y : ratio[j].x;
+      r[u] = 1.f;
+      if (i < total) {
+        const int j = row_of(i), v = (int)(i - (int64_t)j * vecs);
+        const int4 from = items[j];
+        r[u] = __int_as_float(is_v ? from.w : from.z);
+        x[u] = *reinterpret_cast<const uint4*>(base + sp * from.x + sr * from.y + v * 16);
       }
     }
     __syncthreads();
 #pragma unroll
     for (int u = 0; u < kMoveVecs; ++u) {
       const int64_t i = i0 + u * kMoveThreads + tid;
-      if (i < items) {
-        const int j = (int)(i / vecs), v = (int)(i - (int64_t)j * vecs);
+      if (i < total) {
+        const int j = row_of(i), v = (int)(i - (int64_t)j * vecs);
         if (r[u] != 1.f) {
           x[u].x = rescale4(x[u].x, r[u]);
           x[u].y = rescale4(x[u].y, r[u]);
           x[u].z = rescale4(x[u].z, r[u]);
           x[u].w = rescale4(x[u].w, r[u]);
         }
-        *at(j, v) = x[u];
+        *reinterpret_cast<uint4*>(base + sp * table[j >> c.page_lg] + sr * (j & (c.page - 1)) + v * 16) = x[u];
       }
     }
   }
@@ -435,43 +472,39 @@ cudaError_t launch_cache_append(const CacheView& c, const SeqView& s, const void
                                 const void* v, int64_t v_ss, int64_t v_sh, int f16, int* status, cudaStream_t st) {
   const dim3 grid((unsigned)(s.T / c.page + 2 * (int64_t)s.B), c.Hkv, 2);
   if (f16)
-    append_kernel<__half><<<grid, kAppendThreads, 0, st>>>(c, s, static_cast<const __half*>(k), k_ss, k_sh,
-                                                          static_cast<const __half*>(v), v_ss, v_sh, status);
-  else
-    append_kernel<__nv_bfloat16><<<grid, kAppendThreads, 0, st>>>(c, s, static_cast<const __nv_bfloat16*>(k), k_ss,
-                                                                 k_sh, static_cast<const __nv_bfloat16*>(v), v_ss,
-                                                                 v_sh, status);
-  return cudaGetLastError();
+    return launch_early(append_kernel<__half>, grid, kAppendThreads, 0, st, c, s, static_cast<const __half*>(k), k_ss,
+                        k_sh, static_cast<const __half*>(v), v_ss, v_sh, status);
+  return launch_early(append_kernel<__nv_bfloat16>, grid, kAppendThreads, 0, st, c, s,
+                      static_cast<const __nv_bfloat16*>(k), k_ss, k_sh, static_cast<const __nv_bfloat16*>(v), v_ss,
+                      v_sh, status);
 }
 
 cudaError_t launch_cache_gather(const CacheView& c, const SeqView& s, void* k, void* v, int32_t* cu_k,
                                 int64_t total_k, int f16, int* status, cudaStream_t st) {
-  gather_prefix_kernel<<<1, kPrefixThreads, 0, st>>>(s, c.page, cu_k, total_k, status);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = launch_early(gather_prefix_kernel, dim3(1), kPrefixThreads, 0, st, s, c.page, cu_k, total_k, status);
   if (e != cudaSuccess || total_k == 0) return e;
   const dim3 grid((unsigned)(total_k / c.page + s.B), c.Hkv, 2);
   if (f16)
-    gather_kernel<__half><<<grid, kGatherThreads, 0, st>>>(c, s, cu_k, static_cast<__half*>(k),
-                                                          static_cast<__half*>(v), total_k, status);
-  else
-    gather_kernel<__nv_bfloat16><<<grid, kGatherThreads, 0, st>>>(c, s, cu_k, static_cast<__nv_bfloat16*>(k),
-                                                                 static_cast<__nv_bfloat16*>(v), total_k, status);
-  return cudaGetLastError();
+    return launch_early(gather_kernel<__half>, grid, kGatherThreads, 0, st, c, s, (const int32_t*)cu_k,
+                        static_cast<__half*>(k), static_cast<__half*>(v), total_k, status);
+  return launch_early(gather_kernel<__nv_bfloat16>, grid, kGatherThreads, 0, st, c, s, (const int32_t*)cu_k,
+                      static_cast<__nv_bfloat16*>(k), static_cast<__nv_bfloat16*>(v), total_k, status);
 }
 
 cudaError_t launch_cache_evict(const CacheView& c, const SeqView& s, int budget, int recent, int32_t* new_lens,
                                const EvictWorkspace& ws, int sms, int* status, cudaStream_t st) {
-  const int smem_keys = (int)min(ws.cap, (int64_t)kEvictSmemKeys);
-  const int smem = smem_keys * 4;
   static std::atomic<uint64_t> smem_set{0};
   cudaError_t e = smem_limit(evict_select_kernel, kEvictSmemKeys * 4, smem_set);
   if (e != cudaSuccess) return e;
-  evict_select_kernel<<<dim3(c.Hkv, s.B), kSelectThreads, smem, st>>>(c, s, budget, recent, new_lens, ws, smem_keys,
-                                                                     status);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  const int slices = 1;
-  evict_move_kernel<<<dim3(c.Hkv, s.B, 2 * slices), kMoveThreads, 0, st>>>(c, s, budget, ws, slices);
-  return cudaGetLastError();
+  const int smem_keys = (int)(ws.cap < kEvictSmemKeys ? ws.cap : kEvictSmemKeys);
+  e = launch_early(evict_select_kernel, dim3(c.Hkv, s.B), kSelectThreads, smem_keys * 4, st, c, s, budget, recent,
+                   new_lens, ws, smem_keys, status);
+  if (e != cudaSuccess) return e;
+  // Two CTAs per SM if the rows can be cut that far: parts of 32 bytes (a memory sector) or more.
+  const int least = (c.Dqk < c.Dv ? c.Dqk : c.Dv) / 32;
+  int slices = 1;
+  while (slices * 2 <= least && slices < 4 && (int64_t)c.Hkv * s.B * 2 * slices < 2 * sms) slices *= 2;
+  return launch_early(evict_move_kernel, dim3(c.Hkv, s.B, 2 * slices), kMoveThreads, 0, st, c, s, budget, ws, slices);
 }
 
 }  // namespace psf

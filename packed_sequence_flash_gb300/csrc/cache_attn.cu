@@ -32,23 +32,6 @@ __global__ void __launch_bounds__(kWeightThreads) cache_weight_kernel(const __gr
   atomicAdd(c.weight + ((int64_t)pg * c.Hkv + h) * c.page + (j & (c.page - 1)), sum);
 }
 
-// A launch that may begin while the kernel before it in the stream still runs
-// (its kernel waits with griddepcontrol.wait before it reads what that one writes).
-template <typename... A>
-cudaError_t launch_early(void (*kernel)(A...), dim3 grid, int threads, int smem, cudaStream_t st, A... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute at;
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 template <int DQK, int DV>
 cudaError_t run(CacheAttnParams& p, int max_q, int sms, cudaStream_t st) {
   using C = CaCfg<DQK, DV>;
@@ -57,7 +40,7 @@ cudaError_t run(CacheAttnParams& p, int max_q, int sms, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const int grid = sms * C::CTAS;
   p.row_tiles = max(1, (int)(((int64_t)max_q * p.G + kCaRows - 1) / kCaRows));
-  e = launch_early(cache_attn_kernel<DQK, DV>, dim3(grid), kCaThreads, C::SMEM, st, (const CacheAttnParams)p);
+  e = launch_early(cache_attn_kernel<DQK, DV>, dim3(grid), kCaThreads, C::SMEM, st, p);
   if (e != cudaSuccess) return e;
   return launch_early(cache_join_kernel<DQK, DV>, dim3(p.c.Hkv * p.row_tiles, p.s.B + (p.s.cu ? 1 : 0)), kJoinThreads,
                       0, st, (const CacheAttnParams)p, grid);

@@ -24,14 +24,38 @@ inline cudaError_t smem_limit(K kernel, int bytes, std::atomic<uint64_t>& done) 
   return e;
 }
 
+// Waits until the kernel before this one in the stream is done, and lets the
+// one after it start (it waits in the same way): for kernels launched by launch_early.
+__device__ __forceinline__ void after_previous_kernel() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// A launch that may begin while the kernel before it in the stream still runs;
+// its kernel waits with griddepcontrol.wait before it touches memory.
+template <typename... A>
+inline cudaError_t launch_early(void (*kernel)(A...), dim3 grid, int threads, int smem, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // Eviction workspace: per (sequence, head) whether it is evicted from, the kept
-// tokens in order, the ratios old / new scale of each (K, V), the new blocks'
-// scales and, for sequences whose keys do not fit in shared memory, the keys.
+// tokens in order (page and row they come from, old / new scale of K and of V),
+// the new blocks' scales (K, V) and, for sequences too long for shared memory,
+// the keys of their weights.
 constexpr int kEvictSmemKeys = 48 * 1024;
 struct EvictWorkspace {
   int* live;       // [B][Hkv]
-  int32_t* src;    // [B][Hkv][budget]
-  float2* ratio;   // [B][Hkv][budget]
+  int4* items;     // [B][Hkv][budget]
   float2* scale;   // [B][Hkv][blocks]
   uint32_t* keys;  // [B][Hkv][cap], used when cap > kEvictSmemKeys
   int64_t cap;     // tokens a page table row can hold
