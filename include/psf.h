@@ -413,8 +413,8 @@ int psf_grad_add_live_rows(void* dst, const void* src, const int32_t* cu_q, cons
  *    weight each token has received so far, for eviction.
  *  k_strides / v_strides: element strides (page, head, row), all zero for the
  *  contiguous ones; else positive multiples of 16 below 2^38 (a dimension of
- *  extent 1 is ignored), and no overlap. The last dim is contiguous, base
- *  pointers 16-byte aligned. Head dims as for the attention calls.
+ *  extent 1 is ignored), and no overlap. The last dim is contiguous; k, v and
+ *  weight are 16-byte aligned. Head dims as for the attention calls.
  *
  *  Sequences: page_table int32 [B, max_pages] (contiguous) lists the pages of
  *  each sequence in order, seq_lens int32 [B] its tokens: token j of sequence b

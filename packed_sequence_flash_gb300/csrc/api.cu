@@ -635,7 +635,8 @@ int cache_view(const psf_kv_cache* cache, CacheView* v) {
   if (!supported_dims(c.Dqk, c.Dv))
     return fail(PSF_EUNSUPPORTED, "head dims (Dqk=%d, Dv=%d) not in {(64,64),(128,128),(192,128),(512,512)}", c.Dqk, c.Dv);
   if (!c.k || !c.v || !c.k_scale || !c.v_scale) return fail(PSF_EINVAL, "cache: null tensor pointer");
-  if (!aligned16(c.k) || !aligned16(c.v)) return fail(PSF_EINVAL, "cache: k and v must be 16-byte aligned");
+  if (!aligned16(c.k) || !aligned16(c.v) || !aligned16(c.weight))
+    return fail(PSF_EINVAL, "cache: k, v and weight must be 16-byte aligned");
   int rc;
   if ((rc = cache_strides(c.k_strides, "k", c, c.Dqk, &v->k_sp, &v->k_sh, &v->k_sr)) ||
       (rc = cache_strides(c.v_strides, "v", c, c.Dv, &v->v_sp, &v->v_sh, &v->v_sr)))

@@ -16,7 +16,7 @@ namespace {
 // largest magnitude is taken on packed 16-bit patterns (their order without the
 // sign is that of the values) and codes are made with a product by the scale's
 // reciprocal, exact for a power of two: with a division and a test of every
-// element for being finite 16 Ki prompt tokens took 30 us. Sequence b's pages are tasks start(b) .. in an index space that
+// element for being finite 10 Ki prompt tokens of 8 heads of 128 took 30 us, now 18. Sequence b's pages are tasks start(b) .. in an index space that
 // leaves floor(cu / page) + 2 b tasks before it, room enough for the
 // floor((n - 2) / page) + 2 pages that n rows can touch, so a CTA finds its
 // page from cu alone.
@@ -25,7 +25,7 @@ constexpr float kMaxFloat = 3.402823466e38f;
 constexpr int kAppendHeld = 8;  // 16-byte vectors a thread keeps between its two looks at the rows
 
 template <typename T>
-__global__ void __launch_bounds__(kAppendThreads)
+__global__ void __launch_bounds__(kAppendThreads, 8)
     append_kernel(CacheView c, SeqView s, const T* kin, int64_t k_ss, int64_t k_sh, const T* vin, int64_t v_ss,
                   int64_t v_sh, int* status) {
   __shared__ float warp_top[kAppendThreads / 32];
@@ -79,12 +79,14 @@ __global__ void __launch_bounds__(kAppendThreads)
   }
 #pragma unroll
   for (int u = 0; u < kAppendHeld; ++u) look(held[u]);
+#pragma unroll 2
   for (int i = kAppendHeld * kAppendThreads + tid; i < items; i += kAppendThreads) look(load(i));
   const float2 pair = unpack2<T>(most);
   const bool odd = __syncthreads_or(!(pair.x <= kMaxFloat) || !(pair.y <= kMaxFloat));  // inf or NaN among the rows
   float top = fmaxf(pair.x, pair.y);
   if (odd) {  // once more, over the finite values alone
     top = 0.f;
+#pragma unroll 1
     for (int i = tid; i < items; i += kAppendThreads) {
       const uint4 x = load(i);
       const uint32_t w[4] = {x.x, x.y, x.z, x.w};
@@ -112,36 +114,47 @@ __global__ void __launch_bounds__(kAppendThreads)
     for (int i = tid; i < r0 * (D >> 4); i += kAppendThreads) {
       const int row = i / (D >> 4);
       uint4* at = reinterpret_cast<uint4*>(out + sr * row + (i - row * (D >> 4)) * 16);
-      uint4 x = *at;
-      x.x = rescale4(x.x, r);
-      x.y = rescale4(x.y, r);
-      x.z = rescale4(x.z, r);
-      x.w = rescale4(x.w, r);
-      *at = x;
+      *at = rescale16(*at, r);
     }
   }
-  // A scale that the append chose is a power of two; one that was there may not be.
-  const bool plain = !odd && (__float_as_int(scale) & 0x7fffff) == 0 && scale > 0.f;
-  const float inv = 1.f / scale;
-  auto put = [&](int i, const uint4& x) {
+  auto store = [&](int i, const uint32_t (&e)[4]) {
     const int row = row_of(i);
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-    uint32_t e[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 f = unpack2<T>(w[j]);
-      e[j] = plain ? e4m3_pair(f.x * inv, f.y * inv)
-                   : e4m3_pair(finite_or_nan(f.x) / scale, finite_or_nan(f.y) / scale);
-    }
     *reinterpret_cast<uint2*>(out + sr * (r0 + row) + (i - row * vecs) * 8) =
         make_uint2(e[0] | (e[1] << 16), e[2] | (e[3] << 16));
   };
+  // A scale that the append chose is a power of two; one that was there may not be.
+  if (!odd && (__float_as_int(scale) & 0x7fffff) == 0 && scale > 0.f) {
+    const float inv = 1.f / scale;
+    auto put = [&](int i, const uint4& x) {
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+      uint32_t e[4];
 #pragma unroll
-  for (int u = 0; u < kAppendHeld; ++u) {
-    const int i = u * kAppendThreads + tid;
-    if (i < items) put(i, held[u]);
+      for (int j = 0; j < 4; ++j) {
+        const float2 f = unpack2<T>(w[j]);
+        e[j] = e4m3_pair(f.x * inv, f.y * inv);
+      }
+      store(i, e);
+    };
+#pragma unroll
+    for (int u = 0; u < kAppendHeld; ++u) {
+      const int i = u * kAppendThreads + tid;
+      if (i < items) put(i, held[u]);
+    }
+    for (int i = kAppendHeld * kAppendThreads + tid; i < items; i += kAppendThreads) put(i, load(i));
+  } else {
+#pragma unroll 1
+    for (int i = tid; i < items; i += kAppendThreads) {
+      const uint4 x = load(i);
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+      uint32_t e[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 f = unpack2<T>(w[j]);
+        e[j] = e4m3_pair(finite_or_nan(f.x) / scale, finite_or_nan(f.y) / scale);
+      }
+      store(i, e);
+    }
   }
-  for (int i = kAppendHeld * kAppendThreads + tid; i < items; i += kAppendThreads) put(i, load(i));
   if (!is_v && c.weight)
     for (int r = r0 + tid; r < r1; r += kAppendThreads) c.weight[((int64_t)pg * c.Hkv + h) * c.page + r] = 0.f;
 }
@@ -245,7 +258,7 @@ __device__ __forceinline__ float key_weight(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? k & 0x7fffffffu : ~k);
 }
 
-constexpr int kSelectThreads = 1024;
+constexpr int kSelectThreads = 512;
 
 // Exclusive block-wide prefix sum.
 __device__ int select_scan(int v, int* warp_tot) {
@@ -263,16 +276,21 @@ __device__ int select_scan(int v, int* warp_tot) {
   return before + x - v;
 }
 
-// One CTA per (head, sequence). The smallest kept weight is found bit by bit
-// over the integer keys (two bits a step, counted in parallel: no atomics, no
-// order), then the kept tokens are listed in their order, the new blocks'
-// scales set and the weights written. Latency bounds it: a few passes over one
-// head's weights, which stay in shared memory (in the workspace when they are too many).
-__global__ void __launch_bounds__(kSelectThreads)
+constexpr int kSelectBins = 2048;
+
+// One CTA per (head, sequence). The smallest kept weight is found digit by digit
+// (11, 11 and 10 bits of its key) from histograms in shared memory (integer
+// counts: their order does not matter). Then the kept tokens
+// are listed in their order, the new blocks' scales set and the weights written.
+// Latency bounds it: a few passes over one head's weights, which stay in shared
+// memory (in the workspace when they are too many). Halving the interval of keys
+// instead, two bits a pass, took 16 passes: 96 us against XXX for 384 heads of 11 Ki tokens.
+__global__ void __launch_bounds__(kSelectThreads, 2)
     evict_select_kernel(CacheView c, SeqView s, int budget, int recent, int32_t* new_lens, EvictWorkspace ws,
-                        int smem_keys, int* status) {
-  extern __shared__ uint32_t key_smem[];
-  __shared__ int warp_tot[32], cnt[2][3][32];
+                        int smem_keys, int smem_kept, int* status) {
+  extern __shared__ uint32_t dyn_smem[];  // keys, then the list of kept tokens
+  __shared__ int hist[kSelectBins];
+  __shared__ int warp_tot[32], found_bin, found_above;
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   const int h = blockIdx.x, b = blockIdx.y;
   after_previous_kernel();
@@ -292,38 +310,63 @@ __global__ void __launch_bounds__(kSelectThreads)
   if (skip) return;
 
   const int old = n - recent, need = budget - recent;
-  uint32_t* keys = n <= smem_keys ? key_smem : ws.keys + unit * ws.cap;
+  uint32_t* keys = n <= smem_keys ? dyn_smem : ws.keys + unit * ws.cap;
+  int4* items = ws.items + unit * budget;
+  int* kept = reinterpret_cast<int*>(dyn_smem + smem_keys);  // when budget <= smem_kept
+  const bool in_smem = budget <= smem_kept;
   auto weight_at = [&](int j) -> float* {
     return c.weight + ((int64_t)table[j >> c.page_lg] * c.Hkv + h) * c.page + (j & (c.page - 1));
   };
+  // Four tokens at a time (of one page, whose rows all exist).
 #pragma unroll 4
-  for (int j = tid; j < n; j += kSelectThreads) keys[j] = weight_key(*weight_at(j));
-  __syncthreads();
-  uint32_t thr = 0;
-  int flip = 0;
-  for (int bit = 30; bit >= 0; bit -= 2, flip ^= 1) {
-    const uint32_t one = 1u << bit;
-    int n1 = 0, n2 = 0, n3 = 0;
-#pragma unroll 4
-    for (int j = tid; j < old; j += kSelectThreads) {
-      const uint32_t k = keys[j];
-      n1 += k >= thr + one;
-      n2 += k >= thr + 2 * one;
-      n3 += k >= thr + 3 * one;
+  for (int j = tid * 4; j < n; j += kSelectThreads * 4) {
+    const float4 w = *reinterpret_cast<const float4*>(weight_at(j));
+    *reinterpret_cast<uint4*>(keys + j) = make_uint4(weight_key(w.x), weight_key(w.y), weight_key(w.z), weight_key(w.w));
+  }
+  uint32_t thr = 0xffffffffu;  // key of the smallest kept weight
+  int all_above = 0;           // older tokens with a larger key
+  if (need > 0) {
+    thr = 0;
+    int shift = 21;
+    for (int pass = 0; pass < 3; ++pass) {
+      const int bits = pass < 2 ? 11 : 10;
+      for (int i = tid; i < kSelectBins; i += kSelectThreads) hist[i] = 0;
+      __syncthreads();
+#pragma unroll 2
+      for (int j = tid * 4; j < old; j += kSelectThreads * 4) {
+        const uint4 x = *reinterpret_cast<const uint4*>(keys + j);
+        const uint32_t k[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (j + e < old && (pass == 0 || (k[e] >> (shift + bits)) == (thr >> (shift + bits))))
+            atomicAdd(&hist[(k[e] >> shift) & ((1 << bits) - 1)], 1);
+      }
+      __syncthreads();
+      // Bins from the top, a few per thread: the one in which the count reaches `need`.
+      constexpr int PER = kSelectBins / kSelectThreads;
+      const int hi = kSelectBins - 1 - PER * tid;
+      int sum = 0;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) sum += hist[hi - i];
+      int before = all_above + select_scan(sum, warp_tot);
+      if (before < need && before + sum >= need) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          const int count = hist[hi - i];
+          if (before < need && before + count >= need) {
+            found_bin = hi - i;
+            found_above = before;
+          }
+          before += count;
+        }
+      }
+      __syncthreads();
+      thr |= (uint32_t)found_bin << shift;
+      all_above = found_above;
+      shift -= pass == 0 ? 11 : 10;
     }
-    n1 = __reduce_add_sync(0xffffffffu, n1);
-    n2 = __reduce_add_sync(0xffffffffu, n2);
-    n3 = __reduce_add_sync(0xffffffffu, n3);
-    if (lane == 0) {
-      cnt[flip][0][wid] = n1;
-      cnt[flip][1][wid] = n2;
-      cnt[flip][2][wid] = n3;
-    }
-    __syncthreads();  // one a step: the next step counts in the other buffer
-    n1 = __reduce_add_sync(0xffffffffu, cnt[flip][0][lane]);
-    n2 = __reduce_add_sync(0xffffffffu, cnt[flip][1][lane]);
-    n3 = __reduce_add_sync(0xffffffffu, cnt[flip][2][lane]);
-    thr += n3 >= need ? 3 * one : (n2 >= need ? 2 * one : (n1 >= need ? one : 0));
+  } else {
+    __syncthreads();
   }
   // Thread t lists tokens [t per, (t + 1) per); an odd `per` spreads the shared-memory reads.
   const int per = ((n + kSelectThreads - 1) / kSelectThreads) | 1;
@@ -333,23 +376,24 @@ __global__ void __launch_bounds__(kSelectThreads)
     above += keys[j] > thr;
     equal += keys[j] == thr;
   }
-  int all_above = __reduce_add_sync(0xffffffffu, above);
-  if (lane == 0) cnt[flip][0][wid] = all_above;
-  __syncthreads();
-  all_above = __reduce_add_sync(0xffffffffu, cnt[flip][0][lane]);
   const int quota = need - all_above;  // tokens with exactly the smallest kept weight: the first ones
   const int eq_before = select_scan(equal, warp_tot);
   const int eq_kept = min(max(quota - eq_before, 0), equal);
   const int mine = above + eq_kept + max(j1 - max(j0, old), 0);
   int at = select_scan(mine, warp_tot);
-  int4* items = ws.items + unit * budget;
   for (int j = j0, left = eq_kept; j < j1; ++j) {
     bool keep = j >= old || keys[j] > thr;
     if (!keep && keys[j] == thr && left > 0) {
       keep = true;
       --left;
     }
-    if (keep) items[at++].x = j;
+    if (keep) {
+      if (in_smem)
+        kept[at] = j;
+      else
+        items[at].x = j;
+      ++at;
+    }
   }
   __syncthreads();
 
@@ -363,7 +407,7 @@ __global__ void __launch_bounds__(kSelectThreads)
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int j = base + u * 32 + lane;
-      from[u] = j < budget ? items[j].x : -1;
+      from[u] = j < budget ? (in_smem ? kept[j] : items[j].x) : -1;
     }
 #pragma unroll
     for (int u = 0; u < 4; ++u) pg[u] = from[u] >= 0 ? table[from[u] >> c.page_lg] : 0;
@@ -416,51 +460,41 @@ __global__ void __launch_bounds__(kSelectThreads)
 // it. Slices of a row go to CTAs of their own when (head, sequence) pairs alone
 // would not fill the device. Bound by memory: every kept code is read and written once.
 constexpr int kMoveThreads = 256;
-constexpr int kMoveVecs = 8;
-__global__ void __launch_bounds__(kMoveThreads, 3)
+constexpr int kMoveVecs = 4;  // of a batch per thread; more made the rows' reads and writes slower (8: 306 us for 239)
+__global__ void __launch_bounds__(kMoveThreads, 6)
     evict_move_kernel(CacheView c, SeqView s, int budget, EvictWorkspace ws, int slices) {
   const int tid = threadIdx.x, h = blockIdx.x, b = blockIdx.y;
   const bool is_v = blockIdx.z & 1;
   const int slice = blockIdx.z >> 1;
   const int64_t unit = (int64_t)b * c.Hkv + h;
-  const int D = is_v ? c.Dv : c.Dqk;
-  const int vecs = (D >> 4) / slices;  // 16-byte vectors of this CTA's part of a row
+  const int vecs = ((is_v ? c.Dv : c.Dqk) >> 4) / slices;  // 16-byte vectors of this CTA's part of a row
   const int32_t* table = s.table + (int64_t)b * s.max_pages;
-  uint8_t* base = (is_v ? c.v + c.v_sh * h : c.k + c.k_sh * h) + slice * vecs * 16;
+  const int rows = kMoveThreads / vecs, mine = tid / vecs;  // rows a pass, and this thread's of them
   const int64_t sp = is_v ? c.v_sp : c.k_sp, sr = is_v ? c.v_sr : c.k_sr;
+  uint8_t* base = (is_v ? c.v + c.v_sh * h : c.k + c.k_sh * h) + (slice * vecs + tid - mine * vecs) * 16;
   const int4* items = ws.items + unit * budget;
+  const int last = mine < rows ? budget : 0;  // threads past the rows of a pass have none
   after_previous_kernel();
   if (!ws.live[unit]) return;
-  const int64_t total = (int64_t)budget * vecs;
-  const int lg = (vecs & (vecs - 1)) == 0 ? 31 - __clz(vecs) : -1;
-  auto row_of = [&](int64_t i) { return lg >= 0 ? (int)(i >> lg) : (int)(i / vecs); };
-  for (int64_t i0 = 0; i0 < total; i0 += kMoveThreads * kMoveVecs) {
+  for (int j0 = mine; j0 - mine < budget; j0 += rows * kMoveVecs) {
     uint4 x[kMoveVecs];
     float r[kMoveVecs];
 #pragma unroll
     for (int u = 0; u < kMoveVecs; ++u) {
-      const int64_t i = i0 + u * kMoveThreads + tid;
-      r[u] = 1.f;
-      if (i < total) {
-        const int j = row_of(i), v = (int)(i - (int64_t)j * vecs);
+      const int j = j0 + u * rows;
+      if (j < last) {
         const int4 from = items[j];
         r[u] = __int_as_float(is_v ? from.w : from.z);
-        x[u] = *reinterpret_cast<const uint4*>(base + sp * from.x + sr * from.y + v * 16);
+        x[u] = *reinterpret_cast<const uint4*>(base + sp * from.x + sr * from.y);
       }
     }
     __syncthreads();
 #pragma unroll
     for (int u = 0; u < kMoveVecs; ++u) {
-      const int64_t i = i0 + u * kMoveThreads + tid;
-      if (i < total) {
-        const int j = row_of(i), v = (int)(i - (int64_t)j * vecs);
-        if (r[u] != 1.f) {
-          x[u].x = rescale4(x[u].x, r[u]);
-          x[u].y = rescale4(x[u].y, r[u]);
-          x[u].z = rescale4(x[u].z, r[u]);
-          x[u].w = rescale4(x[u].w, r[u]);
-        }
-        *reinterpret_cast<uint4*>(base + sp * table[j >> c.page_lg] + sr * (j & (c.page - 1)) + v * 16) = x[u];
+      const int j = j0 + u * rows;
+      if (j < last) {
+        if (r[u] != 1.f) x[u] = rescale16(x[u], r[u]);
+        *reinterpret_cast<uint4*>(base + sp * table[j >> c.page_lg] + sr * (j & (c.page - 1))) = x[u];
       }
     }
   }
@@ -497,8 +531,9 @@ cudaError_t launch_cache_evict(const CacheView& c, const SeqView& s, int budget,
   cudaError_t e = smem_limit(evict_select_kernel, kEvictSmemKeys * 4, smem_set);
   if (e != cudaSuccess) return e;
   const int smem_keys = (int)(ws.cap < kEvictSmemKeys ? ws.cap : kEvictSmemKeys);
-  e = launch_early(evict_select_kernel, dim3(c.Hkv, s.B), kSelectThreads, smem_keys * 4, st, c, s, budget, recent,
-                   new_lens, ws, smem_keys, status);
+  const int smem_kept = smem_keys + (int64_t)budget <= kEvictSmemKeys ? budget : 0;
+  e = launch_early(evict_select_kernel, dim3(c.Hkv, s.B), kSelectThreads, (smem_keys + smem_kept) * 4, st, c, s, budget,
+                   recent, new_lens, ws, smem_keys, smem_kept, status);
   if (e != cudaSuccess) return e;
   // Two CTAs per SM if the rows can be cut that far: parts of 32 bytes (a memory sector) or more.
   const int least = (c.Dqk < c.Dv ? c.Dqk : c.Dv) / 32;

@@ -81,10 +81,27 @@ __device__ __forceinline__ float2 e4m3_to_float2(uint32_t pair) {
   const uint32_t h = e4m3_to_half2(pair);
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
-// Four codes times r, rounded to e4m3 again.
+// Codes times r <= 1, rounded to e4m3 again. For a power of two the products are
+// made in fp16: exact wherever the result is not 0 (codes have 4 significant
+// bits and results below 2^-10 become 0; fp16 reaches down to 2^-24).
 __device__ __forceinline__ uint32_t rescale4(uint32_t codes, float r) {
   const float2 a = e4m3_to_float2(codes & 0xffff), b = e4m3_to_float2(codes >> 16);
   return e4m3_pair(a.x * r, a.y * r) | (e4m3_pair(b.x * r, b.y * r) << 16);
+}
+__device__ __forceinline__ uint32_t rescale4_half(uint32_t codes, __half2 r) {
+  uint32_t lo = e4m3_to_half2(codes & 0xffff), hi = e4m3_to_half2(codes >> 16);
+  const __half2 a = __hmul2(*reinterpret_cast<__half2*>(&lo), r), b = __hmul2(*reinterpret_cast<__half2*>(&hi), r);
+  uint16_t x, y;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(x) : "r"(*reinterpret_cast<const uint32_t*>(&a)));
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(y) : "r"(*reinterpret_cast<const uint32_t*>(&b)));
+  return x | ((uint32_t)y << 16);
+}
+__device__ __forceinline__ uint4 rescale16(uint4 x, float r) {
+  if ((__float_as_int(r) & 0x7fffff) == 0 && r <= 1.f && r >= 0.f) {
+    const __half2 h = __float2half2_rn(r);
+    return make_uint4(rescale4_half(x.x, h), rescale4_half(x.y, h), rescale4_half(x.z, h), rescale4_half(x.w, h));
+  }
+  return make_uint4(rescale4(x.x, r), rescale4(x.y, r), rescale4(x.z, r), rescale4(x.w, r));
 }
 __device__ __forceinline__ float finite_or_nan(float x) { return fabsf(x) <= 3.402823466e38f ? x : CUDART_NAN_F; }
 

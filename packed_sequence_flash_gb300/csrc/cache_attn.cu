@@ -32,18 +32,27 @@ __global__ void __launch_bounds__(kWeightThreads) cache_weight_kernel(const __gr
   atomicAdd(c.weight + ((int64_t)pg * c.Hkv + h) * c.page + (j & (c.page - 1)), sum);
 }
 
-template <int DQK, int DV>
+template <int DQK, int DV, bool EXTRA>
 cudaError_t run(CacheAttnParams& p, int max_q, int sms, cudaStream_t st) {
   using C = CaCfg<DQK, DV>;
   static std::atomic<uint64_t> smem_set{0};
-  cudaError_t e = smem_limit(cache_attn_kernel<DQK, DV>, C::SMEM, smem_set);
+  cudaError_t e = smem_limit(cache_attn_kernel<DQK, DV, EXTRA>, C::SMEM, smem_set);
   if (e != cudaSuccess) return e;
   const int grid = sms * C::CTAS;
   p.row_tiles = max(1, (int)(((int64_t)max_q * p.G + kCaRows - 1) / kCaRows));
-  e = launch_early(cache_attn_kernel<DQK, DV>, dim3(grid), kCaThreads, C::SMEM, st, p);
+  e = launch_early(cache_attn_kernel<DQK, DV, EXTRA>, dim3(grid), kCaThreads, C::SMEM, st, p);
   if (e != cudaSuccess) return e;
-  return launch_early(cache_join_kernel<DQK, DV>, dim3(p.c.Hkv * p.row_tiles, p.s.B + (p.s.cu ? 1 : 0)), kJoinThreads,
-                      0, st, (const CacheAttnParams)p, grid);
+  const int64_t units = (int64_t)p.c.Hkv * p.row_tiles * p.s.B;
+  int parts = 1;
+  while (parts < kCaRows && units * parts * 2 <= 2 * sms) parts *= 2;
+  return launch_early(cache_join_kernel<DQK, DV>, dim3(p.c.Hkv * p.row_tiles, p.s.B + (p.s.cu ? 1 : 0), parts),
+                      kJoinThreads, 0, st, p, grid);
+}
+
+template <int DQK, int DV>
+cudaError_t run(CacheAttnParams& p, int max_q, int sms, cudaStream_t st) {
+  return p.accumulate || p.softcap > 0.f ? run<DQK, DV, true>(p, max_q, sms, st)
+                                         : run<DQK, DV, false>(p, max_q, sms, st);
 }
 
 }  // namespace
@@ -60,8 +69,7 @@ cudaError_t launch_cache_attn(CacheAttnParams& p, int max_q, int sms, cudaStream
     e = run<512, 512>(p, max_q, sms, st);
   if (e != cudaSuccess || !p.accumulate) return e;
   const unsigned chunks = (unsigned)((p.score_cap + kWeightThreads - 1) / kWeightThreads);
-  return launch_early(cache_weight_kernel, dim3(chunks, p.c.Hkv, p.s.B), kWeightThreads, 0, st,
-                      (const CacheAttnParams)p);
+  return launch_early(cache_weight_kernel, dim3(chunks, p.c.Hkv, p.s.B), kWeightThreads, 0, st, p);
 }
 
 }  // namespace psf

@@ -225,7 +225,8 @@ struct CaWalk {
   }
 };
 
-template <int DQK, int DV>
+// EXTRA: logits are capped or scores kept (p.softcap, p.accumulate).
+template <int DQK, int DV, bool EXTRA>
 __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV>::CTAS)
     cache_attn_kernel(const __grid_constant__ CacheAttnParams p) {
   using C = CaCfg<DQK, DV>;
@@ -532,6 +533,10 @@ __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV>::CTAS)
 #pragma unroll
       for (int c = 0; c < 4; ++c) o[m][c] = 0.f;
 
+    // Where this lane's first row keeps its scores.
+    float* scores = EXTRA && p.accumulate
+                        ? p.scores + (((int64_t)u.b * p.c.Hkv + u.h) * p.score_rows + n0 + 2 * t) * p.score_cap
+                        : nullptr;
     auto tile_step = [&](auto mask_tag, int tile) {
       constexpr bool MASK = decltype(mask_tag)::value;
       const uint8_t* sb = smem + st * C::STAGE;
@@ -571,7 +576,7 @@ __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV>::CTAS)
       float f[2] = {fac[0] * sc.x, fac[1] * sc.x};
 #pragma unroll
       for (int c = 0; c < 4; ++c) s[c] += s2[c];
-      if (p.softcap > 0.f) {
+      if (EXTRA && p.softcap > 0.f) {
         // c tanh(a) log2(e), tanh(a) = 1 - 2 / (e^(2a) + 1): off by some 2^-22 of the cap
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -580,13 +585,12 @@ __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV>::CTAS)
         }
         f[0] = f[1] = 1.f;
       }
-      if (p.accumulate) {
-        const int64_t unit = (int64_t)u.b * p.c.Hkv + u.h;
+      if (EXTRA && p.accumulate) {
+        float* at = scores + key;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int col = n0 + 2 * t + (c & 1), k = key + (c >> 1) * 8;
-          if (col < rows && k < hi) p.scores[(unit * p.score_rows + col) * p.score_cap + k] = s[c] * f[c & 1];
-        }
+        for (int c = 0; c < 4; ++c)
+          if (n0 + 2 * t + (c & 1) < rows && key + (c >> 1) * 8 < hi)
+            at[(c & 1) * p.score_cap + (c >> 1) * 8] = s[c] * f[c & 1];
       }
       const float dy[2] = {sc.y - ro[0], sc.y - ro[1]};
 #pragma unroll
@@ -787,7 +791,10 @@ __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV>::CTAS)
 
 // Joins the partial results of units that several CTAs share, in the order of
 // the CTAs, and writes the rows that no CTA wrote: sequences without keys, and
-// (blockIdx.y = B) rows past the last sequence. One CTA per (head, row tile) and sequence.
+// (blockIdx.y = B) rows past the last sequence. One CTA per (head, row tile),
+// sequence and part of the row tile: rows go to CTAs of their own when there
+// are few units, whose partial results are then many (57 per unit for one
+// sequence of 32 Ki keys and 8 heads: 15 us with one CTA each).
 constexpr int kJoinThreads = 512;
 template <int DQK, int DV>
 __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_constant__ CacheAttnParams p, int grid) {
@@ -808,6 +815,7 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
   };
   const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   if (b == p.s.B) {
+    if (blockIdx.z) return;
     const int first = min(max(p.s.cu[p.s.B], 0), p.s.T);
     for (int64_t x = (int64_t)blockIdx.x * kJoinThreads + tid; x < (int64_t)(p.s.T - first) * p.Hq;
          x += (int64_t)gridDim.x * kJoinThreads) {
@@ -820,8 +828,9 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
   }
   const CaSeq s = ca_seq(p, b);
   const int h = blockIdx.x / p.row_tiles, rt = blockIdx.x % p.row_tiles;
-  if (rt >= s.rt) return;
-  const int rows = s.q.m * p.G, n0 = rt * kCaRows, live = min(kCaRows, rows - n0);
+  const int part = kCaRows / gridDim.z, rows = s.q.m * p.G, n0 = rt * kCaRows + blockIdx.z * part;
+  if (rt >= s.rt || n0 >= rows) return;
+  const int live = min(part, rows - n0);
   if (s.kt == 0) {
     for (int x = tid; x < live * (DV / 8); x += kJoinThreads) {
       const int r = x / (DV / 8), y = n0 + r, i = y / p.G;
@@ -862,14 +871,15 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
   if (c0 == c1) return;  // one CTA had it all and wrote it
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int np = c1 - c0 + 1;
-  auto slot = [&](int i) -> int64_t { return (int64_t)(c0 + i) * 2 + (i == 0); };
+  const int at0 = blockIdx.z * part;  // of the row tile
+  auto row_at = [&](int i, int r) -> int64_t { return ((int64_t)(c0 + i) * 2 + (i == 0)) * kCaRows + at0 + r; };
   for (int r = warp; r < live; r += kJoinThreads / 32) {
     float top = -CUDART_INF_F, sum = 0.f;
-    for (int i = lane; i < np; i += 32) top = fmaxf(top, p.part_l[slot(i) * kCaRows + r]);
+    for (int i = lane; i < np; i += 32) top = fmaxf(top, p.part_l[row_at(i, r)]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     top = minus_inf_as_0(top);
-    for (int i = lane; i < np; i += 32) sum += ex2_approx(p.part_l[slot(i) * kCaRows + r] - top);
+    for (int i = lane; i < np; i += 32) sum += ex2_approx(p.part_l[row_at(i, r)] - top);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (lane == 0) {
@@ -880,19 +890,19 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
     }
   }
   __syncthreads();
-  // A thread takes four columns of a row over every GROUPS-th partial result;
-  // the groups' sums are added in their order.
-  constexpr int VEC = DV / 4, ROWS = kJoinThreads / VEC >= 8 ? 8 : kJoinThreads / VEC;
-  constexpr int GROUPS = kJoinThreads / (VEC * ROWS);
-  const int gr = tid / (VEC * ROWS), rr = tid / VEC % ROWS, d = (tid % VEC) * 4;
-  for (int r0 = 0; r0 < live; r0 += ROWS) {
+  // A thread takes four columns of a row over every groups-th partial result; the
+  // groups' sums are added in their order.
+  constexpr int VEC = DV / 4;
+  const int wide = min(part, kJoinThreads / VEC), groups = kJoinThreads / (VEC * wide);  // rows at a time
+  const int gr = tid / (VEC * wide), rr = tid / VEC % wide, d = (tid % VEC) * 4;
+  for (int r0 = 0; r0 < live; r0 += wide) {
     const int r = min(r0 + rr, live - 1);
     const float l = minus_inf_as_0(row_l[r]);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-    for (int k = gr; k < np; k += GROUPS) {
-      const float w = ex2_approx(p.part_l[slot(k) * kCaRows + r] - l);
-      const float4 a = *reinterpret_cast<const float4*>(p.part_o + (slot(k) * kCaRows + r) * DV + d);
+    for (int k = gr; k < np; k += groups) {
+      const float w = ex2_approx(p.part_l[row_at(k, r)] - l);
+      const float4 a = *reinterpret_cast<const float4*>(p.part_o + row_at(k, r) * DV + d);
       acc.x = fmaf(a.x, w, acc.x);
       acc.y = fmaf(a.y, w, acc.y);
       acc.z = fmaf(a.z, w, acc.z);
@@ -902,9 +912,8 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
     sums[tid] = acc;
     __syncthreads();
     if (gr == 0 && r0 + rr < live) {
-#pragma unroll
-      for (int k = 1; k < GROUPS; ++k) {
-        const float4 a = sums[tid + k * VEC * ROWS];
+      for (int k = 1; k < groups; ++k) {
+        const float4 a = sums[tid + k * VEC * wide];
         acc.x += a.x;
         acc.y += a.y;
         acc.z += a.z;
