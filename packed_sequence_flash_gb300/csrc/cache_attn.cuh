@@ -174,7 +174,6 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                "l"(src), "r"(bytes), "r"(smem_u32(bar))
                : "memory");
 }
-__device__ __forceinline__ float minus_inf_as_0(float x) { return x == -CUDART_INF_F ? 0.f : x; }
 
 // One unit of a share, and the keys and tiles it concerns.
 struct CaUnit {
@@ -800,8 +799,8 @@ template <int DQK, int DV>
 __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_constant__ CacheAttnParams p, int grid) {
   using C = CaCfg<DQK, DV>;
   __shared__ int64_t sum_before[kJoinThreads / 32], sum_all[kJoinThreads / 32];
-  __shared__ float row_l[kCaRows];
   __shared__ float4 sums[kJoinThreads];
+  __shared__ float2 tops[kJoinThreads];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = blockIdx.y;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -870,60 +869,81 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
   const int c0 = shares.owner(x0), c1 = shares.owner(x0 + s.kt - 1);
   if (c0 == c1) return;  // one CTA had it all and wrote it
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int np = c1 - c0 + 1;
-  const int at0 = blockIdx.z * part;  // of the row tile
+  const int np = c1 - c0 + 1, at0 = blockIdx.z * part;
   auto row_at = [&](int i, int r) -> int64_t { return ((int64_t)(c0 + i) * 2 + (i == 0)) * kCaRows + at0 + r; };
-  for (int r = warp; r < live; r += kJoinThreads / 32) {
-    float top = -CUDART_INF_F, sum = 0.f;
-    for (int i = lane; i < np; i += 32) top = fmaxf(top, p.part_l[row_at(i, r)]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    top = minus_inf_as_0(top);
-    for (int i = lane; i < np; i += 32) sum += ex2_approx(p.part_l[row_at(i, r)] - top);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) {
-      const float l = sum == 0.f ? -CUDART_INF_F : top + log2f(sum);
-      const int y = n0 + r, i = y / p.G;
-      row_l[r] = l;
-      p.lse[(int64_t)(h * p.G + y - i * p.G) * p.s.T + s.q.q0 + i] = l * 0.69314718055994531f;
-    }
-  }
-  __syncthreads();
-  // A thread takes four columns of a row over every groups-th partial result; the
-  // groups' sums are added in their order.
+  // A thread takes four columns of a row over every groups-th partial result, with
+  // a running maximum and sum of its own; the groups are added in their order.
   constexpr int VEC = DV / 4;
   const int wide = min(part, kJoinThreads / VEC), groups = kJoinThreads / (VEC * wide);  // rows at a time
   const int gr = tid / (VEC * wide), rr = tid / VEC % wide, d = (tid % VEC) * 4;
   for (int r0 = 0; r0 < live; r0 += wide) {
     const int r = min(r0 + rr, live - 1);
-    const float l = minus_inf_as_0(row_l[r]);
+    float top = kCaFloor, sum = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-    for (int k = gr; k < np; k += groups) {
-      const float w = ex2_approx(p.part_l[row_at(k, r)] - l);
-      const float4 a = *reinterpret_cast<const float4*>(p.part_o + row_at(k, r) * DV + d);
-      acc.x = fmaf(a.x, w, acc.x);
-      acc.y = fmaf(a.y, w, acc.y);
-      acc.z = fmaf(a.z, w, acc.z);
-      acc.w = fmaf(a.w, w, acc.w);
+#pragma unroll 1
+    for (int k0 = gr; k0 < np; k0 += groups * 8) {
+      float l[8];
+      float4 a[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int k = k0 + u * groups;
+        l[u] = -CUDART_INF_F;
+        a[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (k < np) {
+          l[u] = p.part_l[row_at(k, r)];
+          a[u] = *reinterpret_cast<const float4*>(p.part_o + row_at(k, r) * DV + d);
+        }
+      }
+      float m = top;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) m = fmaxf(m, l[u]);
+      const float f = ex2_approx(top - m);
+      acc.x *= f;
+      acc.y *= f;
+      acc.z *= f;
+      acc.w *= f;
+      sum *= f;
+      top = m;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const float w = ex2_approx(l[u] - m);
+        sum += w;
+        acc.x = fmaf(a[u].x, w, acc.x);
+        acc.y = fmaf(a[u].y, w, acc.y);
+        acc.z = fmaf(a[u].z, w, acc.z);
+        acc.w = fmaf(a[u].w, w, acc.w);
+      }
     }
     __syncthreads();
     sums[tid] = acc;
+    tops[tid] = make_float2(top, sum);
     __syncthreads();
     if (gr == 0 && r0 + rr < live) {
+      float m = top;
+      for (int k = 1; k < groups; ++k) m = fmaxf(m, tops[tid + k * VEC * wide].x);
+      float f = ex2_approx(top - m);
+      acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+      sum *= f;
       for (int k = 1; k < groups; ++k) {
+        const float2 ts = tops[tid + k * VEC * wide];
         const float4 a = sums[tid + k * VEC * wide];
-        acc.x += a.x;
-        acc.y += a.y;
-        acc.z += a.z;
-        acc.w += a.w;
+        f = ex2_approx(ts.x - m);
+        sum = fmaf(ts.y, f, sum);
+        acc.x = fmaf(a.x, f, acc.x);
+        acc.y = fmaf(a.y, f, acc.y);
+        acc.z = fmaf(a.z, f, acc.z);
+        acc.w = fmaf(a.w, f, acc.w);
       }
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
       const int y = n0 + r, i = y / p.G;
-      const uint2 w = p.f16 ? make_uint2(pack2<__half>(acc.x, acc.y), pack2<__half>(acc.z, acc.w))
-                            : make_uint2(pack2<__nv_bfloat16>(acc.x, acc.y), pack2<__nv_bfloat16>(acc.z, acc.w));
+      const uint2 w = p.f16 ? make_uint2(pack2<__half>(acc.x * inv, acc.y * inv), pack2<__half>(acc.z * inv, acc.w * inv))
+                            : make_uint2(pack2<__nv_bfloat16>(acc.x * inv, acc.y * inv),
+                                         pack2<__nv_bfloat16>(acc.z * inv, acc.w * inv));
       *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + p.o_ss * (s.q.q0 + i) +
                                 p.o_sh * (h * p.G + y - i * p.G) + d) = w;
+      if (d == 0)
+        p.lse[(int64_t)(h * p.G + y - i * p.G) * p.s.T + s.q.q0 + i] =
+            sum == 0.f ? -CUDART_INF_F : (m + log2f(sum)) * 0.69314718055994531f;
     }
   }
 }
