@@ -33,6 +33,11 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
+@functools.lru_cache(maxsize=None)
+def _call(name):
+    return getattr(_lib.load(), name)
+
+
 def _tensor(t, name, dtype, device):
     """A contiguous tensor of a call, on the cache's device (an index)."""
     if t.dtype is not dtype:
@@ -173,13 +178,13 @@ def kv_cache_append(cache, k, v, page_table, seq_lens, cu_new=None) -> None:
     if v.size(0) != T:
         raise ValueError("k and v must have the same number of rows")
     B, max_pages = _sequences(cache, page_table, seq_lens, cu_new, "cu_new")
-    _launch(cache.device, _lib.load().psf_kv_cache_append, cache._ref, kp, vp, _thd_strides(k, v), _DTYPES[dtype],
+    _launch(cache.device, _call("psf_kv_cache_append"), cache._ref, kp, vp, _thd_strides(k, v), _DTYPES[dtype],
             _ptr(cu_new), page_table.data_ptr(), seq_lens.data_ptr(), B, max_pages, T)
 
 
 @functools.lru_cache(maxsize=256)
 def _attn_workspace(*sizes) -> int:
-    return int(_lib.load().psf_attn_cache_workspace_size(*sizes))
+    return int(_call("psf_attn_cache_workspace_size")(*sizes))
 
 
 def attn_cache_workspace_size(cache, B, max_pages, Hq, max_q=1, accumulate=False) -> int:
@@ -227,7 +232,7 @@ def attn_cache_fwd(q, cache, page_table, seq_lens, scale, cu_q=None, max_q=None,
     else:
         _tensor(workspace, "workspace", workspace.dtype, device)
         size = workspace.numel() * workspace.element_size()
-    _launch(device, _lib.load().psf_attn_cache_fwd, qp, cache._ref, op, lse.data_ptr(), _ptr(cu_q),
+    _launch(device, _call("psf_attn_cache_fwd"), qp, cache._ref, op, lse.data_ptr(), _ptr(cu_q),
             page_table.data_ptr(), seq_lens.data_ptr(), B, max_pages, T, max_q, Hq, _thd_strides(q, out),
             _DTYPES[dtype], scale, 1 if causal else 0, _window(window), _cap(softcap),
             PSF_CACHE_ACCUMULATE if accumulate else 0, workspace.data_ptr(), size)
@@ -236,7 +241,7 @@ def attn_cache_fwd(q, cache, page_table, seq_lens, scale, cu_q=None, max_q=None,
 
 @functools.lru_cache(maxsize=256)
 def _evict_workspace(*sizes) -> int:
-    return int(_lib.load().psf_kv_cache_evict_workspace_size(*sizes))
+    return int(_call("psf_kv_cache_evict_workspace_size")(*sizes))
 
 
 def kv_cache_evict_workspace_size(cache, B, max_pages, budget) -> int:
@@ -263,7 +268,7 @@ def kv_cache_evict(cache, page_table, seq_lens, budget, recent, new_lens=None, w
     else:
         _tensor(workspace, "workspace", workspace.dtype, cache.device)
         size = workspace.numel() * workspace.element_size()
-    _launch(cache.device, _lib.load().psf_kv_cache_evict, cache._ref, page_table.data_ptr(), seq_lens.data_ptr(),
+    _launch(cache.device, _call("psf_kv_cache_evict"), cache._ref, page_table.data_ptr(), seq_lens.data_ptr(),
             new_lens.data_ptr(), B, max_pages, budget, recent, workspace.data_ptr(), size)
     return new_lens
 
@@ -283,6 +288,6 @@ def kv_cache_gather(cache, page_table, seq_lens, total_k, dtype=torch.bfloat16):
     k = torch.empty((total_k, cache.Hkv, cache.Dqk), dtype=dtype, device=dev)
     v = torch.empty((total_k, cache.Hkv, cache.Dv), dtype=dtype, device=dev)
     cu_k = torch.empty(B + 1, dtype=torch.int32, device=dev)
-    _launch(cache.device, _lib.load().psf_kv_cache_gather, cache._ref, page_table.data_ptr(), seq_lens.data_ptr(), B,
+    _launch(cache.device, _call("psf_kv_cache_gather"), cache._ref, page_table.data_ptr(), seq_lens.data_ptr(), B,
             max_pages, k.data_ptr(), v.data_ptr(), cu_k.data_ptr(), total_k, _DTYPES[dtype])
     return k, v, cu_k

@@ -167,6 +167,7 @@ __global__ void __launch_bounds__(kPrefixThreads)
   __shared__ int64_t tot[32];
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   after_previous_kernel();
+  let_next_kernel_start();
   int64_t carry = 0;
   for (int base = 0; base < s.B; base += kPrefixThreads) {
     const int b = base + tid;
@@ -294,6 +295,7 @@ __global__ void __launch_bounds__(kSelectThreads, 2)
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   const int h = blockIdx.x, b = blockIdx.y;
   after_previous_kernel();
+  let_next_kernel_start();
   const int n = s.lens[b];
   const int32_t* table = s.table + (int64_t)b * s.max_pages;
   const int64_t unit = (int64_t)b * c.Hkv + h;
@@ -527,8 +529,8 @@ cudaError_t launch_cache_gather(const CacheView& c, const SeqView& s, void* k, v
 
 cudaError_t launch_cache_evict(const CacheView& c, const SeqView& s, int budget, int recent, int32_t* new_lens,
                                const EvictWorkspace& ws, int sms, int* status, cudaStream_t st) {
-  static std::atomic<uint64_t> smem_set{0};
-  cudaError_t e = smem_limit(evict_select_kernel, kEvictSmemKeys * 4, smem_set);
+  static std::atomic<uint64_t> select_set{0};
+  cudaError_t e = kernel_setup(evict_select_kernel, kEvictSmemKeys * 4, false, select_set);
   if (e != cudaSuccess) return e;
   const int smem_keys = (int)(ws.cap < kEvictSmemKeys ? ws.cap : kEvictSmemKeys);
   const int smem_kept = smem_keys + (int64_t)budget <= kEvictSmemKeys ? budget : 0;

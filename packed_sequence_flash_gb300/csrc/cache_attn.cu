@@ -6,37 +6,52 @@ namespace psf {
 
 namespace {
 
-// Weights of the keys, from the stored scores and the finished lse: a thread per
-// key sums exp2(score - lse) over the rows that see it, in their order, and
-// adds the sum once (atomically: another sequence may share the page).
-constexpr int kWeightThreads = 256;
+// Weights of the keys, from the stored scores and the finished lse: a thread
+// sums exp2(score - lse) of four keys over the rows that see them, in their
+// order, and adds the sums once (atomically: another sequence may share the page).
+constexpr int kWeightThreads = 128;
+constexpr int kWeightKeys = 4 * kWeightThreads;
 __global__ void __launch_bounds__(kWeightThreads) cache_weight_kernel(const __grid_constant__ CacheAttnParams p) {
   const CacheView& c = p.c;
-  const int b = blockIdx.z, h = blockIdx.y, j = blockIdx.x * kWeightThreads + threadIdx.x;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int b = blockIdx.z, h = blockIdx.y, j = blockIdx.x * kWeightKeys + threadIdx.x * 4;
+  let_next_kernel_start();
+  // (No CTA ends before the kernels before this one: the next one waits for this one alone.)
   const Seq q = seq_at(p.s, c.page, b);
-  if (j >= q.n) return;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int pg = p.s.table[(int64_t)b * p.s.max_pages + (j >> c.page_lg)];
+  const int pg = j < q.n ? p.s.table[(int64_t)b * p.s.max_pages + (j >> c.page_lg)] : -1;
+  after_previous_kernel();
   if (pg < 0 || pg >= c.pages) return;
+  float* weight = c.weight + ((int64_t)pg * c.Hkv + h) * c.page + (j & (c.page - 1));
   const float* s = p.scores + (((int64_t)b * c.Hkv + h) * p.score_rows) * p.score_cap + j;
-  float sum = 0.f;
+  float sum[4] = {0.f, 0.f, 0.f, 0.f};
   for (int i = 0; i < q.m; ++i) {
     int lo, hi;
     ca_row_keys(p, q.n, q.m, i, lo, hi);
-    if (j < lo || j >= hi) continue;
-    for (int g = 0; g < p.G; ++g)
-      sum += ex2_approx(s[(int64_t)(i * p.G + g) * p.score_cap] -
-                        p.lse[(int64_t)(h * p.G + g) * p.s.T + q.q0 + i] * 1.4426950408889634f);
+    if (j + 4 <= lo || j >= hi) continue;
+#pragma unroll 4
+    for (int g = 0; g < p.G; ++g) {
+      const float4 z = *reinterpret_cast<const float4*>(s + (int64_t)(i * p.G + g) * p.score_cap);
+      const float l = p.lse[(int64_t)(h * p.G + g) * p.s.T + q.q0 + i] * 1.4426950408889634f;
+      const float e[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (j + k >= lo && j + k < hi) sum[k] += ex2_approx(e[k] - l);  // scores past these were never written
+    }
   }
-  atomicAdd(c.weight + ((int64_t)pg * c.Hkv + h) * c.page + (j & (c.page - 1)), sum);
+  if (j + 4 <= q.n) {
+    asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(weight), "f"(sum[0]), "f"(sum[1]), "f"(sum[2]),
+                 "f"(sum[3])
+                 : "memory");
+  } else {
+    for (int k = 0; j + k < q.n; ++k) atomicAdd(weight + k, sum[k]);
+  }
 }
 
 template <int DQK, int DV, bool EXTRA>
 cudaError_t run(CacheAttnParams& p, int max_q, int sms, cudaStream_t st) {
   using C = CaCfg<DQK, DV>;
-  static std::atomic<uint64_t> smem_set{0};
-  cudaError_t e = smem_limit(cache_attn_kernel<DQK, DV, EXTRA>, C::SMEM, smem_set);
+  static std::atomic<uint64_t> main_set{0}, join_set{0};
+  cudaError_t e = kernel_setup(cache_attn_kernel<DQK, DV, EXTRA>, C::SMEM, true, main_set);
+  if (e == cudaSuccess) e = kernel_setup(cache_join_kernel<DQK, DV>, 0, true, join_set);
   if (e != cudaSuccess) return e;
   const int grid = sms * C::CTAS;
   p.row_tiles = max(1, (int)(((int64_t)max_q * p.G + kCaRows - 1) / kCaRows));
@@ -68,7 +83,9 @@ cudaError_t launch_cache_attn(CacheAttnParams& p, int max_q, int sms, cudaStream
   else
     e = run<512, 512>(p, max_q, sms, st);
   if (e != cudaSuccess || !p.accumulate) return e;
-  const unsigned chunks = (unsigned)((p.score_cap + kWeightThreads - 1) / kWeightThreads);
+  static std::atomic<uint64_t> weight_set{0};
+  if ((e = kernel_setup(cache_weight_kernel, 0, true, weight_set)) != cudaSuccess) return e;
+  const unsigned chunks = (unsigned)((p.score_cap + kWeightKeys - 1) / kWeightKeys);
   return launch_early(cache_weight_kernel, dim3(chunks, p.c.Hkv, p.s.B), kWeightThreads, 0, st, p);
 }
 

@@ -258,8 +258,8 @@ __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV>::CTAS)
   }
   // Nothing above touches memory that the kernel before this one may still
   // write; the join may start once every CTA is past this point.
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  after_previous_kernel();
+  let_next_kernel_start();
 
   // The whole work, and the sequence that this share begins in.
   int64_t total = 0, before = 0, count = 0;  // places before and of this thread's sequence
@@ -803,44 +803,18 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
   __shared__ float2 tops[kJoinThreads];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = blockIdx.y;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  auto write8 = [&](int64_t row, int hq, int d, const float* x) {
-    uint32_t w[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      w[e] = p.f16 ? pack2<__half>(x[2 * e], x[2 * e + 1]) : pack2<__nv_bfloat16>(x[2 * e], x[2 * e + 1]);
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + p.o_ss * row + p.o_sh * hq + d) =
-        make_uint4(w[0], w[1], w[2], w[3]);
+  let_next_kernel_start();
+  auto zero8 = [&](int64_t row, int hq, int d) {
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + p.o_ss * row + p.o_sh * hq + d) = make_uint4(0, 0, 0, 0);
   };
-  const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  if (b == p.s.B) {
-    if (blockIdx.z) return;
-    const int first = min(max(p.s.cu[p.s.B], 0), p.s.T);
-    for (int64_t x = (int64_t)blockIdx.x * kJoinThreads + tid; x < (int64_t)(p.s.T - first) * p.Hq;
-         x += (int64_t)gridDim.x * kJoinThreads) {
-      const int64_t row = first + x / p.Hq;
-      const int hq = (int)(x % p.Hq);
-      for (int d = 0; d < DV; d += 8) write8(row, hq, d, zero);
-      p.lse[(int64_t)hq * p.s.T + row] = -CUDART_INF_F;
-    }
-    return;
-  }
-  const CaSeq s = ca_seq(p, b);
+  // Until the attention kernel is done (no CTA ends before it: what comes next
+  // waits for this kernel alone): where this unit's partial results are.
+  const bool tail = b == p.s.B;
+  CaSeq s = {};
+  if (!tail) s = ca_seq(p, b);
   const int h = blockIdx.x / p.row_tiles, rt = blockIdx.x % p.row_tiles;
   const int part = kCaRows / gridDim.z, rows = s.q.m * p.G, n0 = rt * kCaRows + blockIdx.z * part;
-  if (rt >= s.rt || n0 >= rows) return;
-  const int live = min(part, rows - n0);
-  if (s.kt == 0) {
-    for (int x = tid; x < live * (DV / 8); x += kJoinThreads) {
-      const int r = x / (DV / 8), y = n0 + r, i = y / p.G;
-      write8(s.q.q0 + i, h * p.G + y - i * p.G, (x - r * (DV / 8)) * 8, zero);
-    }
-    if (tid < live) {
-      const int y = n0 + tid, i = y / p.G;
-      p.lse[(int64_t)(h * p.G + y - i * p.G) * p.s.T + s.q.q0 + i] = -CUDART_INF_F;
-    }
-    return;
-  }
+  const int live = tail || rt >= s.rt ? 0 : min(part, rows - n0);
   int64_t before = 0, total = 0;
   for (int x = tid; x < p.s.B; x += kJoinThreads) {
     const int64_t n = ca_seq(p, x).places(p.c.Hkv);
@@ -863,12 +837,36 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
     total += sum_all[w];
     before += sum_before[w];
   }
-  const int parts = ca_parts(total, grid, p.min_share);
+  const CaShares shares(total, ca_parts(total, grid, p.min_share));
   const int64_t x0 = before + ((int64_t)h * s.rt + rt) * s.cost() + kCaUnit;  // the unit's first tile
-  const CaShares shares(total, parts);
-  const int c0 = shares.owner(x0), c1 = shares.owner(x0 + s.kt - 1);
+  const bool split = live > 0 && s.kt > 0;
+  const int c0 = split ? shares.owner(x0) : 0, c1 = split ? shares.owner(x0 + s.kt - 1) : 0;
+  after_previous_kernel();
+  if (tail) {  // rows past the last sequence
+    if (blockIdx.z) return;
+    const int first = min(max(p.s.cu[p.s.B], 0), p.s.T);
+    for (int64_t x = (int64_t)blockIdx.x * kJoinThreads + tid; x < (int64_t)(p.s.T - first) * p.Hq;
+         x += (int64_t)gridDim.x * kJoinThreads) {
+      const int64_t row = first + x / p.Hq;
+      const int hq = (int)(x % p.Hq);
+      for (int d = 0; d < DV; d += 8) zero8(row, hq, d);
+      p.lse[(int64_t)hq * p.s.T + row] = -CUDART_INF_F;
+    }
+    return;
+  }
+  if (live <= 0) return;
+  if (s.kt == 0) {  // a sequence without keys
+    for (int x = tid; x < live * (DV / 8); x += kJoinThreads) {
+      const int r = x / (DV / 8), y = n0 + r, i = y / p.G;
+      zero8(s.q.q0 + i, h * p.G + y - i * p.G, (x - r * (DV / 8)) * 8);
+    }
+    if (tid < live) {
+      const int y = n0 + tid, i = y / p.G;
+      p.lse[(int64_t)(h * p.G + y - i * p.G) * p.s.T + s.q.q0 + i] = -CUDART_INF_F;
+    }
+    return;
+  }
   if (c0 == c1) return;  // one CTA had it all and wrote it
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int np = c1 - c0 + 1, at0 = blockIdx.z * part;
   auto row_at = [&](int i, int r) -> int64_t { return ((int64_t)(c0 + i) * 2 + (i == 0)) * kCaRows + at0 + r; };
   // A thread takes four columns of a row over every groups-th partial result, with

@@ -11,23 +11,32 @@
 
 namespace psf {
 
-// Sets a kernel's dynamic shared memory limit once per device (done: a bit per device index).
+// Once per device (done: a bit per device index): a kernel's dynamic shared
+// memory limit and, for the attention's kernels, all of an SM's memory to shared
+// memory rather than L1. A kernel that starts early shares SMs with the one
+// before it, whose split stays while they run: behind a kernel with a small share
+// the attention had room for two of its three CTAs per SM, and the third waited
+// for one of them to end. The copying kernels need the L1 (the gather took 98 us
+// for 84 without it), so they keep it and let nothing start before they are done.
 template <typename K>
-inline cudaError_t smem_limit(K kernel, int bytes, std::atomic<uint64_t>& done) {
+inline cudaError_t kernel_setup(K kernel, int smem_bytes, bool all_shared, std::atomic<uint64_t>& done) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const uint64_t bit = uint64_t(1) << (dev & 63);
   if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (all_shared)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+  if (e == cudaSuccess && smem_bytes > 0)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes);
   if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
   return e;
 }
 
-// Waits until the kernel before this one in the stream is done, and lets the
-// one after it start (it waits in the same way): for kernels launched by launch_early.
-__device__ __forceinline__ void after_previous_kernel() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+// For kernels launched by launch_early: waits until the kernel before this one in
+// the stream is done, and lets the one after it start (it waits in the same way).
+__device__ __forceinline__ void after_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_kernel_start() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
