@@ -15,11 +15,12 @@ __global__ void __launch_bounds__(kWeightThreads) cache_weight_kernel(const __gr
   const CacheView& c = p.c;
   const int b = blockIdx.z, h = blockIdx.y, j = blockIdx.x * kWeightKeys + threadIdx.x * 4;
   let_next_kernel_start();
-  // (No CTA ends before the kernels before this one: the next one waits for this one alone.)
   const Seq q = seq_at(p.s, c.page, b);
   const int pg = j < q.n ? p.s.table[(int64_t)b * p.s.max_pages + (j >> c.page_lg)] : -1;
+  const bool none = pg < 0 || pg >= c.pages;
+  if (none && !first_block()) return;
   after_previous_kernel();
-  if (pg < 0 || pg >= c.pages) return;
+  if (none) return;
   float* weight = c.weight + ((int64_t)pg * c.Hkv + h) * c.page + (j & (c.page - 1));
   const float* s = p.scores + (((int64_t)b * c.Hkv + h) * p.score_rows) * p.score_cap + j;
   float sum[4] = {0.f, 0.f, 0.f, 0.f};

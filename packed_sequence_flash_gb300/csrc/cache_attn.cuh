@@ -807,14 +807,14 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
   auto zero8 = [&](int64_t row, int hq, int d) {
     *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + p.o_ss * row + p.o_sh * hq + d) = make_uint4(0, 0, 0, 0);
   };
-  // Until the attention kernel is done (no CTA ends before it: what comes next
-  // waits for this kernel alone): where this unit's partial results are.
+  // Until the attention kernel is done: where this unit's partial results are.
   const bool tail = b == p.s.B;
   CaSeq s = {};
   if (!tail) s = ca_seq(p, b);
   const int h = blockIdx.x / p.row_tiles, rt = blockIdx.x % p.row_tiles;
   const int part = kCaRows / gridDim.z, rows = s.q.m * p.G, n0 = rt * kCaRows + blockIdx.z * part;
   const int live = tail || rt >= s.rt ? 0 : min(part, rows - n0);
+  if (!tail && live <= 0 && !first_block()) return;
   int64_t before = 0, total = 0;
   for (int x = tid; x < p.s.B; x += kJoinThreads) {
     const int64_t n = ca_seq(p, x).places(p.c.Hkv);
@@ -841,6 +841,8 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
   const int64_t x0 = before + ((int64_t)h * s.rt + rt) * s.cost() + kCaUnit;  // the unit's first tile
   const bool split = live > 0 && s.kt > 0;
   const int c0 = split ? shares.owner(x0) : 0, c1 = split ? shares.owner(x0 + s.kt - 1) : 0;
+  const bool done = split && c0 == c1;  // one CTA had it all and wrote it
+  if (done && !first_block()) return;
   after_previous_kernel();
   if (tail) {  // rows past the last sequence
     if (blockIdx.z) return;
@@ -854,7 +856,7 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
     }
     return;
   }
-  if (live <= 0) return;
+  if (live <= 0 || done) return;
   if (s.kt == 0) {  // a sequence without keys
     for (int x = tid; x < live * (DV / 8); x += kJoinThreads) {
       const int r = x / (DV / 8), y = n0 + r, i = y / p.G;
@@ -866,7 +868,6 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
     }
     return;
   }
-  if (c0 == c1) return;  // one CTA had it all and wrote it
   const int np = c1 - c0 + 1, at0 = blockIdx.z * part;
   auto row_at = [&](int i, int r) -> int64_t { return ((int64_t)(c0 + i) * 2 + (i == 0)) * kCaRows + at0 + r; };
   // A thread takes four columns of a row over every groups-th partial result, with

@@ -40,6 +40,10 @@ __device__ __forceinline__ void let_next_kernel_start() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// The kernel that comes next waits for this one alone, so this one must not be
+// over before the one in front of it: its first block always waits, whatever the others do.
+__device__ __forceinline__ bool first_block() { return blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0; }
+
 // A launch that may begin while the kernel before it in the stream still runs;
 // its kernel waits with griddepcontrol.wait before it touches memory.
 template <typename... A>
