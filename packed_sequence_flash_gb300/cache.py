@@ -33,6 +33,9 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 @functools.lru_cache(maxsize=None)
 def _call(name):
     return getattr(_lib.load(), name)
@@ -76,7 +79,7 @@ def _dtype16(t, name):
 
 def _launch(device, call, *args) -> None:
     """call(*args, stream) with `device` current (a call's tensors may be on another than the current one)."""
-    if torch.cuda.current_device() == device:
+    if _current_device() == device:
         rc = call(*args, _raw_stream(device))
     else:
         with torch.cuda.device(device):
@@ -103,28 +106,30 @@ class KVCache:
         if device < 0:
             _wrong_device(k, "cache k")
         kp, vp = _view(k, "cache k", _E4M3, device), _view(v, "cache v", _E4M3, device)
-        shape = k.shape
-        if len(shape) != 4 or v.shape[:3] != shape[:3] or v.dim() != 4:
-            raise ValueError("cache k and v must be [num_pages, Hkv, page_size, D] with equal leading dims")
-        num_pages, Hkv, page_size, Dqk = shape
-        Dv = v.size(3)
         _tensor(k_scale, "k_scale", torch.float32, device)
         _tensor(v_scale, "v_scale", torch.float32, device)
-        if k_scale.shape != shape[:2] or v_scale.shape != shape[:2]:
-            raise ValueError(f"k_scale and v_scale must be {list(shape[:2])}")
+        if k.dim() != 4 or v.dim() != 4:
+            raise ValueError("cache k and v must be [num_pages, Hkv, page_size, D]")
+        num_pages, Hkv, page_size, Dqk = k.shape
+        Dv = v.size(3)
+        if v.shape != (num_pages, Hkv, page_size, Dv):
+            raise ValueError("cache k and v must have equal leading dims [num_pages, Hkv, page_size]")
+        if k_scale.shape != (num_pages, Hkv) or v_scale.shape != (num_pages, Hkv):
+            raise ValueError(f"k_scale and v_scale must be {[num_pages, Hkv]}")
+        wp = None
         if weight is not None:
             _tensor(weight, "weight", torch.float32, device)
-            if weight.shape != shape[:3]:
-                raise ValueError(f"weight must be {list(shape[:3])}, got {list(weight.shape)}")
+            if weight.shape != (num_pages, Hkv, page_size):
+                raise ValueError(f"weight must be {[num_pages, Hkv, page_size]}, got {list(weight.shape)}")
+            wp = weight.data_ptr()
         self.k, self.v, self.k_scale, self.v_scale, self.weight = k, v, k_scale, v_scale, weight
         self.num_pages, self.Hkv, self.page_size, self.Dqk, self.Dv = num_pages, Hkv, page_size, Dqk, Dv
         self.device = device
-        c = _lib.KVCacheStruct(kp, vp, k_scale.data_ptr(), v_scale.data_ptr(), _ptr(weight), num_pages, page_size, Hkv,
-                               Dqk, Dv)
+        c = self._struct = _lib.KVCacheStruct(kp, vp, k_scale.data_ptr(), v_scale.data_ptr(), wp, num_pages, page_size,
+                                              Hkv, Dqk, Dv)
         if not (k.is_contiguous() and v.is_contiguous()):
             c.k_strides[:] = k.stride()[:3]
             c.v_strides[:] = v.stride()[:3]
-        self._struct = c
         self._ref = ctypes.byref(c)
 
 
@@ -142,14 +147,14 @@ def _sequences(cache, page_table, seq_lens, cu=None, name=""):
     device = cache.device
     _tensor(page_table, "page_table", torch.int32, device)
     _tensor(seq_lens, "seq_lens", torch.int32, device)
-    if page_table.dim() != 2 or seq_lens.dim() != 1 or seq_lens.size(0) != page_table.size(0):
+    shape = page_table.shape
+    if len(shape) != 2 or seq_lens.shape != shape[:1]:
         raise ValueError("page_table must be [B, max_pages] and seq_lens [B]")
-    B, max_pages = page_table.shape
     if cu is not None:
         _tensor(cu, name, torch.int32, device)
-        if cu.dim() != 1 or cu.size(0) != B + 1:
+        if cu.shape != (shape[0] + 1,):
             raise ValueError(f"{name} must be [B + 1]")
-    return B, max_pages
+    return shape
 
 
 def _thd_strides(a, b):
