@@ -678,7 +678,8 @@ int seq_view(const int32_t* page_table, const int32_t* seq_lens, const int32_t* 
 size_t cache_attn_ws_layout(int B, int max_pages, int page_size, int Hq, int Hkv, int Dqk, int Dv, int max_q,
                             int accumulate, CacheAttnParams* p, void* base) {
   const int64_t rows = (int64_t)max_q * (Hq / Hkv), cap = (int64_t)max_pages * page_size;
-  const size_t slots = 2 * (size_t)kMaxSms * cache_attn_ctas(Dqk) * kCacheAttnRows;  // rows of partial results
+  const int nt = cache_attn_nt(Dqk, rows);
+  const size_t slots = 2 * (size_t)kMaxSms * cache_attn_ctas(Dqk, nt) * 8 * nt;  // rows of partial results
   const size_t l_off = align256(sizeof(float) * slots * Dv);
   const size_t s_off = l_off + align256(sizeof(float) * slots);
   if (p && base) {

@@ -47,42 +47,44 @@ __global__ void __launch_bounds__(kWeightThreads) cache_weight_kernel(const __gr
   }
 }
 
-template <int DQK, int DV, bool EXTRA>
+template <int DQK, int DV, int NT, bool EXTRA>
 cudaError_t run(CacheAttnParams& p, int max_q, int sms, cudaStream_t st) {
-  using C = CaCfg<DQK, DV>;
+  using C = CaCfg<DQK, DV, NT>;
   static std::atomic<uint64_t> main_set{0}, join_set{0};
-  cudaError_t e = kernel_setup(cache_attn_kernel<DQK, DV, EXTRA>, C::SMEM, true, main_set);
-  if (e == cudaSuccess) e = kernel_setup(cache_join_kernel<DQK, DV>, 0, true, join_set);
+  cudaError_t e = kernel_setup(cache_attn_kernel<DQK, DV, NT, EXTRA>, C::SMEM, true, main_set);
+  if (e == cudaSuccess) e = kernel_setup(cache_join_kernel<DV>, 0, true, join_set);
   if (e != cudaSuccess) return e;
   const int grid = sms * C::CTAS;
-  p.row_tiles = max(1, (int)(((int64_t)max_q * p.G + kCaRows - 1) / kCaRows));
-  e = launch_early(cache_attn_kernel<DQK, DV, EXTRA>, dim3(grid), kCaThreads, C::SMEM, st, p);
+  p.tile_lg = NT == 1 ? 3 : 4;
+  p.row_tiles = max(1, (int)(((int64_t)max_q * p.G + C::R - 1) / C::R));
+  e = launch_early(cache_attn_kernel<DQK, DV, NT, EXTRA>, dim3(grid), kCaThreads, C::SMEM, st, p);
   if (e != cudaSuccess) return e;
   const int64_t units = (int64_t)p.c.Hkv * p.row_tiles * p.s.B;
   int parts = 1;
-  while (parts < kCaRows && units * parts * 2 <= 2 * sms) parts *= 2;
-  return launch_early(cache_join_kernel<DQK, DV>, dim3(p.c.Hkv * p.row_tiles, p.s.B + (p.s.cu ? 1 : 0), parts),
+  while (parts < C::R && units * parts * 2 <= 2 * sms) parts *= 2;
+  return launch_early(cache_join_kernel<DV>, dim3(p.c.Hkv * p.row_tiles, p.s.B + (p.s.cu ? 1 : 0), parts),
                       kJoinThreads, 0, st, p, grid);
 }
 
-template <int DQK, int DV>
+template <int DQK, int DV, int NT>
 cudaError_t run(CacheAttnParams& p, int max_q, int sms, cudaStream_t st) {
-  return p.accumulate || p.softcap > 0.f ? run<DQK, DV, true>(p, max_q, sms, st)
-                                         : run<DQK, DV, false>(p, max_q, sms, st);
+  return p.accumulate || p.softcap > 0.f ? run<DQK, DV, NT, true>(p, max_q, sms, st)
+                                         : run<DQK, DV, NT, false>(p, max_q, sms, st);
 }
 
 }  // namespace
 
 cudaError_t launch_cache_attn(CacheAttnParams& p, int max_q, int sms, cudaStream_t st) {
+  const bool one = cache_attn_nt(p.c.Dqk, (int64_t)max_q * p.G) == 1;
   cudaError_t e;
   if (p.c.Dqk == 64)
-    e = run<64, 64>(p, max_q, sms, st);
+    e = one ? run<64, 64, 1>(p, max_q, sms, st) : run<64, 64, 2>(p, max_q, sms, st);
   else if (p.c.Dqk == 128)
-    e = run<128, 128>(p, max_q, sms, st);
+    e = one ? run<128, 128, 1>(p, max_q, sms, st) : run<128, 128, 2>(p, max_q, sms, st);
   else if (p.c.Dqk == 192)
-    e = run<192, 128>(p, max_q, sms, st);
+    e = one ? run<192, 128, 1>(p, max_q, sms, st) : run<192, 128, 2>(p, max_q, sms, st);
   else
-    e = run<512, 512>(p, max_q, sms, st);
+    e = run<512, 512, 1>(p, max_q, sms, st);
   if (e != cudaSuccess || !p.accumulate) return e;
   static std::atomic<uint64_t> weight_set{0};
   if ((e = kernel_setup(cache_weight_kernel, 0, true, weight_set)) != cudaSuccess) return e;

@@ -12,7 +12,7 @@
 // codes are expanded in place, so the legacy instruction is the fitting one.
 //
 // Rows: the query rows of one KV head (m rows x G heads, token-major) in tiles
-// of 8. Keys: tiles of 64. A CTA takes an equal share of all
+// of R = 8 NT rows: 8 for one group of heads and one token, 16 where there are more rows. Keys: tiles of 64. A CTA takes an equal share of all
 // (sequence, KV head, row tile, key tile) in that order, wherever it begins and
 // ends, so ragged batches and a single long sequence alike fill the device.
 // A share that covers all tiles of a (sequence, head, row tile) writes its
@@ -50,7 +50,6 @@
 namespace psf {
 
 constexpr int kCaKeys = 64;       // keys per tile
-constexpr int kCaRows = kCacheAttnRows;
 constexpr int kCaWarps = 4;       // consumer warps, 16 keys of a tile each
 constexpr int kCaConsumers = 32 * kCaWarps;
 constexpr int kCaThreads = kCaConsumers + 32;
@@ -59,18 +58,19 @@ constexpr float kCaLazy = 8.f;    // a reference moves when a score is 2^8 above
 constexpr float kCaHead = 7.f;    // the P reference sits 2^7 below the largest value
 constexpr float kCaFloor = -3e38f;  // references before the first score (finite: no inf - inf)
 
-template <int DQK, int DV>
+template <int DQK, int DV, int NT>
 struct CaCfg {
+  static constexpr int R = 8 * NT;
   static constexpr int KP = DQK <= 128 ? 1 : (DQK + 127) / 128;  // 128-byte planes of a K row
   static constexpr int VP = DV <= 128 ? 1 : (DV + 127) / 128;
   static constexpr int ROWB = DQK == 64 ? 64 : 128;  // bytes of a row in a plane
   static constexpr int PLANE = kCaKeys * ROWB;
   static constexpr int STAGE = (KP + VP) * PLANE;
-  static constexpr int CTAS = cache_attn_ctas(DQK);
-  static constexpr int RAW = kCaRows * DQK * 2;        // queries as they come, one of kCaUnits buffers
+  static constexpr int CTAS = cache_attn_ctas(DQK, NT);
+  static constexpr int RAW = R * DQK * 2;        // queries as they come, one of kCaUnits buffers
   static constexpr int QPITCH = DQK + 8;         // fp16 elements of a query row
   static constexpr int OPITCH = DV + 4;          // fp32 elements
-  static constexpr int OBYTES = kCaWarps * kCaRows * OPITCH * 4;
+  static constexpr int OBYTES = kCaWarps * R * OPITCH * 4;
   static constexpr int FIXED = kCaUnits * RAW + OBYTES + 1024;
   // As many stages as fit beside 2 KB of static and 1 KB of reserved shared
   // memory: 64 KB or more of the cache in flight per SM.
@@ -81,8 +81,8 @@ struct CaCfg {
   static constexpr int Q_OFF = O_OFF;  // the queries are done with before O is written
   static constexpr int SMEM = STAGES * STAGE + FIXED;
   static_assert(STAGES >= 2 && CTAS * STAGES * STAGE >= 64 * 1024, "bytes in flight");
-  static_assert(kCaRows * QPITCH * 2 <= OBYTES, "queries fit where O goes");
-  static constexpr bool QREGS = DQK <= 192;  // Q operand kept in registers
+  static_assert(R * QPITCH * 2 <= OBYTES, "queries fit where O goes");
+  static constexpr bool QREGS = NT * DQK <= 256;  // Q operand kept in registers
 };
 
 // a / b, in 32 bits when both fit (most of the time).
@@ -110,7 +110,7 @@ __device__ __forceinline__ CaSeq ca_seq(const CacheAttnParams& p, int b) {
   const int lo = p.window > 0 ? max(0, s.q.n - s.q.m - p.window + 1) : 0;
   s.t0 = lo / kCaKeys;
   s.kt = s.q.m > 0 ? max(0, (s.q.n + kCaKeys - 1) / kCaKeys - s.t0) : 0;
-  s.rt = (s.q.m * p.G + kCaRows - 1) / kCaRows;
+  s.rt = (s.q.m * p.G + (1 << p.tile_lg) - 1) >> p.tile_lg;
   return s;
 }
 // CTAs that share `total` places, and how they do.
@@ -213,7 +213,7 @@ struct CaWalk {
       u.t1 = s.t0 + k1;
       u.whole = k1 - k0 == s.kt;
       u.slot = k0 == 0;
-      const int i0 = u.rt * kCaRows / p.G, i1 = (min((u.rt + 1) * kCaRows, u.m * p.G) - 1) / p.G;
+      const int i0 = (u.rt << p.tile_lg) / p.G, i1 = (min((u.rt + 1) << p.tile_lg, u.m * p.G) - 1) / p.G;
       ca_row_keys(p, u.n, u.m, i0, u.lo, u.in_hi);
       ca_row_keys(p, u.n, u.m, i1, u.in_lo, u.hi);
       u.ta = max(u.t0, u.lo / kCaKeys);
@@ -225,19 +225,19 @@ struct CaWalk {
 };
 
 // EXTRA: logits are capped or scores kept (p.softcap, p.accumulate).
-template <int DQK, int DV, bool EXTRA>
-__global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV>::CTAS)
+template <int DQK, int DV, int NT, bool EXTRA>
+__global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV, NT>::CTAS)
     cache_attn_kernel(const __grid_constant__ CacheAttnParams p) {
-  using C = CaCfg<DQK, DV>;
+  using C = CaCfg<DQK, DV, NT>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ uint64_t full[C::STAGES], empty[C::STAGES];
   __shared__ float2 meta[C::STAGES][kCaWarps];  // K scale and log2 of the V scale of 16 keys
   __shared__ uint64_t q_full[kCaUnits], q_empty[kCaUnits];
   __shared__ CaUnit unit_at[kCaUnits];  // b < 0: no more units
-  __shared__ float row_fac[kCaRows];  // query scale times the logit scale
-  __shared__ int2 row_lim[kCaRows];   // keys that a row sees
-  __shared__ float st_mu[kCaWarps][kCaRows], st_l[kCaWarps][kCaRows], fin_l[kCaRows];
+  __shared__ float row_fac[C::R];  // query scale times the logit scale
+  __shared__ int2 row_lim[C::R];   // keys that a row sees
+  __shared__ float st_mu[kCaWarps][C::R], st_l[kCaWarps][C::R], fin_l[C::R];
   __shared__ int64_t scan[kCaThreads / 32], found_base;
   __shared__ int found_b, abort_flag;
 
@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV>::CTAS)
     auto announce = [&](bool more, const CaUnit& u) {
       const int qb = nu % kCaUnits;
       if (nu >= kCaUnits && !wait_bar(&q_empty[qb], (nu / kCaUnits - 1) & 1, ctl)) return false;
-      const int n0 = u.rt * kCaRows, rows = more ? min(u.m * p.G - n0, kCaRows) : 0;
+      const int n0 = u.rt * C::R, rows = more ? min(u.m * p.G - n0, C::R) : 0;
       if (lane == 0) {
         if (more)
           unit_at[qb] = u;
@@ -474,10 +474,10 @@ __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV>::CTAS)
     if (!consumers_all(wait_bar(&q_full[qb], (nu / kCaUnits) & 1, ctl))) break;
     const CaUnit& u = unit_at[qb];
     if (u.b < 0) break;
-    const int rows = u.m * p.G, n0 = u.rt * kCaRows, lo = u.lo, hi = u.hi;
+    const int rows = u.m * p.G, n0 = u.rt * C::R, lo = u.lo, hi = u.hi;
     // Queries to fp16, each row scaled by a power of two: a warp two rows.
 #pragma unroll
-    for (int e2 = 0; e2 < 2; ++e2) {
+    for (int e2 = 0; e2 < 2 * NT; ++e2) {
       constexpr int E = DQK / 32;  // elements per lane and row
       const int r = warp + e2 * kCaWarps;
       const uint32_t* from = reinterpret_cast<const uint32_t*>(smem + C::RAW_OFF + qb * C::RAW + r * DQK * 2) + lane * (E / 2);
@@ -505,32 +505,37 @@ __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV>::CTAS)
       }
     }
     consumers_sync();
-    uint32_t qf[C::QREGS ? DQK / 8 : 1];
+    uint32_t qf[NT][C::QREGS ? DQK / 8 : 1];
     if constexpr (C::QREGS) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int j = 0; j < DQK / 64; ++j)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          const uint4 a = lds128(qs + j * 128 + x * 16);
-          qf[j * 8 + x * 4] = a.x;
-          qf[j * 8 + x * 4 + 1] = a.y;
-          qf[j * 8 + x * 4 + 2] = a.z;
-          qf[j * 8 + x * 4 + 3] = a.w;
+          const uint4 a = lds128(qs + nt * 8 * C::QPITCH * 2 + j * 128 + x * 16);
+          qf[nt][j * 8 + x * 4] = a.x;
+          qf[nt][j * 8 + x * 4 + 1] = a.y;
+          qf[nt][j * 8 + x * 4 + 2] = a.z;
+          qf[nt][j * 8 + x * 4 + 3] = a.w;
         }
     }
-    // Columns of this lane: rows r0 + 2 t and + 1 of the tile.
-    const float fac[2] = {row_fac[2 * t], row_fac[2 * t + 1]};
-    float mu[2], ro[2], l[2];
-    float o[MT][4];
+    float fac[NT][2], mu[NT][2], ro[NT][2], l[NT][2];
+    float o[MT][NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      mu[c] = ro[c] = kCaFloor;
-      l[c] = 0.f;
+      fac[nt][c] = row_fac[nt * 8 + 2 * t + c];
+      mu[nt][c] = ro[nt][c] = kCaFloor;
+      l[nt][c] = 0.f;
     }
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) o[m][c] = 0.f;
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) o[m][nt][c] = 0.f;
 
     // Where this lane's first row keeps its scores.
     float* scores = EXTRA && p.accumulate
@@ -540,104 +545,117 @@ __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV>::CTAS)
       constexpr bool MASK = decltype(mask_tag)::value;
       const uint8_t* sb = smem + st * C::STAGE;
       const int key = tile * kCaKeys + ka;
-      float s[4], s2[4];
+      float s[NT][4], s2[NT][4];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) s[c] = s2[c] = 0.f;
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) s[nt][c] = s2[nt][c] = 0.f;
 #pragma unroll
       for (int j = 0; j < DQK / 64; ++j) {
         const uint4 xa = lds128(sb + k_off(ka, j)), xb = lds128(sb + k_off(ka + 8, j));
         const uint32_t wa[4] = {xa.x, xa.y, xa.z, xa.w}, wb[4] = {xb.x, xb.y, xb.z, xb.w};
-        uint32_t qv[8];
+        uint32_t qv[NT][8];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
         if constexpr (C::QREGS) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) qv[e] = qf[j * 8 + e];
+          for (int e = 0; e < 8; ++e) qv[nt][e] = qf[nt][j * 8 + e];
         } else {
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            const uint4 a = lds128(qs + j * 128 + x * 16);
-            qv[x * 4] = a.x;
-            qv[x * 4 + 1] = a.y;
-            qv[x * 4 + 2] = a.z;
-            qv[x * 4 + 3] = a.w;
+            const uint4 a = lds128(qs + nt * 8 * C::QPITCH * 2 + j * 128 + x * 16);
+            qv[nt][x * 4] = a.x;
+            qv[nt][x * 4 + 1] = a.y;
+            qv[nt][x * 4 + 2] = a.z;
+            qv[nt][x * 4 + 3] = a.w;
           }
         }
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
           const uint32_t a0 = e4m3_to_half2(wa[w] & 0xffff), a2 = e4m3_to_half2(wa[w] >> 16);
           const uint32_t a1 = e4m3_to_half2(wb[w] & 0xffff), a3 = e4m3_to_half2(wb[w] >> 16);
-          mma16816((w & 1) ? s2 : s, a0, a1, a2, a3, qv[2 * w], qv[2 * w + 1]);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma16816((w & 1) ? s2[nt] : s[nt], a0, a1, a2, a3, qv[nt][2 * w], qv[nt][2 * w + 1]);
         }
       }
-      // Exponents of the row sum's terms (x) and of P (y) against the references:
-      // x = z - mu, y = z + log2 v_scale - ro, z the score in log2 units.
       const float2 sc = meta[st][warp];
-      float x[4], y[4];
-      float f[2] = {fac[0] * sc.x, fac[1] * sc.x};
+      float x[NT][4], y[NT][4], f[NT][2];
+      bool move = false;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) s[c] += s2[c];
+      for (int nt = 0; nt < NT; ++nt) {
+      f[nt][0] = fac[nt][0] * sc.x; f[nt][1] = fac[nt][1] * sc.x;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) s[nt][c] += s2[nt][c];
       if (EXTRA && p.softcap > 0.f) {
-        // c tanh(a) log2(e), tanh(a) = 1 - 2 / (e^(2a) + 1): off by some 2^-22 of the cap
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          const float e = ex2_approx(s[c] * f[c & 1] * 2.8853900817779268f);
-          s[c] = p.softcap * 1.4426950408889634f * fmaf(-2.f, rcp_approx(e + 1.f), 1.f);
+          const float e = ex2_approx(s[nt][c] * f[nt][c & 1] * 2.8853900817779268f);
+          s[nt][c] = p.softcap * 1.4426950408889634f * fmaf(-2.f, rcp_approx(e + 1.f), 1.f);
         }
-        f[0] = f[1] = 1.f;
+        f[nt][0] = f[nt][1] = 1.f;
       }
       if (EXTRA && p.accumulate) {
         float* at = scores + key;
 #pragma unroll
         for (int c = 0; c < 4; ++c)
-          if (n0 + 2 * t + (c & 1) < rows && key + (c >> 1) * 8 < hi)
-            at[(c & 1) * p.score_cap + (c >> 1) * 8] = s[c] * f[c & 1];
+          if (n0 + nt * 8 + 2 * t + (c & 1) < rows && key + (c >> 1) * 8 < hi)
+            at[(nt * 8 + (c & 1)) * p.score_cap + (c >> 1) * 8] = s[nt][c] * f[nt][c & 1];
       }
-      const float dy[2] = {sc.y - ro[0], sc.y - ro[1]};
+      const float dy[2] = {sc.y - ro[nt][0], sc.y - ro[nt][1]};
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        x[c] = fmaf(s[c], f[c & 1], -mu[c & 1]);
-        y[c] = fmaf(s[c], f[c & 1], dy[c & 1]);
+        x[nt][c] = fmaf(s[nt][c], f[nt][c & 1], -mu[nt][c & 1]);
+        y[nt][c] = fmaf(s[nt][c], f[nt][c & 1], dy[c & 1]);
         if constexpr (MASK) {
-          const int2 lim = row_lim[2 * t + (c & 1)];
+          const int2 lim = row_lim[nt * 8 + 2 * t + (c & 1)];
           const int k = key + (c >> 1) * 8;
-          if (k < lim.x || k >= lim.y) s[c] = x[c] = y[c] = -CUDART_INF_F;
+          if (k < lim.x || k >= lim.y) s[nt][c] = x[nt][c] = y[nt][c] = -CUDART_INF_F;
         }
       }
-      const bool move = fmaxf(fmax3(x[0], x[1], x[2]), x[3]) > kCaLazy ||
-                        fmaxf(fmax3(y[0], y[1], y[2]), y[3]) > kCaHead + kCaLazy;
+      move |= fmaxf(fmax3(x[nt][0], x[nt][1], x[nt][2]), x[nt][3]) > kCaLazy ||
+                        fmaxf(fmax3(y[nt][0], y[nt][1], y[nt][2]), y[nt][3]) > kCaHead + kCaLazy;
+      }
       if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
         float of[2];
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           float z[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e)
-            z[e] = MASK && s[c + 2 * e] == -CUDART_INF_F ? -CUDART_INF_F : s[c + 2 * e] * f[c];
+            z[e] = MASK && s[nt][c + 2 * e] == -CUDART_INF_F ? -CUDART_INF_F : s[nt][c + 2 * e] * f[nt][c];
           float top = fmaxf(z[0], z[1]);
 #pragma unroll
           for (int e = 4; e < 32; e <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, e));
-          const float m1 = fmaxf(mu[c], top), r1 = fmaxf(ro[c], top + sc.y - kCaHead);
-          l[c] *= ex2_approx(mu[c] - m1);
-          of[c] = ex2_approx(ro[c] - r1);
-          mu[c] = m1;
-          ro[c] = r1;
+          const float m1 = fmaxf(mu[nt][c], top), r1 = fmaxf(ro[nt][c], top + sc.y - kCaHead);
+          l[nt][c] *= ex2_approx(mu[nt][c] - m1);
+          of[c] = ex2_approx(ro[nt][c] - r1);
+          mu[nt][c] = m1;
+          ro[nt][c] = r1;
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            x[c + 2 * e] = z[e] - m1;
-            y[c + 2 * e] = z[e] + (sc.y - r1);
+            x[nt][c + 2 * e] = z[e] - m1;
+            y[nt][c + 2 * e] = z[e] + (sc.y - r1);
           }
         }
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) o[m][c] *= of[c & 1];
+          for (int c = 0; c < 4; ++c) o[m][nt][c] *= of[c & 1];
+        }
       }
+      uint32_t p0[NT], p1[NT];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
       float w[4];
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        l[c & 1] += ex2_approx(x[c]);
-        w[c] = ex2_approx(y[c]);
+        l[nt][c & 1] += ex2_approx(x[nt][c]);
+        w[c] = ex2_approx(y[nt][c]);
       }
-      const uint32_t p0 = transpose8x8(pack2<__half>(w[0], w[1])), p1 = transpose8x8(pack2<__half>(w[2], w[3]));
+      p0[nt] = transpose8x8(pack2<__half>(w[0], w[1])); p1[nt] = transpose8x8(pack2<__half>(w[2], w[3]));
+      }
       uint32_t nan_seen = 0;
 #pragma unroll
       for (int j = 0; j < C::VP; ++j) {
@@ -675,10 +693,13 @@ __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV>::CTAS)
           const uint32_t y0 = __byte_perm(v[0][e], v[1][e], 0x5140), y1 = __byte_perm(v[0][e], v[1][e], 0x7362);
           const uint32_t z0 = __byte_perm(v[2][e], v[3][e], 0x5140), z1 = __byte_perm(v[2][e], v[3][e], 0x7362);
           const int m = j * 8 + e * 2;
-          mma16816(o[m], e4m3_to_half2(y0 & 0xffff), e4m3_to_half2(y0 >> 16), e4m3_to_half2(z0 & 0xffff),
-                   e4m3_to_half2(z0 >> 16), p0, p1);
-          mma16816(o[m + 1], e4m3_to_half2(y1 & 0xffff), e4m3_to_half2(y1 >> 16), e4m3_to_half2(z1 & 0xffff),
-                   e4m3_to_half2(z1 >> 16), p0, p1);
+          const uint32_t A0=e4m3_to_half2(y0 & 0xffff), A1=e4m3_to_half2(y0 >> 16), A2=e4m3_to_half2(z0 & 0xffff), A3=e4m3_to_half2(z0 >> 16);
+          const uint32_t B0=e4m3_to_half2(y1 & 0xffff), B1=e4m3_to_half2(y1 >> 16), B2=e4m3_to_half2(z1 & 0xffff), B3=e4m3_to_half2(z1 >> 16);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+          mma16816(o[m][nt], A0, A1, A2, A3, p0[nt], p1[nt]);
+          mma16816(o[m + 1][nt], B0, B1, B2, B3, p0[nt], p1[nt]);
+          }
         }
       }
       if constexpr (MASK) {
@@ -693,9 +714,9 @@ __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV>::CTAS)
                 const uint32_t code = sb[v_off(row, m >> 3) + (m & 7) * 2 + e];
                 if ((code & 0x7f) == 0x7f)
 #pragma unroll
-                  for (int c = 0; c < 2; ++c) {
-                    const int2 lim = row_lim[2 * t + c];
-                    if (k >= lim.x && k < lim.y) o[m][2 * e + c] = CUDART_NAN_F;
+                  for (int c = 0; c < 2 * NT; ++c) {
+                    const int2 lim = row_lim[(c >> 1) * 8 + 2 * t + (c & 1)];
+                    if (k >= lim.x && k < lim.y) o[m][c >> 1][2 * e + (c & 1)] = CUDART_NAN_F;
                   }
               }
           }
@@ -722,46 +743,49 @@ __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV>::CTAS)
 
     // ---------------------------------------------------------- end of the unit: four states into one
 #pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
     for (int c = 0; c < 2; ++c) {
 #pragma unroll
-      for (int x = 4; x < 32; x <<= 1) l[c] += __shfl_xor_sync(0xffffffffu, l[c], x);
+      for (int x = 4; x < 32; x <<= 1) l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], x);
       if (g == 0) {
-        st_mu[warp][2 * t + c] = mu[c];
-        st_l[warp][2 * t + c] = l[c];
+        st_mu[warp][nt * 8 + 2 * t + c] = mu[nt][c];
+        st_l[warp][nt * 8 + 2 * t + c] = l[nt][c];
       }
     }
     consumers_sync();
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
     float f[2];
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      const int r = 2 * t + c;
+      const int r = nt * 8 + 2 * t + c;
       float top = kCaFloor, sum = 0.f;
 #pragma unroll
       for (int w = 0; w < kCaWarps; ++w) top = fmaxf(top, st_mu[w][r]);
 #pragma unroll
       for (int w = 0; w < kCaWarps; ++w) sum += st_l[w][r] * ex2_approx(st_mu[w][r] - top);
-      // sum > 0 unless the row saw nothing; NaN stays NaN
-      f[c] = sum == 0.f ? 0.f : ex2_approx(ro[c] - top) / sum;
+      f[c] = sum == 0.f ? 0.f : ex2_approx(ro[nt][c] - top) / sum;
       if (warp == 0 && g == 0) fin_l[r] = sum == 0.f ? -CUDART_INF_F : top + log2f(sum);
     }
-    // O into shared memory, a buffer per warp, added up on the way out.
 #pragma unroll
     for (int m = 0; m < MT; m += 2) {
       const int d = DV == 64 ? g * 8 + m * 2 : (m >> 3) * 128 + g * 16 + (m & 7) * 2;
 #pragma unroll
       for (int c = 0; c < 2; ++c)
-        *reinterpret_cast<float4*>(ob + (warp * kCaRows + 2 * t + c) * C::OPITCH + d) =
-            make_float4(o[m][c] * f[c], o[m][2 + c] * f[c], o[m + 1][c] * f[c], o[m + 1][2 + c] * f[c]);
+        *reinterpret_cast<float4*>(ob + (warp * C::R + nt * 8 + 2 * t + c) * C::OPITCH + d) =
+            make_float4(o[m][nt][c] * f[c], o[m][nt][2 + c] * f[c], o[m + 1][nt][c] * f[c], o[m + 1][nt][2 + c] * f[c]);
+    }
     }
     consumers_sync();
-    const int live = min(kCaRows, rows - n0);
+    const int live = min(C::R, rows - n0);
     const int64_t slot = (int64_t)blockIdx.x * 2 + u.slot;
     for (int x = tid; x < live * (DV / 4); x += kCaConsumers) {
       const int r = x / (DV / 4), d = (x - r * (DV / 4)) * 4, z = n0 + r, i = z / p.G;
       float4 a = *reinterpret_cast<const float4*>(ob + r * C::OPITCH + d);
 #pragma unroll
       for (int w = 1; w < kCaWarps; ++w) {
-        const float4 b = *reinterpret_cast<const float4*>(ob + (w * kCaRows + r) * C::OPITCH + d);
+        const float4 b = *reinterpret_cast<const float4*>(ob + (w * C::R + r) * C::OPITCH + d);
         a.x += b.x;
         a.y += b.y;
         a.z += b.z;
@@ -773,7 +797,7 @@ __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV>::CTAS)
         *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + p.o_ss * (u.q0 + i) +
                                   p.o_sh * (u.h * p.G + z - i * p.G) + d) = w;
       } else {
-        *reinterpret_cast<float4*>(p.part_o + (slot * kCaRows + r) * DV + d) = a;
+        *reinterpret_cast<float4*>(p.part_o + (slot * C::R + r) * DV + d) = a;
       }
     }
     if (tid < live) {
@@ -781,7 +805,7 @@ __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV>::CTAS)
       if (u.whole)
         p.lse[(int64_t)(u.h * p.G + z - i * p.G) * p.s.T + u.q0 + i] = fin_l[tid] * 0.69314718055994531f;
       else
-        p.part_l[slot * kCaRows + tid] = fin_l[tid];
+        p.part_l[slot * C::R + tid] = fin_l[tid];
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&q_empty[qb]);
@@ -795,9 +819,8 @@ __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV>::CTAS)
 // are few units, whose partial results are then many (57 per unit for one
 // sequence of 32 Ki keys and 8 heads: 15 us with one CTA each).
 constexpr int kJoinThreads = 512;
-template <int DQK, int DV>
+template <int DV>
 __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_constant__ CacheAttnParams p, int grid) {
-  using C = CaCfg<DQK, DV>;
   __shared__ int64_t sum_before[kJoinThreads / 32], sum_all[kJoinThreads / 32];
   __shared__ float4 sums[kJoinThreads];
   __shared__ float2 tops[kJoinThreads];
@@ -812,7 +835,7 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
   CaSeq s = {};
   if (!tail) s = ca_seq(p, b);
   const int h = blockIdx.x / p.row_tiles, rt = blockIdx.x % p.row_tiles;
-  const int part = kCaRows / gridDim.z, rows = s.q.m * p.G, n0 = rt * kCaRows + blockIdx.z * part;
+  const int part = (1 << p.tile_lg) / gridDim.z, rows = s.q.m * p.G, n0 = (rt << p.tile_lg) + blockIdx.z * part;
   const int live = tail || rt >= s.rt ? 0 : min(part, rows - n0);
   if (!tail && live <= 0 && !first_block()) return;
   int64_t before = 0, total = 0;
@@ -869,7 +892,7 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
     return;
   }
   const int np = c1 - c0 + 1, at0 = blockIdx.z * part;
-  auto row_at = [&](int i, int r) -> int64_t { return ((int64_t)(c0 + i) * 2 + (i == 0)) * kCaRows + at0 + r; };
+  auto row_at = [&](int i, int r) -> int64_t { return (((int64_t)(c0 + i) * 2 + (i == 0)) << p.tile_lg) + at0 + r; };
   // A thread takes four columns of a row over every groups-th partial result, with
   // a running maximum and sum of its own; the groups are added in their order.
   constexpr int VEC = DV / 4;

@@ -100,6 +100,7 @@ struct CacheAttnParams {
   int f16;
   int min_share;  // a CTA's share is at least this many key tiles
   int row_tiles;  // of a sequence with the most rows
+  int tile_lg;    // log2 of the rows of a tile
   // Workspace: partial results [CTA][2][R][Dv] and their lse in log2 units
   // [CTA][2][R]; scores [B * Hkv][score_rows][score_cap] in log2 units.
   float *part_o, *part_l, *scores;
@@ -107,9 +108,13 @@ struct CacheAttnParams {
   int* status;
   uint64_t limit_ns;
 };
-constexpr int kCacheAttnRows = 8;  // query rows per tile
+// Groups of 8 query rows in a row tile, for the most rows a KV head has in a
+// sequence. Two share what the codes cost to expand: 16 rows over 32 x 32 Ki keys
+// took 361 us as one tile and 627 us as two; with up to 8 rows half of the tile
+// would be empty. One at head dim 512, whose state fills the registers.
+constexpr int cache_attn_nt(int Dqk, int64_t rows) { return Dqk == 512 || rows <= 8 ? 1 : 2; }
 // CTAs per SM: as many as shared memory and registers hold.
-constexpr int cache_attn_ctas(int Dqk) { return Dqk == 512 ? 1 : (Dqk == 192 ? 2 : 3); }
+constexpr int cache_attn_ctas(int Dqk, int nt) { return Dqk == 512 ? 1 : (Dqk == 192 || nt == 2 ? 2 : 3); }
 cudaError_t launch_cache_attn(CacheAttnParams& p, int max_q, int sms, cudaStream_t st);
 
 }  // namespace psf
