@@ -422,10 +422,11 @@ int psf_grad_add_live_rows(void* dst, const void* src, const int32_t* cu_q, cons
  *  ceil(seq_lens[b] / page_size) are not read. Several sequences may name the
  *  same page (a shared prefix) as long as no call writes to it. All of it is
  *  read on the device: nothing synchronises, and the calls can be captured.
- *  A length outside [0, max_pages * page_size], rows outside the packed tensor,
- *  or a page outside [0, num_pages) is a PSF_EDEVICE_ARGS device status; nothing
- *  outside the tensors is touched, a page that does not exist is not written,
- *  and the results of the other sequences stand.
+ *  A length outside [0, max_pages * page_size], prefix sums that do not begin at 0
+ *  or whose rows lie outside the packed tensor, or a page outside [0, num_pages)
+ *  is a PSF_EDEVICE_ARGS device status; nothing outside the tensors is touched, a
+ *  page that does not exist is not written, and the results of the other
+ *  sequences stand.
  */
 typedef struct {
   void* k;

@@ -217,6 +217,7 @@ def attn_cache_fwd(q, cache, page_table, seq_lens, scale, cu_q=None, max_q=None,
         if cu_q is not None:
             raise ValueError("cu_q needs max_q, the most query rows of a sequence")
         max_q = T // B if B else 0
+    max_q = int(max_q)
     if out is None:
         out = torch.empty((T, Hq, cache.Dv), dtype=dtype, device=q.device)
         op = out.data_ptr()
@@ -239,7 +240,7 @@ def attn_cache_fwd(q, cache, page_table, seq_lens, scale, cu_q=None, max_q=None,
         size = workspace.numel() * workspace.element_size()
     _launch(device, _call("psf_attn_cache_fwd"), qp, cache._ref, op, lse.data_ptr(), _ptr(cu_q),
             page_table.data_ptr(), seq_lens.data_ptr(), B, max_pages, T, max_q, Hq, _thd_strides(q, out),
-            _DTYPES[dtype], scale, 1 if causal else 0, _window(window), _cap(softcap),
+            _DTYPES[dtype], float(scale), 1 if causal else 0, _window(window), _cap(softcap),
             PSF_CACHE_ACCUMULATE if accumulate else 0, workspace.data_ptr(), size)
     return out, lse
 
@@ -261,6 +262,7 @@ def kv_cache_evict(cache, page_table, seq_lens, budget, recent, new_lens=None, w
     afterwards. See psf_kv_cache_evict for the scales.
     """
     B, max_pages = _sequences(cache, page_table, seq_lens)
+    budget, recent = int(budget), int(recent)
     if new_lens is None:
         new_lens = torch.empty_like(seq_lens)
     else:
@@ -286,6 +288,7 @@ def kv_cache_gather(cache, page_table, seq_lens, total_k, dtype=torch.bfloat16):
     """
     if dtype not in _DTYPES:
         raise ValueError(f"dtype must be bfloat16 or float16, got {dtype}")
+    total_k = int(total_k)
     if total_k < 0:
         raise ValueError("total_k must not be negative")
     B, max_pages = _sequences(cache, page_table, seq_lens)

@@ -33,12 +33,17 @@ __global__ void __launch_bounds__(kAppendThreads, 8)
   const bool is_v = blockIdx.z;
   auto start = [&](int b) -> int64_t { return (s.cu ? s.cu[b] : b * s.each) / c.page + 2 * (int64_t)b; };
   after_previous_kernel();
+  if (first_block()) {
+    bool bad = cu_bad(s);
+    for (int i = tid; i < s.B; i += kAppendThreads) {
+      const Seq x = seq_at(s, c.page, i);
+      bad |= x.bad || x.m > x.n;
+    }
+    if (bad) record_status(status, kStatusDeviceArgs);
+  }
   const int b = warp_find(s.B, blockIdx.x, start);
   const Seq q = seq_at(s, c.page, b);
-  if (q.bad || q.m > q.n) {
-    if (tid == 0) record_status(status, kStatusDeviceArgs);
-    return;
-  }
+  if (q.bad || q.m > q.n) return;
   const int64_t nth = (int64_t)blockIdx.x - start(b);
   const int first = q.n - q.m;  // position of the first new token
   const int64_t pi = (first >> c.page_lg) + nth;

@@ -54,6 +54,9 @@ __device__ __forceinline__ Seq seq_at(const SeqView& s, int page, int b) {
   return r;
 }
 
+// Whether the prefix sums do not begin at 0 (rows in front of the first sequence would belong to none).
+__device__ __forceinline__ bool cu_bad(const SeqView& s) { return s.cu && s.cu[0] != 0; }
+
 // Scale of a block whose largest magnitude is a (finite, >= 0): the smallest
 // power of two s >= 2^-126 with a <= 448 s (448 = 1.75 * 2^8 is the largest e4m3
 // value). A power of two costs no precision in a floating format and keeps a
@@ -115,7 +118,8 @@ __device__ __forceinline__ int warp_find(int B, int64_t x, F start) {
     const int step = (hi - lo + 31) >> 5;
     const int probe = lo + (int)(threadIdx.x & 31) * step;
     const bool in = probe < hi && start(probe) <= x;
-    const int c = __popc(__ballot_sync(0xffffffffu, in));
+    // (at least one, whatever a caller's array holds: b stays in range)
+    const int c = max(__popc(__ballot_sync(0xffffffffu, in)), 1);
     lo += (c - 1) * step;
     hi = min(hi, lo + step);
   }

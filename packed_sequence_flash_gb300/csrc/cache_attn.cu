@@ -14,7 +14,6 @@ constexpr int kWeightKeys = 4 * kWeightThreads;
 __global__ void __launch_bounds__(kWeightThreads) cache_weight_kernel(const __grid_constant__ CacheAttnParams p) {
   const CacheView& c = p.c;
   const int b = blockIdx.z, h = blockIdx.y, j = blockIdx.x * kWeightKeys + threadIdx.x * 4;
-  let_next_kernel_start();
   const Seq q = seq_at(p.s, c.page, b);
   const int pg = j < q.n ? p.s.table[(int64_t)b * p.s.max_pages + (j >> c.page_lg)] : -1;
   const bool none = pg < 0 || pg >= c.pages;
@@ -56,7 +55,7 @@ cudaError_t run(CacheAttnParams& p, int max_q, int sms, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const int grid = sms * C::CTAS;
   p.tile_lg = NT == 1 ? 3 : 4;
-  p.row_tiles = max(1, (int)(((int64_t)max_q * p.G + C::R - 1) / C::R));
+  p.row_tiles = max(1, (int)(((int64_t)min(max_q, p.s.T) * p.G + C::R - 1) / C::R));
   e = launch_early(cache_attn_kernel<DQK, DV, NT, EXTRA>, dim3(grid), kCaThreads, C::SMEM, st, p);
   if (e != cudaSuccess) return e;
   const int64_t units = (int64_t)p.c.Hkv * p.row_tiles * p.s.B;

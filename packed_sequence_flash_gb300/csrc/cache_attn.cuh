@@ -82,7 +82,6 @@ struct CaCfg {
   static constexpr int SMEM = STAGES * STAGE + FIXED;
   static_assert(STAGES >= 2 && CTAS * STAGES * STAGE >= 64 * 1024, "bytes in flight");
   static_assert(R * QPITCH * 2 <= OBYTES, "queries fit where O goes");
-  static constexpr bool QREGS = NT * DQK <= 256;  // Q operand kept in registers
 };
 
 // a / b, in 32 bits when both fit (most of the time).
@@ -184,6 +183,7 @@ struct CaUnit {
   int lo, hi;        // keys that some row of the row tile sees
   int in_lo, in_hi;  // keys that every row sees: tiles inside need no mask
   int ta, tb;        // key tiles of the share with keys in [lo, hi)
+  float* scores;     // where the tile's first row keeps its scores
 };
 struct CaWalk {
   int64_t pos, end, base;
@@ -216,6 +216,7 @@ struct CaWalk {
       const int i0 = (u.rt << p.tile_lg) / p.G, i1 = (min((u.rt + 1) << p.tile_lg, u.m * p.G) - 1) / p.G;
       ca_row_keys(p, u.n, u.m, i0, u.lo, u.in_hi);
       ca_row_keys(p, u.n, u.m, i1, u.in_lo, u.hi);
+      u.scores = p.scores + (((int64_t)b * p.c.Hkv + u.h) * p.score_rows + (u.rt << p.tile_lg)) * p.score_cap;
       u.ta = max(u.t0, u.lo / kCaKeys);
       u.tb = min(u.t1, (u.hi + kCaKeys - 1) / kCaKeys);
       return true;
@@ -229,6 +230,7 @@ template <int DQK, int DV, int NT, bool EXTRA>
 __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV, NT>::CTAS)
     cache_attn_kernel(const __grid_constant__ CacheAttnParams p) {
   using C = CaCfg<DQK, DV, NT>;
+  constexpr bool QREGS = NT * DQK <= (EXTRA ? 64 : 256);  // Q operand kept in registers
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ uint64_t full[C::STAGES], empty[C::STAGES];
@@ -262,6 +264,7 @@ __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV, NT>::CTAS)
   let_next_kernel_start();
 
   // The whole work, and the sequence that this share begins in.
+  if (tid == 0 && blockIdx.x == 0 && cu_bad(p.s)) record_status(p.status, kStatusDeviceArgs);
   int64_t total = 0, before = 0, count = 0;  // places before and of this thread's sequence
   for (int base = 0; base < p.s.B; base += kCaThreads) {
     const int b = base + tid;
@@ -434,12 +437,14 @@ __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV, NT>::CTAS)
       u = next;
       pg = pg_unit;
     }
-    // After an abort the copies in flight are waited for (with a limit) before the CTA ends.
-    if (abort_flag) {
+    // The CTA does not end before its copies have landed (the wait has a limit of
+    // its own: the consumers may give up and end first).
+    {
+      const uint64_t limit = p.limit_ns > 100000000ull ? p.limit_ns : 100000000ull;
       for (uint32_t k = it > C::STAGES ? it - C::STAGES : 0; k < it; ++k)
-        wait_bar_drain(&full[k % C::STAGES], (k / C::STAGES) & 1, p.limit_ns);
+        wait_bar_drain(&full[k % C::STAGES], (k / C::STAGES) & 1, limit);
       for (uint32_t k = nu > kCaUnits ? nu - kCaUnits : 0; k < nu; ++k)
-        wait_bar_drain(&q_full[k % kCaUnits], (k / kCaUnits) & 1, p.limit_ns);
+        wait_bar_drain(&q_full[k % kCaUnits], (k / kCaUnits) & 1, limit);
     }
     return;
   }
@@ -505,8 +510,8 @@ __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV, NT>::CTAS)
       }
     }
     consumers_sync();
-    uint32_t qf[NT][C::QREGS ? DQK / 8 : 1];
-    if constexpr (C::QREGS) {
+    uint32_t qf[NT][QREGS ? DQK / 8 : 1];
+    if constexpr (QREGS) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -537,10 +542,6 @@ __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV, NT>::CTAS)
 #pragma unroll
       for (int c = 0; c < 4; ++c) o[m][nt][c] = 0.f;
 
-    // Where this lane's first row keeps its scores.
-    float* scores = EXTRA && p.accumulate
-                        ? p.scores + (((int64_t)u.b * p.c.Hkv + u.h) * p.score_rows + n0 + 2 * t) * p.score_cap
-                        : nullptr;
     auto tile_step = [&](auto mask_tag, int tile) {
       constexpr bool MASK = decltype(mask_tag)::value;
       const uint8_t* sb = smem + st * C::STAGE;
@@ -557,7 +558,7 @@ __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV, NT>::CTAS)
         uint32_t qv[NT][8];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
-        if constexpr (C::QREGS) {
+        if constexpr (QREGS) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) qv[nt][e] = qf[nt][j * 8 + e];
         } else {
@@ -595,11 +596,11 @@ __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV, NT>::CTAS)
         f[nt][0] = f[nt][1] = 1.f;
       }
       if (EXTRA && p.accumulate) {
-        float* at = scores + key;
+        float* at = u.scores + (int64_t)(nt * 8 + 2 * t) * (int)p.score_cap + key;
 #pragma unroll
         for (int c = 0; c < 4; ++c)
           if (n0 + nt * 8 + 2 * t + (c & 1) < rows && key + (c >> 1) * 8 < hi)
-            at[(nt * 8 + (c & 1)) * p.score_cap + (c >> 1) * 8] = s[nt][c] * f[nt][c & 1];
+            at[(c & 1) * p.score_cap + (c >> 1) * 8] = s[nt][c] * f[nt][c & 1];
       }
       const float dy[2] = {sc.y - ro[nt][0], sc.y - ro[nt][1]};
 #pragma unroll

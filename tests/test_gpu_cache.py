@@ -244,6 +244,31 @@ def test_nan_codes_reach_only_the_rows_that_see_them(dims):
     assert nan[:, 3].all() and int(nan.sum()) == 2
 
 
+@pytest.mark.parametrize("dims", DIMS)
+def test_nan_codes_in_a_tile_of_sixteen_rows(dims):
+    lens, G = [150], 4
+    rows, t, pages = tables(lens, 64)
+    cache = random_cache(pages, 1, *dims, 64, seed=10)
+    raw = cache.v.view(torch.uint8)
+    raw[rows[0][2], 0, 149 % 64, 7] = 0x7F  # seen by the last token's rows only
+    raw[rows[0][2], 0, 148 % 64, 9] = 0xFF  # by the last two tokens'
+    q = torch.randn(4, G, dims[0], generator=torch.Generator().manual_seed(9)).bfloat16().cuda()
+    out, lse = psf.attn_cache_fwd(q, cache, t, i32(lens), 0.1)
+    assert lse.isfinite().all() and out[:2].isfinite().all()
+    nan = out.isnan()
+    assert nan[2, :, 9].all() and int(nan[2].sum()) == G
+    assert nan[3, :, 7].all() and nan[3, :, 9].all() and int(nan[3].sum()) == 2 * G
+
+
+def test_windows_as_long_as_numbers_go():
+    lens, m_rows = [5, 300, 40], [9, 2, 40]
+    rows, t, pages = tables(lens, 16)
+    cache = random_cache(pages, 1, 64, 64, 16)
+    q = torch.randn(sum(m_rows), 2, 64, generator=torch.Generator().manual_seed(5)).bfloat16().cuda()
+    for window in (2 ** 31 - 1, t.shape[1] * 16, t.shape[1] * 16 - 1):
+        check_attend(cache, q, rows, t, lens, m_rows, 0.1, window=window)
+
+
 def test_strided_cache_and_rows_with_guard_bands():
     lens, m_rows = [33, 200, 7], [2, 1, 4]
     rows, t, pages = tables(lens, 32)
@@ -372,6 +397,94 @@ def test_graphs_share_a_workspace_and_follow_the_lengths():
             close(outs[i][1], want[1], want[3], "lse")
 
 
+def decode(cache, t, n, data, sync):
+    """Steps of a decode loop on the current stream, nothing between the calls unless sync."""
+    outs = []
+    for i, (k, v, q) in enumerate(data):
+        n += 1
+        psf.kv_cache_append(cache, k, v, t, n)
+        if sync:
+            torch.cuda.synchronize()
+        outs += psf.attn_cache_fwd(q, cache, t, n, 0.09, accumulate=i % 2 == 0)
+        if sync:
+            torch.cuda.synchronize()
+        if i % 7 == 6:
+            n.copy_(psf.kv_cache_evict(cache, t, n, 900, 100))
+        if i % 5 == 4:
+            outs += psf.kv_cache_gather(cache, t, n, 4 * 1100)[2:]
+        if sync:
+            torch.cuda.synchronize()
+    torch.cuda.synchronize()
+    return outs
+
+
+def test_calls_one_after_another_without_waiting():
+    """Kernels that begin before the one in front is over must not read what it has yet to write."""
+    lens = [905, 60, 1, 890]
+    rows, t, pages = tables(lens, 32, extra=60)
+    data = [(torch.randn(4, 2, 128).bfloat16().cuda(), torch.randn(4, 2, 128).bfloat16().cuda(),
+             torch.randn(4, 8, 128).bfloat16().cuda()) for _ in range(30)]
+    runs = []
+    for sync in (True, False, False):
+        cache = random_cache(pages, 2, 128, 128, 32, weights=True, seed=5)
+        n = i32(lens)
+        runs.append(decode(cache, t, n, data, sync) + [cache.k.view(torch.uint8), cache.v.view(torch.uint8),
+                                                       cache.k_scale, cache.v_scale, cache.weight, n])
+    for other in runs[1:]:
+        for a, b in zip(runs[0], other):
+            assert torch.equal(a, b)
+
+
+def test_a_captured_decode_step():
+    """Length, append and attention in one graph, between a fill and a copy, replayed while the sequences grow."""
+    lens = [31, 300, 0]
+    rows, t, pages = tables(lens, 32, extra=20)
+    k, v = (torch.zeros(3, 2, 64, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    q = torch.zeros(3, 4, 64, dtype=torch.bfloat16, device="cuda")
+    n = i32(lens)
+    cache = random_cache(pages, 2, 64, 64, 32, weights=True, seed=6)
+    copy = torch.empty(3, 4, 64, dtype=torch.bfloat16, device="cuda")
+    scratch = torch.empty(1024, device="cuda")
+
+    def step():
+        scratch.fill_(1.0)
+        n.add_(1)
+        psf.kv_cache_append(cache, k, v, t, n)
+        out, lse = psf.attn_cache_fwd(q, cache, t, n, 0.125, accumulate=True)
+        copy.copy_(out)
+        return out, lse
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        warm = random_cache(pages, 2, 64, 64, 32, weights=True, seed=6)
+        psf.kv_cache_append(warm, k, v, t, i32([x + 1 for x in lens]))
+        psf.attn_cache_fwd(q, warm, t, i32([x + 1 for x in lens]), 0.125, accumulate=True)
+        side.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            out, lse = step()
+    torch.cuda.synchronize()
+    n.copy_(i32(lens))
+    c = ref.from_cache(cache)
+    g = torch.Generator().manual_seed(3)
+    for _ in range(12):
+        lens = [x + 1 for x in lens]
+        for x in (k, v, q):
+            x.copy_(torch.randn(x.shape, generator=g).bfloat16())
+        ref.append(c, k, v, rows, lens, [0, 1, 2, 3])
+        want = ref.attend(c, q, rows, lens, [0, 1, 2, 3], 0.125, accumulate=True)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert n.tolist() == lens
+        close(out, want[0], want[2], "out")
+        close(lse, want[1], want[3], "lse")
+        assert torch.equal(copy, out)
+        close(cache.weight, c["w"], want[4], "weight")
+        c["w"] = cache.weight.cpu().double()
+        same(cache, c)
+
+
 def test_two_streams_at_once():
     lens = [4000, 2500, 900]
     rows, t, pages = tables(lens, 64)
@@ -440,6 +553,37 @@ def test_device_checks_leave_the_other_sequences_alone(fault):
         assert torch.equal(a[rows[1]], z[rows[1]])
     psf.kv_cache_gather(cache, bad_t, bad_n, 203)
     assert psf.device_status() == EDEVICE_ARGS
+
+
+@pytest.mark.parametrize("cu", [[3, 5, 9], [0, 5, 2], [0, 5, 400], [0, -1, 4], [-40, 2, 4], [1000, 1001, 1002]])
+def test_prefix_sums_that_cannot_be(cu):
+    lens = [40, 30]
+    rows, t, pages = tables(lens, 16, extra=16)
+    cache = random_cache(pages, 1, 64, 64, 16)
+    q = torch.randn(9, 2, 64).bfloat16().cuda()
+    psf.attn_cache_fwd(q, cache, t, i32(lens), 0.1, cu_q=i32(cu), max_q=9)
+    assert psf.device_status() == EDEVICE_ARGS
+    before = cache.k.view(torch.uint8).clone()
+    owned = torch.zeros(pages, dtype=torch.bool, device="cuda")
+    owned[[pg for r in rows for pg in r]] = True
+    x = torch.randn(9, 1, 64).bfloat16().cuda()
+    psf.kv_cache_append(cache, x, x, t, i32(lens), cu_new=i32(cu))
+    assert psf.device_status() == EDEVICE_ARGS
+    assert torch.equal(cache.k.view(torch.uint8)[~owned], before[~owned])
+
+
+def test_numbers_of_other_kinds():
+    import numpy as np
+
+    lens = [20, 30]
+    rows, t, pages = tables(lens, 16)
+    cache = random_cache(pages, 1, 64, 64, 16, weights=True)
+    q = torch.randn(3, 2, 64).bfloat16().cuda()
+    a = psf.attn_cache_fwd(q, cache, t, i32(lens), np.float64(0.1), cu_q=i32([0, 1, 3]), max_q=np.int64(2))
+    b = psf.attn_cache_fwd(q, cache, t, i32(lens), 0.1, cu_q=i32([0, 1, 3]), max_q=7)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    assert psf.kv_cache_gather(cache, t, i32(lens), np.int32(50))[0].shape == (50, 1, 64)
+    assert psf.kv_cache_evict(cache, t, i32(lens), np.int64(25), np.int64(3)).tolist() == [20, 25]
 
 
 # ---------------------------------------------------------------------------
