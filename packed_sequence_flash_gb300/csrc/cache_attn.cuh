@@ -904,11 +904,11 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
     float top = kCaFloor, sum = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-    for (int k0 = gr; k0 < np; k0 += groups * 8) {
-      float l[8];
-      float4 a[8];
+    for (int k0 = gr; k0 < np; k0 += groups * 4) {
+      float l[4];
+      float4 a[4];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
+      for (int u = 0; u < 4; ++u) {
         const int k = k0 + u * groups;
         l[u] = -CUDART_INF_F;
         a[u] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -919,7 +919,7 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
       }
       float m = top;
 #pragma unroll
-      for (int u = 0; u < 8; ++u) m = fmaxf(m, l[u]);
+      for (int u = 0; u < 4; ++u) m = fmaxf(m, l[u]);
       const float f = ex2_approx(top - m);
       acc.x *= f;
       acc.y *= f;
@@ -928,7 +928,7 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
       sum *= f;
       top = m;
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
+      for (int u = 0; u < 4; ++u) {
         const float w = ex2_approx(l[u] - m);
         sum += w;
         acc.x = fmaf(a[u].x, w, acc.x);
