@@ -491,7 +491,7 @@ int psf_attn_cache_fwd(const void* q, const psf_kv_cache* cache, void* out, floa
  * Evict down to `budget` tokens per sequence and KV head, in place.
  *  A sequence longer than budget keeps, for each KV head on its own, its last
  *  `recent` tokens and the budget - recent others of largest weight (of equal
- *  weights the earliest; NaN counts as the largest), in their order, moved to
+ *  weights the earliest; NaN counts as the largest, -0 as 0), in their order, moved to
  *  positions 0 .. budget - 1; weights move along. new_lens[b] = min(seq_lens[b],
  *  budget); other sequences are not touched. A new block's scale is the largest
  *  old scale of its tokens, codes become RNE_e4m3(c * (old / new)). Rows past the

@@ -4,24 +4,33 @@
 //   out_i = sum_j p_ij V_j,  p_ij = exp(z_ij - lse_i),  z_ij = scale q_i . K_j (capped)
 //
 // What bounds it: every key and value byte is read once per group of query
-// heads and used for 8 to 32 rows, 2 flop per byte and row, so the kernel is a
+// heads and used for 8 or 16 rows, 2 flop per byte and row, so the kernel is a
 // stream of the cache: the floor is bytes / HBM bandwidth. A 128-row tensor
 // tile (tcgen05) would be nearly empty and would need the codes as 16-bit
 // operands in shared memory, that is every byte expanded and written back
 // once; warp-level products take their operands from registers, where the
-// codes are expanded in place, so the legacy instruction is the fitting one.
+// codes are expanded in place, so that instruction is the fitting one.
+// Measured (bf16, head dim 128, 32 query and 8 KV heads; GB300): 64 sequences of
+// 16 to 32 Ki tokens 480 us for 3.27 GB, the rate of a plain copy; 32 of 64 to
+// 8192 tokens 58.6 us for 307 MB (floor 45.2: 5 us until the first tile, 4 us of
+// join and some 4 us in which the CTAs end); one of 32 Ki tokens 21.8 us (floor
+// 9.9); one of 777 tokens with 16 / 4 heads 10 us, all latency. Out of L2 a tile of
+// 64 keys takes an SM 515 cycles for 8 rows and 790 for 16 (the expansion, two
+// cycles of the integer pipe for two codes, is most of it); from memory 690.
 //
 // Rows: the query rows of one KV head (m rows x G heads, token-major) in tiles
-// of R = 8 NT rows: 8 for one group of heads and one token, 16 where there are more rows. Keys: tiles of 64. A CTA takes an equal share of all
-// (sequence, KV head, row tile, key tile) in that order, wherever it begins and
-// ends, so ragged batches and a single long sequence alike fill the device.
-// A share that covers all tiles of a (sequence, head, row tile) writes its
-// result; otherwise it leaves a partial result (o / l, lse) that the join kernel
-// adds up in the order of the CTAs. Nothing depends on the order of execution.
+// of R = 8 NT rows: 8 where a KV head has no more, else 16. Keys: tiles of 64. A
+// CTA takes an equal share of all (sequence, KV head, row tile, key tile) in
+// that order, wherever it begins and ends, so ragged batches and a single long
+// sequence alike fill the device. A share that covers all tiles of a (sequence,
+// head, row tile) writes its result; otherwise it leaves a partial result (o / l,
+// lse) that the join kernel adds up in the order of the CTAs. Nothing depends on
+// the order of execution.
 //
-//   warp 4     producer: the next unit and its queries ahead of time, page numbers and
-//              scales one batch ahead, K and V pages by TMA into a ring of stages
-//              (128-byte rows, 128-byte swizzle; 64-byte rows for head dim 64)
+//   warp 4     producer: the next unit and its queries ahead of time, page
+//              numbers and scales one batch ahead, K and V pages by TMA into a
+//              ring of stages (128-byte rows, 128-byte swizzle; 64-byte rows
+//              for head dim 64)
 //   warps 0-3  16 keys of each tile each, with a softmax state of their own
 //              (nothing but the ring's barriers between them); joined at the
 //              end of the unit
@@ -32,8 +41,8 @@
 // rows and its Q operand is arranged to match. O^T += V^T P^T likewise: a lane
 // reads 16 consecutive codes of four keys, pairs up keys with byte permutes,
 // and owns those 16 head-dim rows of O^T. P^T is S^T's accumulator transposed
-// in registers (movmatrix). The map R from a position in the product to a key row is
-// chosen so that neither kind of read has a bank conflict under the swizzle.
+// in registers (movmatrix). The map from a position in the product to a key
+// row is chosen so that neither kind of read has a bank conflict under the swizzle.
 //
 // Numbers: codes are exact in fp16. Q rows are scaled by a power of two into
 // fp16's range (exact for what matters: 28 octaves below the row's largest).
@@ -485,7 +494,8 @@ __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV, NT>::CTAS)
     for (int e2 = 0; e2 < 2 * NT; ++e2) {
       constexpr int E = DQK / 32;  // elements per lane and row
       const int r = warp + e2 * kCaWarps;
-      const uint32_t* from = reinterpret_cast<const uint32_t*>(smem + C::RAW_OFF + qb * C::RAW + r * DQK * 2) + lane * (E / 2);
+      const uint32_t* from =
+          reinterpret_cast<const uint32_t*>(smem + C::RAW_OFF + qb * C::RAW + r * DQK * 2) + lane * (E / 2);
       float v[E], top = 0.f;
 #pragma unroll
       for (int e = 0; e < E; e += 2) {
@@ -515,32 +525,32 @@ __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV, NT>::CTAS)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int j = 0; j < DQK / 64; ++j)
+        for (int j = 0; j < DQK / 64; ++j)
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const uint4 a = lds128(qs + nt * 8 * C::QPITCH * 2 + j * 128 + x * 16);
-          qf[nt][j * 8 + x * 4] = a.x;
-          qf[nt][j * 8 + x * 4 + 1] = a.y;
-          qf[nt][j * 8 + x * 4 + 2] = a.z;
-          qf[nt][j * 8 + x * 4 + 3] = a.w;
-        }
+          for (int x = 0; x < 2; ++x) {
+            const uint4 a = lds128(qs + nt * 8 * C::QPITCH * 2 + j * 128 + x * 16);
+            qf[nt][j * 8 + x * 4] = a.x;
+            qf[nt][j * 8 + x * 4 + 1] = a.y;
+            qf[nt][j * 8 + x * 4 + 2] = a.z;
+            qf[nt][j * 8 + x * 4 + 3] = a.w;
+          }
     }
     float fac[NT][2], mu[NT][2], ro[NT][2], l[NT][2];
     float o[MT][NT][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      fac[nt][c] = row_fac[nt * 8 + 2 * t + c];
-      mu[nt][c] = ro[nt][c] = kCaFloor;
-      l[nt][c] = 0.f;
-    }
+      for (int c = 0; c < 2; ++c) {
+        fac[nt][c] = row_fac[nt * 8 + 2 * t + c];
+        mu[nt][c] = ro[nt][c] = kCaFloor;
+        l[nt][c] = 0.f;
+      }
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) o[m][nt][c] = 0.f;
+        for (int c = 0; c < 4; ++c) o[m][nt][c] = 0.f;
 
     auto tile_step = [&](auto mask_tag, int tile) {
       constexpr bool MASK = decltype(mask_tag)::value;
@@ -550,7 +560,7 @@ __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV, NT>::CTAS)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) s[nt][c] = s2[nt][c] = 0.f;
+        for (int c = 0; c < 4; ++c) s[nt][c] = s2[nt][c] = 0.f;
 #pragma unroll
       for (int j = 0; j < DQK / 64; ++j) {
         const uint4 xa = lds128(sb + k_off(ka, j)), xb = lds128(sb + k_off(ka + 8, j));
@@ -558,104 +568,110 @@ __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV, NT>::CTAS)
         uint32_t qv[NT][8];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
-        if constexpr (QREGS) {
+          if constexpr (QREGS) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) qv[nt][e] = qf[nt][j * 8 + e];
-        } else {
+            for (int e = 0; e < 8; ++e) qv[nt][e] = qf[nt][j * 8 + e];
+          } else {
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const uint4 a = lds128(qs + nt * 8 * C::QPITCH * 2 + j * 128 + x * 16);
-            qv[nt][x * 4] = a.x;
-            qv[nt][x * 4 + 1] = a.y;
-            qv[nt][x * 4 + 2] = a.z;
-            qv[nt][x * 4 + 3] = a.w;
+            for (int x = 0; x < 2; ++x) {
+              const uint4 a = lds128(qs + nt * 8 * C::QPITCH * 2 + j * 128 + x * 16);
+              qv[nt][x * 4] = a.x;
+              qv[nt][x * 4 + 1] = a.y;
+              qv[nt][x * 4 + 2] = a.z;
+              qv[nt][x * 4 + 3] = a.w;
+            }
           }
-        }
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
           const uint32_t a0 = e4m3_to_half2(wa[w] & 0xffff), a2 = e4m3_to_half2(wa[w] >> 16);
           const uint32_t a1 = e4m3_to_half2(wb[w] & 0xffff), a3 = e4m3_to_half2(wb[w] >> 16);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma16816((w & 1) ? s2[nt] : s[nt], a0, a1, a2, a3, qv[nt][2 * w], qv[nt][2 * w + 1]);
+          for (int nt = 0; nt < NT; ++nt)
+            mma16816((w & 1) ? s2[nt] : s[nt], a0, a1, a2, a3, qv[nt][2 * w], qv[nt][2 * w + 1]);
         }
       }
+      // Exponents of the row sum's terms (x) and of P (y) against the references:
+      // x = z - mu, y = z + log2 v_scale - ro, z the score in log2 units.
       const float2 sc = meta[st][warp];
       float x[NT][4], y[NT][4], f[NT][2];
       bool move = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-      f[nt][0] = fac[nt][0] * sc.x; f[nt][1] = fac[nt][1] * sc.x;
+        f[nt][0] = fac[nt][0] * sc.x;
+        f[nt][1] = fac[nt][1] * sc.x;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) s[nt][c] += s2[nt][c];
-      if (EXTRA && p.softcap > 0.f) {
+        for (int c = 0; c < 4; ++c) s[nt][c] += s2[nt][c];
+        if (EXTRA && p.softcap > 0.f) {
+          // c tanh(a) log2(e), tanh(a) = 1 - 2 / (e^(2a) + 1): off by some 2^-22 of the cap
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const float e = ex2_approx(s[nt][c] * f[nt][c & 1] * 2.8853900817779268f);
+            s[nt][c] = p.softcap * 1.4426950408889634f * fmaf(-2.f, rcp_approx(e + 1.f), 1.f);
+          }
+          f[nt][0] = f[nt][1] = 1.f;
+        }
+        if (EXTRA && p.accumulate) {
+          float* at = u.scores + (int64_t)(nt * 8 + 2 * t) * (int)p.score_cap + key;
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (n0 + nt * 8 + 2 * t + (c & 1) < rows && key + (c >> 1) * 8 < hi)
+              at[(c & 1) * p.score_cap + (c >> 1) * 8] = s[nt][c] * f[nt][c & 1];
+        }
+        const float dy[2] = {sc.y - ro[nt][0], sc.y - ro[nt][1]};
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          const float e = ex2_approx(s[nt][c] * f[nt][c & 1] * 2.8853900817779268f);
-          s[nt][c] = p.softcap * 1.4426950408889634f * fmaf(-2.f, rcp_approx(e + 1.f), 1.f);
+          x[nt][c] = fmaf(s[nt][c], f[nt][c & 1], -mu[nt][c & 1]);
+          y[nt][c] = fmaf(s[nt][c], f[nt][c & 1], dy[c & 1]);
+          if constexpr (MASK) {
+            const int2 lim = row_lim[nt * 8 + 2 * t + (c & 1)];
+            const int k = key + (c >> 1) * 8;
+            if (k < lim.x || k >= lim.y) s[nt][c] = x[nt][c] = y[nt][c] = -CUDART_INF_F;
+          }
         }
-        f[nt][0] = f[nt][1] = 1.f;
-      }
-      if (EXTRA && p.accumulate) {
-        float* at = u.scores + (int64_t)(nt * 8 + 2 * t) * (int)p.score_cap + key;
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if (n0 + nt * 8 + 2 * t + (c & 1) < rows && key + (c >> 1) * 8 < hi)
-            at[(c & 1) * p.score_cap + (c >> 1) * 8] = s[nt][c] * f[nt][c & 1];
-      }
-      const float dy[2] = {sc.y - ro[nt][0], sc.y - ro[nt][1]};
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        x[nt][c] = fmaf(s[nt][c], f[nt][c & 1], -mu[nt][c & 1]);
-        y[nt][c] = fmaf(s[nt][c], f[nt][c & 1], dy[c & 1]);
-        if constexpr (MASK) {
-          const int2 lim = row_lim[nt * 8 + 2 * t + (c & 1)];
-          const int k = key + (c >> 1) * 8;
-          if (k < lim.x || k >= lim.y) s[nt][c] = x[nt][c] = y[nt][c] = -CUDART_INF_F;
-        }
-      }
-      move |= fmaxf(fmax3(x[nt][0], x[nt][1], x[nt][2]), x[nt][3]) > kCaLazy ||
-                        fmaxf(fmax3(y[nt][0], y[nt][1], y[nt][2]), y[nt][3]) > kCaHead + kCaLazy;
+        move |= fmaxf(fmax3(x[nt][0], x[nt][1], x[nt][2]), x[nt][3]) > kCaLazy ||
+                fmaxf(fmax3(y[nt][0], y[nt][1], y[nt][2]), y[nt][3]) > kCaHead + kCaLazy;
       }
       if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-        float of[2];
+          float of[2];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          float z[2];
+          for (int c = 0; c < 2; ++c) {
+            float z[2];
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
-            z[e] = MASK && s[nt][c + 2 * e] == -CUDART_INF_F ? -CUDART_INF_F : s[nt][c + 2 * e] * f[nt][c];
-          float top = fmaxf(z[0], z[1]);
+            for (int e = 0; e < 2; ++e)
+              z[e] = MASK && s[nt][c + 2 * e] == -CUDART_INF_F ? -CUDART_INF_F : s[nt][c + 2 * e] * f[nt][c];
+            float top = fmaxf(z[0], z[1]);
 #pragma unroll
-          for (int e = 4; e < 32; e <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, e));
-          const float m1 = fmaxf(mu[nt][c], top), r1 = fmaxf(ro[nt][c], top + sc.y - kCaHead);
-          l[nt][c] *= ex2_approx(mu[nt][c] - m1);
-          of[c] = ex2_approx(ro[nt][c] - r1);
-          mu[nt][c] = m1;
-          ro[nt][c] = r1;
+            for (int e = 4; e < 32; e <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, e));
+            const float m1 = fmaxf(mu[nt][c], top), r1 = fmaxf(ro[nt][c], top + sc.y - kCaHead);
+            l[nt][c] *= ex2_approx(mu[nt][c] - m1);
+            of[c] = ex2_approx(ro[nt][c] - r1);
+            mu[nt][c] = m1;
+            ro[nt][c] = r1;
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            x[nt][c + 2 * e] = z[e] - m1;
-            y[nt][c + 2 * e] = z[e] + (sc.y - r1);
+            for (int e = 0; e < 2; ++e) {
+              x[nt][c + 2 * e] = z[e] - m1;
+              y[nt][c + 2 * e] = z[e] + (sc.y - r1);
+            }
           }
-        }
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+          for (int m = 0; m < MT; ++m)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) o[m][nt][c] *= of[c & 1];
+            for (int c = 0; c < 4; ++c) o[m][nt][c] *= of[c & 1];
         }
       }
       uint32_t p0[NT], p1[NT];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-      float w[4];
+        float w[4];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        l[nt][c & 1] += ex2_approx(x[nt][c]);
-        w[c] = ex2_approx(y[nt][c]);
-      }
-      p0[nt] = transpose8x8(pack2<__half>(w[0], w[1])); p1[nt] = transpose8x8(pack2<__half>(w[2], w[3]));
+        for (int c = 0; c < 4; ++c) {
+          l[nt][c & 1] += ex2_approx(x[nt][c]);
+          w[c] = ex2_approx(y[nt][c]);
+        }
+        p0[nt] = transpose8x8(pack2<__half>(w[0], w[1]));
+        p1[nt] = transpose8x8(pack2<__half>(w[2], w[3]));
       }
       uint32_t nan_seen = 0;
 #pragma unroll
@@ -694,12 +710,14 @@ __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV, NT>::CTAS)
           const uint32_t y0 = __byte_perm(v[0][e], v[1][e], 0x5140), y1 = __byte_perm(v[0][e], v[1][e], 0x7362);
           const uint32_t z0 = __byte_perm(v[2][e], v[3][e], 0x5140), z1 = __byte_perm(v[2][e], v[3][e], 0x7362);
           const int m = j * 8 + e * 2;
-          const uint32_t A0=e4m3_to_half2(y0 & 0xffff), A1=e4m3_to_half2(y0 >> 16), A2=e4m3_to_half2(z0 & 0xffff), A3=e4m3_to_half2(z0 >> 16);
-          const uint32_t B0=e4m3_to_half2(y1 & 0xffff), B1=e4m3_to_half2(y1 >> 16), B2=e4m3_to_half2(z1 & 0xffff), B3=e4m3_to_half2(z1 >> 16);
+          const uint32_t a0 = e4m3_to_half2(y0 & 0xffff), a1 = e4m3_to_half2(y0 >> 16);
+          const uint32_t a2 = e4m3_to_half2(z0 & 0xffff), a3 = e4m3_to_half2(z0 >> 16);
+          const uint32_t b0 = e4m3_to_half2(y1 & 0xffff), b1 = e4m3_to_half2(y1 >> 16);
+          const uint32_t b2 = e4m3_to_half2(z1 & 0xffff), b3 = e4m3_to_half2(z1 >> 16);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-          mma16816(o[m][nt], A0, A1, A2, A3, p0[nt], p1[nt]);
-          mma16816(o[m + 1][nt], B0, B1, B2, B3, p0[nt], p1[nt]);
+            mma16816(o[m][nt], a0, a1, a2, a3, p0[nt], p1[nt]);
+            mma16816(o[m + 1][nt], b0, b1, b2, b3, p0[nt], p1[nt]);
           }
         }
       }
@@ -746,37 +764,38 @@ __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV, NT>::CTAS)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
+      for (int c = 0; c < 2; ++c) {
 #pragma unroll
-      for (int x = 4; x < 32; x <<= 1) l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], x);
-      if (g == 0) {
-        st_mu[warp][nt * 8 + 2 * t + c] = mu[nt][c];
-        st_l[warp][nt * 8 + 2 * t + c] = l[nt][c];
+        for (int x = 4; x < 32; x <<= 1) l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], x);
+        if (g == 0) {
+          st_mu[warp][nt * 8 + 2 * t + c] = mu[nt][c];
+          st_l[warp][nt * 8 + 2 * t + c] = l[nt][c];
+        }
       }
-    }
     consumers_sync();
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-    float f[2];
+      float f[2];
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const int r = nt * 8 + 2 * t + c;
-      float top = kCaFloor, sum = 0.f;
+      for (int c = 0; c < 2; ++c) {
+        const int r = nt * 8 + 2 * t + c;
+        float top = kCaFloor, sum = 0.f;
 #pragma unroll
-      for (int w = 0; w < kCaWarps; ++w) top = fmaxf(top, st_mu[w][r]);
+        for (int w = 0; w < kCaWarps; ++w) top = fmaxf(top, st_mu[w][r]);
 #pragma unroll
-      for (int w = 0; w < kCaWarps; ++w) sum += st_l[w][r] * ex2_approx(st_mu[w][r] - top);
-      f[c] = sum == 0.f ? 0.f : ex2_approx(ro[nt][c] - top) / sum;
-      if (warp == 0 && g == 0) fin_l[r] = sum == 0.f ? -CUDART_INF_F : top + log2f(sum);
-    }
+        for (int w = 0; w < kCaWarps; ++w) sum += st_l[w][r] * ex2_approx(st_mu[w][r] - top);
+        f[c] = sum == 0.f ? 0.f : ex2_approx(ro[nt][c] - top) / sum;
+        if (warp == 0 && g == 0) fin_l[r] = sum == 0.f ? -CUDART_INF_F : top + log2f(sum);
+      }
 #pragma unroll
-    for (int m = 0; m < MT; m += 2) {
-      const int d = DV == 64 ? g * 8 + m * 2 : (m >> 3) * 128 + g * 16 + (m & 7) * 2;
+      for (int m = 0; m < MT; m += 2) {
+        const int d = DV == 64 ? g * 8 + m * 2 : (m >> 3) * 128 + g * 16 + (m & 7) * 2;
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
-        *reinterpret_cast<float4*>(ob + (warp * C::R + nt * 8 + 2 * t + c) * C::OPITCH + d) =
-            make_float4(o[m][nt][c] * f[c], o[m][nt][2 + c] * f[c], o[m + 1][nt][c] * f[c], o[m + 1][nt][2 + c] * f[c]);
-    }
+        for (int c = 0; c < 2; ++c)
+          *reinterpret_cast<float4*>(ob + (warp * C::R + nt * 8 + 2 * t + c) * C::OPITCH + d) =
+              make_float4(o[m][nt][c] * f[c], o[m][nt][2 + c] * f[c], o[m + 1][nt][c] * f[c],
+                          o[m + 1][nt][2 + c] * f[c]);
+      }
     }
     consumers_sync();
     const int live = min(C::R, rows - n0);
@@ -959,9 +978,9 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
       }
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
       const int y = n0 + r, i = y / p.G;
-      const uint2 w = p.f16 ? make_uint2(pack2<__half>(acc.x * inv, acc.y * inv), pack2<__half>(acc.z * inv, acc.w * inv))
-                            : make_uint2(pack2<__nv_bfloat16>(acc.x * inv, acc.y * inv),
-                                         pack2<__nv_bfloat16>(acc.z * inv, acc.w * inv));
+      acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+      const uint2 w = p.f16 ? make_uint2(pack2<__half>(acc.x, acc.y), pack2<__half>(acc.z, acc.w))
+                            : make_uint2(pack2<__nv_bfloat16>(acc.x, acc.y), pack2<__nv_bfloat16>(acc.z, acc.w));
       *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + p.o_ss * (s.q.q0 + i) +
                                 p.o_sh * (h * p.G + y - i * p.G) + d) = w;
       if (d == 0)
