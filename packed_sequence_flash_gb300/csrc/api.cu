@@ -1023,8 +1023,10 @@ int psf_attn_cache_fwd(const void* q, const psf_kv_cache* cache, void* out, floa
       (rc = strided_view(strides, 1, "out", PSF_LAYOUT_THD, 1, T, Hq, p.c.Dv, true, &vo)))
     return rc;
   const int64_t cap = (int64_t)max_pages * p.c.page;
-  if ((int64_t)max_q * (Hq / p.c.Hkv) + cap > 0x7fffffff || (int64_t)max_q * Hq > 0x7fffffff)
-    return fail(PSF_EINVAL, "max_q=%d rows of %d heads over %lld keys exceed 2^31 - 1", max_q, Hq, (long long)cap);
+  if ((int64_t)max_q * (Hq / p.c.Hkv) + cap > 0x7fffffff || (int64_t)max_q * Hq > 0x7fffffff ||
+      (int64_t)T * Hq > 0x7fffffff)
+    return fail(PSF_EINVAL, "T=%d (max_q=%d) rows of %d heads over %lld keys exceed 2^31 - 1", T, max_q, Hq,
+                (long long)cap);
   if (T == 0) return PSF_OK;
   if (!q || !out || !lse || !aligned16(q) || !aligned16(out)) return fail(PSF_EINVAL, "null or unaligned q, out or lse");
   const size_t need = psf_attn_cache_workspace_size(B, max_pages, p.c.page, Hq, p.c.Hkv, p.c.Dqk, p.c.Dv, max_q, flags);

@@ -101,6 +101,7 @@ def test_cache_and_sequences_are_checked(lib, call, kw, code, word):
     (dict(dtype=2), EINVAL, b"dtype"), (dict(flags=2), EINVAL, b"flags"), (dict(flags=1, weight=None), EINVAL, b"weights"),
     (dict(cu=None, T=7), EINVAL, b"divide"), (dict(cu=None, max_q=1), EINVAL, b"max_q"), (dict(max_q=-1), EINVAL, b"max_q"),
     (dict(max_q=2 ** 30, T=2 ** 30, cu=A), EINVAL, b"2^31"), (dict(max_q=2 ** 31 - 1, Hq=2), EINVAL, b"2^31"),
+    (dict(T=2 ** 30, Hq=4), EINVAL, b"2^31"),
     (dict(q=None), EINVAL, b"null"), (dict(out=A + 4), EINVAL, b"aligned"), (dict(T=-1), EINVAL, b"T"),
     (dict(strides=(ctypes.c_int64 * 6)(0, 4, 512, 0, 128, 512)), EINVAL, b"stride"),
     (dict(strides=(ctypes.c_int64 * 6)(0, 128, 512, 0, 64, 512)), EINVAL, b"overlaps"),
