@@ -84,12 +84,29 @@ __device__ __forceinline__ float2 e4m3_to_float2(uint32_t pair) {
   const uint32_t h = e4m3_to_half2(pair);
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
+// q = a value rounded to fp32, rest = that value minus q: q with an odd last bit
+// where it is not exact, so that rounding it again, to fewer bits, is the value's
+// own rounding (65 / 1.3f is 50 in fp32, a tie of e4m3 that the quotient is not).
+__device__ __forceinline__ float round_to_odd(float q, float rest) {
+  const int bits = __float_as_int(q);
+  const bool move = fabsf(rest) > 0.f && !(bits & 1) && fabsf(q) > 0.f;
+  return move ? __int_as_float((rest > 0.f) == (q > 0.f) ? bits + 1 : bits - 1) : q;
+}
+__device__ __forceinline__ float divide_to_odd(float x, float y) {
+  const float q = x / y;
+  return round_to_odd(q, fmaf(-q, y, x));
+}
+__device__ __forceinline__ float multiply_to_odd(float x, float y) {
+  const float p = x * y;
+  return round_to_odd(p, fmaf(x, y, -p));
+}
 // Codes times r <= 1, rounded to e4m3 again. For a power of two the products are
 // made in fp16: exact wherever the result is not 0 (codes have 4 significant
 // bits and results below 2^-10 become 0; fp16 reaches down to 2^-24).
 __device__ __forceinline__ uint32_t rescale4(uint32_t codes, float r) {
   const float2 a = e4m3_to_float2(codes & 0xffff), b = e4m3_to_float2(codes >> 16);
-  return e4m3_pair(a.x * r, a.y * r) | (e4m3_pair(b.x * r, b.y * r) << 16);
+  return e4m3_pair(multiply_to_odd(a.x, r), multiply_to_odd(a.y, r)) |
+         (e4m3_pair(multiply_to_odd(b.x, r), multiply_to_odd(b.y, r)) << 16);
 }
 __device__ __forceinline__ uint32_t rescale4_half(uint32_t codes, __half2 r) {
   uint32_t lo = e4m3_to_half2(codes & 0xffff), hi = e4m3_to_half2(codes >> 16);

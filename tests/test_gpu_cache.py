@@ -159,6 +159,30 @@ def test_more_sequences_than_a_block_has_threads():
     check_attend(cache, q, rows, t, lens, m_rows, 0.125)
 
 
+@pytest.mark.parametrize("B,G,hi", [(700, 4, 60), (513, 2, 300), (1100, 1, 40)])
+@pytest.mark.parametrize("softcap", [None, 5.0])
+def test_more_units_than_shares(B, G, hi, softcap):
+    """Sequences without keys, with few and with many among them, and rows past the last one."""
+    r = random.Random(B)
+    lens = [r.choice([0, 1, 20, hi, r.randint(0, hi)]) for _ in range(B)]
+    lens[B // 2] = 4000
+    m_rows = [r.choice([0, 1, 1, 2]) for _ in range(B)]
+    m_rows[B // 2] = 1
+    rows, t, pages = tables(lens, 16, seed=B)
+    cache = random_cache(pages, 2, 64, 64, 16, seed=B, weights=True)
+    cu = prefix(m_rows)
+    q = torch.randn(cu[-1] + 9, 2 * G, 64, generator=torch.Generator().manual_seed(B)).bfloat16().cuda()
+    out = torch.full_like(q, 3.0)
+    c = ref.from_cache(cache)
+    got = psf.attn_cache_fwd(q, cache, t, i32(lens), 0.2, cu_q=i32(cu), max_q=2, softcap=softcap, out=out,
+                             accumulate=True)
+    assert psf.device_status() == 0
+    want = ref.attend(c, q, rows, lens, cu, 0.2, softcap=softcap, accumulate=True)
+    close(got[0], want[0], want[2], "out")
+    close(got[1], want[1], want[3], "lse")
+    close(cache.weight, c["w"], want[4], "weight")
+
+
 @pytest.mark.parametrize("G,m", [(4, 1), (1, 1), (8, 5), (3, 2)])
 @pytest.mark.parametrize("window", [None, 50])
 def test_accumulated_weights(G, m, window):
@@ -633,6 +657,33 @@ def test_append_token_by_token(page):
         x = (torch.randn(4, 2, 128, generator=g) * 2.0 ** (step % 9 - 4)).bfloat16().cuda()
         y = (torch.randn(4, 2, 128, generator=g) * 2.0 ** (step / 4)).bfloat16().cuda()
         check_append(cache, x, y, rows, t, lens, [1] * 4, uniform=True)
+
+
+@pytest.mark.parametrize("dims", DIMS)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_append_one_token_to_every_sequence(dims, dtype):
+    """Growing and shrinking rows, values that are not finite, rows at page ends, scales that are no powers of two."""
+    lens = [1, 17, 32, 33, 64, 5, 40, 2, 31]
+    rows, t, pages = tables(lens, 32)
+    cache = random_cache(pages, 3, *dims, 32, weights=True)
+    cache.k_scale.mul_(1.3)
+    g = torch.Generator().manual_seed(1)
+    x = torch.randn(9, 3, dims[0], generator=g) * torch.exp2(torch.randint(-9, 12, (9, 3, 1), generator=g))
+    y = torch.randn(9, 3, dims[1], generator=g) * torch.exp2(torch.randint(-9, 12, (9, 3, 1), generator=g))
+    x[1, 0, 3], x[2, 1, 0], x[4, 2] = math.inf, math.nan, 0.0
+    y[3, 0], y[5, 1, 7] = math.nan, -math.inf
+    k = x.to(dtype).cuda()
+    fused = torch.zeros(9, 3, 2 * dims[1], dtype=dtype, device="cuda")
+    v = fused[:, :, dims[1]:]
+    v.copy_(y.to(dtype))
+    check_append(cache, k, v, rows, t, lens, [1] * 9, uniform=True)
+    # the same rows through prefix sums (a page at a time) give the same cache
+    other = random_cache(pages, 3, *dims, 32, weights=True)
+    other.k_scale.mul_(1.3)
+    psf.kv_cache_append(other, k, v, t, i32(lens), i32(list(range(10))))
+    for name in ("k", "v", "k_scale", "v_scale", "weight"):
+        a, b = getattr(cache, name), getattr(other, name)
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
 
 
 def test_append_values_at_the_borders():
