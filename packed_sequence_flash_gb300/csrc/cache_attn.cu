@@ -49,9 +49,10 @@ __global__ void __launch_bounds__(kWeightThreads) cache_weight_kernel(const __gr
 template <int DQK, int DV, int NT, bool EXTRA>
 cudaError_t run(CacheAttnParams& p, int max_q, int sms, cudaStream_t st) {
   using C = CaCfg<DQK, DV, NT>;
-  static std::atomic<uint64_t> main_set{0}, join_set{0};
+  static std::atomic<uint64_t> main_set{0}, unit_set{0}, share_set{0};
   cudaError_t e = kernel_setup(cache_attn_kernel<DQK, DV, NT, EXTRA>, C::SMEM, true, main_set);
-  if (e == cudaSuccess) e = kernel_setup(cache_join_kernel<DV>, 0, true, join_set);
+  if (e == cudaSuccess) e = kernel_setup(cache_join_kernel<DV, true>, 0, true, unit_set);
+  if (e == cudaSuccess) e = kernel_setup(cache_join_kernel<DV, false>, 0, true, share_set);
   if (e != cudaSuccess) return e;
   const int grid = sms * C::CTAS;
   p.tile_lg = NT == 1 ? 3 : 4;
@@ -59,9 +60,11 @@ cudaError_t run(CacheAttnParams& p, int max_q, int sms, cudaStream_t st) {
   e = launch_early(cache_attn_kernel<DQK, DV, NT, EXTRA>, dim3(grid), kCaThreads, C::SMEM, st, p);
   if (e != cudaSuccess) return e;
   const int64_t units = (int64_t)p.c.Hkv * p.row_tiles * p.s.B;
+  if (units > 2 * grid)  // fewer shares than units: a CTA per share
+    return launch_early(cache_join_kernel<DV, false>, dim3(grid), kJoinThreads, 0, st, p, grid);
   int parts = 1;
   while (parts < C::R && units * parts * 2 <= 2 * sms) parts *= 2;
-  return launch_early(cache_join_kernel<DV>, dim3(p.c.Hkv * p.row_tiles, p.s.B + (p.s.cu ? 1 : 0), parts),
+  return launch_early(cache_join_kernel<DV, true>, dim3(p.c.Hkv * p.row_tiles, p.s.B + (p.s.cu ? 1 : 0), parts),
                       kJoinThreads, 0, st, p, grid);
 }
 

@@ -183,6 +183,107 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                : "memory");
 }
 
+// By all threads of a block: the places of all sequences, and (with no more
+// sequences than threads) those of sequence `threadIdx.x` and before it.
+struct CaCount {
+  int64_t total, before, mine;
+};
+template <int THREADS>
+__device__ CaCount ca_count(const CacheAttnParams& p, int64_t* scan, bool record) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  CaCount r = {0, 0, 0};
+  for (int base = 0; base < p.s.B; base += THREADS) {
+    const int b = base + tid;
+    r.mine = 0;
+    if (b < p.s.B) {
+      const CaSeq s = ca_seq(p, b);
+      if (record && s.q.bad) record_status(p.status, kStatusDeviceArgs);
+      r.mine = s.places(p.c.Hkv);
+    }
+    int64_t x = r.mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (base) __syncthreads();
+    if (lane == 31) scan[warp] = x;
+    __syncthreads();
+    r.before = r.total + x - r.mine;
+    for (int w = 0; w < THREADS / 32; ++w) {
+      if (w < warp) r.before += scan[w];
+      r.total += scan[w];
+    }
+  }
+  return r;
+}
+// The sequence that place `pos` (< total) lies in, and the places before it, for all threads of the block.
+template <int THREADS>
+__device__ void ca_locate(const CacheAttnParams& p, int64_t* scan, const CaCount& count, int64_t pos, int* found_b,
+                          int64_t* found_base) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (p.s.B <= THREADS) {
+    if (count.mine > 0 && pos >= count.before && pos < count.before + count.mine) {
+      *found_b = tid;
+      *found_base = count.before;
+    }
+  } else {
+    int64_t carry = 0;
+    for (int base = 0; base < p.s.B; base += THREADS) {
+      const int b = base + tid;
+      const int64_t n = b < p.s.B ? ca_seq(p, b).places(p.c.Hkv) : 0;
+      int64_t x = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      __syncthreads();
+      if (lane == 31) scan[warp] = x;
+      __syncthreads();
+      int64_t at = carry;
+      for (int w = 0; w < THREADS / 32; ++w) {
+        if (w < warp) at += scan[w];
+        carry += scan[w];
+      }
+      if (n > 0 && pos >= at + x - n && pos < at + x) {
+        *found_b = b;
+        *found_base = at + x - n;
+      }
+      if (carry > pos) break;  // the same for every thread
+    }
+  }
+  __syncthreads();
+}
+
+// The same without a search: the places of all sequences, and those before
+// sequence `b`, for all threads of the block. (Two sums over the warps; the scan
+// above cost the join of one long sequence 0.6 us more.)
+template <int THREADS>
+__device__ int64_t ca_before(const CacheAttnParams& p, longlong2* sums, int b, int64_t* total) {
+  int64_t all = 0, before = 0;
+  for (int i = threadIdx.x; i < p.s.B; i += THREADS) {
+    const int64_t n = ca_seq(p, i).places(p.c.Hkv);
+    all += n;
+    before += i < b ? n : 0;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    all += __shfl_xor_sync(0xffffffffu, all, o);
+    before += __shfl_xor_sync(0xffffffffu, before, o);
+  }
+  if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = make_longlong2(all, before);
+  __syncthreads();
+  all = before = 0;
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) {
+    all += sums[w].x;
+    before += sums[w].y;
+  }
+  *total = all;
+  return before;
+}
+
 // One unit of a share, and the keys and tiles it concerns.
 struct CaUnit {
   int b, h, rt, n, m, q0;
@@ -274,68 +375,14 @@ __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV, NT>::CTAS)
 
   // The whole work, and the sequence that this share begins in.
   if (tid == 0 && blockIdx.x == 0 && cu_bad(p.s)) record_status(p.status, kStatusDeviceArgs);
-  int64_t total = 0, before = 0, count = 0;  // places before and of this thread's sequence
-  for (int base = 0; base < p.s.B; base += kCaThreads) {
-    const int b = base + tid;
-    count = 0;
-    if (b < p.s.B) {
-      const CaSeq s = ca_seq(p, b);
-      if (s.q.bad && blockIdx.x == 0) record_status(p.status, kStatusDeviceArgs);
-      count = s.places(p.c.Hkv);
-    }
-    int64_t x = count;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    if (base) __syncthreads();
-    if (lane == 31) scan[warp] = x;
-    __syncthreads();
-    before = total + x - count;
-    for (int w = 0; w < kCaThreads / 32; ++w) {
-      if (w < warp) before += scan[w];
-      total += scan[w];
-    }
-  }
-  const int parts = ca_parts(total, gridDim.x, p.min_share);
+  const CaCount count = ca_count<kCaThreads>(p, scan, blockIdx.x == 0);
+  const int parts = ca_parts(count.total, gridDim.x, p.min_share);
   if ((int)blockIdx.x >= parts) return;
-  const CaShares shares(total, parts);
+  const CaShares shares(count.total, parts);
   CaWalk walk;
   walk.pos = shares.first(blockIdx.x);
   walk.end = shares.first(blockIdx.x + 1);
-  if (p.s.B <= kCaThreads) {
-    if (count > 0 && walk.pos >= before && walk.pos < before + count) {
-      found_b = tid;
-      found_base = before;
-    }
-  } else {
-    int64_t carry = 0;
-    for (int base = 0; base < p.s.B; base += kCaThreads) {
-      const int b = base + tid;
-      const int64_t n = b < p.s.B ? ca_seq(p, b).places(p.c.Hkv) : 0;
-      int64_t x = n;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-      }
-      __syncthreads();
-      if (lane == 31) scan[warp] = x;
-      __syncthreads();
-      int64_t at = carry;
-      for (int w = 0; w < kCaThreads / 32; ++w) {
-        if (w < warp) at += scan[w];
-        carry += scan[w];
-      }
-      if (n > 0 && walk.pos >= at + x - n && walk.pos < at + x) {
-        found_b = b;
-        found_base = at + x - n;
-      }
-      if (carry > walk.pos) break;  // the same for every thread
-    }
-  }
-  __syncthreads();
+  ca_locate<kCaThreads>(p, scan, count, walk.pos, &found_b, &found_base);
   const Ctl ctl{p.status, p.limit_ns, &abort_flag};
 
   if (warp == kCaWarps) {
@@ -833,85 +880,89 @@ __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV, NT>::CTAS)
 }
 
 // Joins the partial results of units that several CTAs share, in the order of
-// the CTAs, and writes the rows that no CTA wrote: sequences without keys, and
-// (blockIdx.y = B) rows past the last sequence. One CTA per (head, row tile),
-// sequence and part of the row tile: rows go to CTAs of their own when there
-// are few units, whose partial results are then many (57 per unit for one
-// sequence of 32 Ki keys and 8 heads: 15 us with one CTA each).
+// the CTAs, and writes the rows that no CTA wrote: sequences without keys and
+// rows past the last sequence.
+// BY_UNIT: one CTA per (head, row tile), sequence and part of the row tile: rows
+// go to CTAs of their own when there are few units, whose partial results are
+// then many (57 per unit for one sequence of 32 Ki keys and 8 heads: 15 us with
+// one CTA each). blockIdx.y = B: rows past the last sequence.
+// Otherwise (more units than CTAs could share) one CTA per share, for the unit
+// that begins in it and goes on in the next one.
 constexpr int kJoinThreads = 512;
-template <int DV>
+template <int DV, bool BY_UNIT>
 __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_constant__ CacheAttnParams p, int grid) {
-  __shared__ int64_t sum_before[kJoinThreads / 32], sum_all[kJoinThreads / 32];
   __shared__ float4 sums[kJoinThreads];
   __shared__ float2 tops[kJoinThreads];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int b = blockIdx.y;
+  const int tid = threadIdx.x;
   let_next_kernel_start();
-  auto zero8 = [&](int64_t row, int hq, int d) {
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + p.o_ss * row + p.o_sh * hq + d) = make_uint4(0, 0, 0, 0);
+  auto zero_rows = [&](const Seq& q, int h, int n0, int count) {  // `count` rows of head h from row n0 of the tile order
+    for (int x = tid; x < count * (DV / 8); x += kJoinThreads) {
+      const int r = x / (DV / 8), y = n0 + r, i = y / p.G, hq = h * p.G + y - i * p.G;
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + p.o_ss * (q.q0 + i) + p.o_sh * hq +
+                                (x - r * (DV / 8)) * 8) = make_uint4(0, 0, 0, 0);
+      if (x == r * (DV / 8)) p.lse[(int64_t)hq * p.s.T + q.q0 + i] = -CUDART_INF_F;
+    }
   };
-  // Until the attention kernel is done: where this unit's partial results are.
-  const bool tail = b == p.s.B;
+  // Until the attention kernel is done: which unit this CTA joins, and where its
+  // partial results are.
+  const bool tail = BY_UNIT && blockIdx.y == p.s.B;
   CaSeq s = {};
-  if (!tail) s = ca_seq(p, b);
-  const int h = blockIdx.x / p.row_tiles, rt = blockIdx.x % p.row_tiles;
-  const int part = (1 << p.tile_lg) / gridDim.z, rows = s.q.m * p.G, n0 = (rt << p.tile_lg) + blockIdx.z * part;
-  const int live = tail || rt >= s.rt ? 0 : min(part, rows - n0);
-  if (!tail && live <= 0 && !first_block()) return;
-  int64_t before = 0, total = 0;
-  for (int x = tid; x < p.s.B; x += kJoinThreads) {
-    const int64_t n = ca_seq(p, x).places(p.c.Hkv);
-    total += n;
-    before += x < b ? n : 0;
+  int h = 0, n0 = 0, live = 0, c0 = 0, c1 = 0;  // rows [n0, n0 + live) of head h; shares c0 .. c1
+  const int part = BY_UNIT ? (1 << p.tile_lg) / gridDim.z : 1 << p.tile_lg;
+  if constexpr (BY_UNIT) {
+    if (!tail) s = ca_seq(p, blockIdx.y);
+    h = blockIdx.x / p.row_tiles;
+    const int rt = blockIdx.x % p.row_tiles;
+    n0 = (rt << p.tile_lg) + blockIdx.z * part;
+    live = tail || rt >= s.rt ? 0 : min(part, s.q.m * p.G - n0);
+    if (!tail && live <= 0 && !first_block()) return;
+    __shared__ longlong2 counts[kJoinThreads / 32];
+    int64_t total;
+    const int64_t before = ca_before<kJoinThreads>(p, counts, blockIdx.y, &total);
+    if (live > 0 && s.kt > 0) {
+      const CaShares shares(total, ca_parts(total, grid, p.min_share));
+      const int64_t x0 = before + ((int64_t)h * s.rt + rt) * s.cost() + kCaUnit;  // the unit's first tile
+      c0 = shares.owner(x0);
+      c1 = shares.owner(x0 + s.kt - 1);
+      if (c0 == c1 && !first_block()) return;  // one CTA had it all and wrote it
+    }
+  } else {
+    __shared__ int64_t scan[kJoinThreads / 32], found_base;
+    __shared__ int found_b;
+    const CaCount count = ca_count<kJoinThreads>(p, scan, false);
+    const int parts = ca_parts(count.total, grid, p.min_share);
+    if ((int)blockIdx.x + 1 < parts) {
+      const CaShares shares(count.total, parts);
+      const int64_t cut = shares.first(blockIdx.x + 1);
+      ca_locate<kJoinThreads>(p, scan, count, cut, &found_b, &found_base);
+      s = ca_seq(p, found_b);
+      const int64_t unit = quotient(cut - found_base, s.cost()), x0 = found_base + unit * s.cost() + kCaUnit;
+      c0 = shares.owner(x0);
+      c1 = shares.owner(x0 + s.kt - 1);
+      h = (int)(unit / s.rt);
+      n0 = (int)(unit - (int64_t)h * s.rt) << p.tile_lg;
+      live = c0 == (int)blockIdx.x ? min(part, s.q.m * p.G - n0) : 0;
+    }
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    total += __shfl_xor_sync(0xffffffffu, total, o);
-    before += __shfl_xor_sync(0xffffffffu, before, o);
-  }
-  if (lane == 0) {
-    sum_all[warp] = total;
-    sum_before[warp] = before;
-  }
-  __syncthreads();
-  total = before = 0;
-#pragma unroll
-  for (int w = 0; w < kJoinThreads / 32; ++w) {
-    total += sum_all[w];
-    before += sum_before[w];
-  }
-  const CaShares shares(total, ca_parts(total, grid, p.min_share));
-  const int64_t x0 = before + ((int64_t)h * s.rt + rt) * s.cost() + kCaUnit;  // the unit's first tile
-  const bool split = live > 0 && s.kt > 0;
-  const int c0 = split ? shares.owner(x0) : 0, c1 = split ? shares.owner(x0 + s.kt - 1) : 0;
-  const bool done = split && c0 == c1;  // one CTA had it all and wrote it
-  if (done && !first_block()) return;
   after_previous_kernel();
-  if (tail) {  // rows past the last sequence
-    if (blockIdx.z) return;
-    const int first = min(max(p.s.cu[p.s.B], 0), p.s.T);
-    for (int64_t x = (int64_t)blockIdx.x * kJoinThreads + tid; x < (int64_t)(p.s.T - first) * p.Hq;
-         x += (int64_t)gridDim.x * kJoinThreads) {
-      const int64_t row = first + x / p.Hq;
-      const int hq = (int)(x % p.Hq);
-      for (int d = 0; d < DV; d += 8) zero8(row, hq, d);
-      p.lse[(int64_t)hq * p.s.T + row] = -CUDART_INF_F;
-    }
-    return;
+  if (tail || !BY_UNIT) {  // rows past the last sequence
+    const int first = p.s.cu ? min(max(p.s.cu[p.s.B], 0), p.s.T) : p.s.T;
+    const Seq rest = {0, p.s.T - first, first, false};
+    if (rest.m > 0 && blockIdx.z == 0)
+      for (int64_t x = blockIdx.x; x < (int64_t)rest.m * p.c.Hkv; x += gridDim.x)
+        zero_rows(rest, (int)(x % p.c.Hkv), (int)(x / p.c.Hkv) * p.G, p.G);
   }
-  if (live <= 0 || done) return;
-  if (s.kt == 0) {  // a sequence without keys
-    for (int x = tid; x < live * (DV / 8); x += kJoinThreads) {
-      const int r = x / (DV / 8), y = n0 + r, i = y / p.G;
-      zero8(s.q.q0 + i, h * p.G + y - i * p.G, (x - r * (DV / 8)) * 8);
+  if constexpr (BY_UNIT) {
+    if (live > 0 && s.kt == 0) zero_rows(s.q, h, n0, live);  // a sequence without keys
+  } else {
+    for (int b = blockIdx.x; b < p.s.B; b += gridDim.x) {
+      const CaSeq e = ca_seq(p, b);
+      if (e.kt == 0 && e.q.m > 0)
+        for (int x = 0; x < p.c.Hkv; ++x) zero_rows(e.q, x, 0, e.q.m * p.G);
     }
-    if (tid < live) {
-      const int y = n0 + tid, i = y / p.G;
-      p.lse[(int64_t)(h * p.G + y - i * p.G) * p.s.T + s.q.q0 + i] = -CUDART_INF_F;
-    }
-    return;
   }
-  const int np = c1 - c0 + 1, at0 = blockIdx.z * part;
+  if (live <= 0 || c0 == c1) return;
+  const int np = c1 - c0 + 1, at0 = BY_UNIT ? blockIdx.z * part : 0;
   auto row_at = [&](int i, int r) -> int64_t { return (((int64_t)(c0 + i) * 2 + (i == 0)) << p.tile_lg) + at0 + r; };
   // A thread takes four columns of a row over every groups-th partial result, with
   // a running maximum and sum of its own; the groups are added in their order.
