@@ -112,7 +112,8 @@ struct CaSeq {
   __device__ __forceinline__ int cost() const { return kt + kCaUnit; }
   __device__ __forceinline__ int64_t places(int Hkv) const { return kt ? (int64_t)Hkv * rt * cost() : 0; }
 };
-__device__ __forceinline__ CaSeq ca_seq(const CacheAttnParams& p, int b) {
+template <typename P>  // CacheAttnParams or what ca_seq needs of it
+__device__ __forceinline__ CaSeq ca_seq(const P& p, int b) {
   CaSeq s;
   s.q = seq_at(p.s, p.c.page, b);
   const int lo = p.window > 0 ? max(0, s.q.n - s.q.m - p.window + 1) : 0;
@@ -183,75 +184,93 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                : "memory");
 }
 
-// By all threads of a block: the places of all sequences, and (with no more
-// sequences than threads) those of sequence `threadIdx.x` and before it.
+// By all threads of a block: the places of all sequences, and those before and in
+// this thread's run of `per` neighbouring sequences. A run's loads do not wait
+// for one another; with a scan per THREADS sequences, 4096 of them took 45 us.
 struct CaCount {
   int64_t total, before, mine;
+  int first, per;
 };
+// (Calls of their own, with the parameters in registers: as part of the kernels
+// these loops made one sequence of 777 keys 0.5 us slower, which takes neither.)
+struct CaFew {
+  SeqView s;
+  struct {
+    int page, Hkv;
+  } c;
+  int window, G, tile_lg;
+  __device__ __forceinline__ explicit CaFew(const CacheAttnParams& p)
+      : s(p.s), c{p.c.page, p.c.Hkv}, window(p.window), G(p.G), tile_lg(p.tile_lg) {}
+};
+__device__ __noinline__ int64_t ca_run_places(const CacheAttnParams& params, int first, int per, bool record) {
+  const CaFew p(params);
+  int64_t n = 0;
+  bool bad = false;
+#pragma unroll 8
+  for (int i = 0; i < per; ++i)
+    if (first + i < p.s.B) {
+      const CaSeq s = ca_seq(p, first + i);
+      bad |= s.q.bad;
+      n += s.places(p.c.Hkv);
+    }
+  if (record && bad) record_status(params.status, kStatusDeviceArgs);
+  return n;
+}
+// The sequence of a run that place `pos` lies in; *base: the places before the run, and then those before the sequence.
+__device__ __noinline__ int ca_run_find(const CacheAttnParams& params, int first, int per, int64_t pos, int64_t* base) {
+  const CaFew p(params);
+  int b = first;
+  int64_t end = *base, at = end;
+#pragma unroll 8
+  for (int i = 0; i < per; ++i) {
+    const int x = min(first + i, p.s.B - 1);  // (more than once the last: `end` is above `pos` by then)
+    end += ca_seq(p, x).places(p.c.Hkv);
+    if (end <= pos) {
+      b = x + 1;
+      at = end;
+    }
+  }
+  *base = at;
+  return b;
+}
 template <int THREADS>
-__device__ CaCount ca_count(const CacheAttnParams& p, int64_t* scan, bool record) {
+__device__ __forceinline__ CaCount ca_count(const CacheAttnParams& p, int64_t* scan, bool record) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  CaCount r = {0, 0, 0};
-  for (int base = 0; base < p.s.B; base += THREADS) {
-    const int b = base + tid;
-    r.mine = 0;
-    if (b < p.s.B) {
-      const CaSeq s = ca_seq(p, b);
+  CaCount r = {0, 0, 0, tid, 1};
+  if (p.s.B <= THREADS) {
+    if (tid < p.s.B) {
+      const CaSeq s = ca_seq(p, tid);
       if (record && s.q.bad) record_status(p.status, kStatusDeviceArgs);
       r.mine = s.places(p.c.Hkv);
     }
-    int64_t x = r.mine;
+  } else {
+    r.per = (p.s.B + THREADS - 1) / THREADS;
+    r.first = tid * r.per;
+    r.mine = ca_run_places(p, r.first, r.per, record);
+  }
+  int64_t x = r.mine;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    if (base) __syncthreads();
-    if (lane == 31) scan[warp] = x;
-    __syncthreads();
-    r.before = r.total + x - r.mine;
-    for (int w = 0; w < THREADS / 32; ++w) {
-      if (w < warp) r.before += scan[w];
-      r.total += scan[w];
-    }
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) scan[warp] = x;
+  __syncthreads();
+  r.before = x - r.mine;
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) {
+    if (w < warp) r.before += scan[w];
+    r.total += scan[w];
   }
   return r;
 }
 // The sequence that place `pos` (< total) lies in, and the places before it, for all threads of the block.
-template <int THREADS>
-__device__ void ca_locate(const CacheAttnParams& p, int64_t* scan, const CaCount& count, int64_t pos, int* found_b,
-                          int64_t* found_base) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (p.s.B <= THREADS) {
-    if (count.mine > 0 && pos >= count.before && pos < count.before + count.mine) {
-      *found_b = tid;
-      *found_base = count.before;
-    }
-  } else {
-    int64_t carry = 0;
-    for (int base = 0; base < p.s.B; base += THREADS) {
-      const int b = base + tid;
-      const int64_t n = b < p.s.B ? ca_seq(p, b).places(p.c.Hkv) : 0;
-      int64_t x = n;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-      }
-      __syncthreads();
-      if (lane == 31) scan[warp] = x;
-      __syncthreads();
-      int64_t at = carry;
-      for (int w = 0; w < THREADS / 32; ++w) {
-        if (w < warp) at += scan[w];
-        carry += scan[w];
-      }
-      if (n > 0 && pos >= at + x - n && pos < at + x) {
-        *found_b = b;
-        *found_base = at + x - n;
-      }
-      if (carry > pos) break;  // the same for every thread
-    }
+__device__ __forceinline__ void ca_locate(const CacheAttnParams& p, const CaCount& count, int64_t pos, int* found_b,
+                                          int64_t* found_base) {
+  if (pos >= count.before && pos < count.before + count.mine) {
+    int64_t base = count.before;
+    *found_b = count.per == 1 ? count.first : ca_run_find(p, count.first, count.per, pos, &base);
+    *found_base = base;
   }
   __syncthreads();
 }
@@ -382,7 +401,7 @@ __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV, NT>::CTAS)
   CaWalk walk;
   walk.pos = shares.first(blockIdx.x);
   walk.end = shares.first(blockIdx.x + 1);
-  ca_locate<kCaThreads>(p, scan, count, walk.pos, &found_b, &found_base);
+  ca_locate(p, count, walk.pos, &found_b, &found_base);
   const Ctl ctl{p.status, p.limit_ns, &abort_flag};
 
   if (warp == kCaWarps) {
@@ -934,7 +953,7 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
     if ((int)blockIdx.x + 1 < parts) {
       const CaShares shares(count.total, parts);
       const int64_t cut = shares.first(blockIdx.x + 1);
-      ca_locate<kJoinThreads>(p, scan, count, cut, &found_b, &found_base);
+      ca_locate(p, count, cut, &found_b, &found_base);
       s = ca_seq(p, found_b);
       const int64_t unit = quotient(cut - found_base, s.cost()), x0 = found_base + unit * s.cost() + kCaUnit;
       c0 = shares.owner(x0);
