@@ -451,7 +451,9 @@ typedef struct {
  *  exact down to the format's subnormals. New codes are RNE_e4m3(x / scale); a
  *  value that is not finite becomes NaN. The weights of new tokens become 0.
  *  Rows of T past cu_new[B] are not read; rows of a page past the new ones keep
- *  their contents. A page that is written belongs to one sequence.
+ *  their contents. A page that is written belongs to one sequence. A sequence
+ *  with more new rows than tokens takes none (a PSF_EDEVICE_ARGS status): idle
+ *  entries of a batch have no rows in cu_new.
  *  strides: NULL, or 6 element strides (batch, head, row) of k, v (batch ignored).
  */
 int psf_kv_cache_append(const psf_kv_cache* cache, const void* k, const void* v, const int64_t* strides, int dtype,
@@ -477,7 +479,8 @@ int psf_kv_cache_append(const psf_kv_cache* cache, const void* k, const void* v,
  *  is not fixed. Other bits: PSF_EINVAL.
  *  strides: NULL, or 6 element strides (batch, head, row) of q, out (batch ignored).
  *  workspace: psf_attn_cache_workspace_size(...) bytes, 16-byte aligned; nothing in it
- *  has to be kept or cleared between calls.
+ *  has to be kept or cleared between calls. (With PSF_CACHE_ACCUMULATE it holds the
+ *  scores, 4 B * Hq * max_q * max_pages * page_size bytes more; SIZE_MAX where no memory holds them.)
  */
 #define PSF_CACHE_ACCUMULATE 1
 size_t psf_attn_cache_workspace_size(int B, int max_pages, int page_size, int Hq, int Hkv, int Dqk, int Dv,

@@ -690,7 +690,9 @@ size_t cache_attn_ws_layout(int B, int max_pages, int page_size, int Hq, int Hkv
     p->score_rows = rows;
     p->score_cap = cap;
   }
-  return s_off + (accumulate ? sizeof(float) * (size_t)(B * (int64_t)Hkv * rows * cap) : 0);
+  if (!accumulate) return s_off;
+  if ((double)B * Hkv * rows * cap > 1e18) return SIZE_MAX;  // no memory holds it
+  return s_off + sizeof(float) * (size_t)(B * (int64_t)Hkv * rows * cap);
 }
 
 // TMA view (d, row, head, page) of cache codes: boxes of one plane of a page's
@@ -708,6 +710,7 @@ size_t evict_ws_layout(int B, int max_pages, int page_size, int Hkv, int budget,
   const int64_t units = (int64_t)B * Hkv, cap = (int64_t)max_pages * page_size;
   // A sequence longer than the budget is what makes a unit use its part.
   const int64_t kept = budget < cap ? budget : cap, blocks = (kept + page_size - 1) / page_size;
+  if ((double)units * (4.0 * kept + cap) > 1e17) return SIZE_MAX;  // no memory holds it
   size_t off = 0;
   const size_t live = off;
   off += align256(sizeof(int) * (size_t)units);

@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(kAppendThreads, 8)
 // One new row per sequence (a decode step): a warp per (sequence, K or V, head).
 // Latency bounds it: length -> page -> old scale, the row's largest magnitude in
 // a warp, at most a page of older codes when the scale grew. 64 sequences of 8
-// heads: 3.7 us; 4096: 27.5 us. With a CTA each, as above, 6.6 and 252 us.
+// heads: 3.7 us; 4096: 30 us. With a CTA each, as above, 6.6 and 252 us.
 template <typename T>
 __global__ void __launch_bounds__(kAppendThreads)
     append_one_kernel(CacheView c, SeqView s, const T* kin, int64_t k_ss, int64_t k_sh, const T* vin, int64_t v_ss,

@@ -150,3 +150,12 @@ def test_reference_rounding_and_scale():
     assert torch.equal(ref.e4m3(x.float().double()), x.float().to(torch.float8_e4m3fn).double())
     assert ref.scale_of(448.0) == 1.0 and ref.scale_of(448.5) == 2.0 and ref.scale_of(224.0) == 0.5
     assert ref.scale_of(0.0) == 2.0 ** -126 and ref.scale_of(1e-45) == 2.0 ** -126
+
+
+def test_workspace_sizes_that_no_memory_holds(lib):
+    """Products past 2^64 do not come out as small sizes: a call with such a workspace is refused."""
+    big = 2 ** 64 - 1
+    assert lib.psf_attn_cache_workspace_size(65534, 2 ** 24 - 1, 128, 4096, 2, 128, 128, 2 ** 19 - 1, 1) == big
+    assert lib.psf_attn_cache_workspace_size(65534, 2 ** 24 - 1, 128, 4096, 2, 128, 128, 2 ** 19 - 1, 0) < 2 ** 30
+    assert lib.psf_kv_cache_evict_workspace_size(65534, 2 ** 24 - 1, 128, 65535, 2 ** 31 - 1) == big
+    assert attend(lib, B=65534, max_pages=2 ** 23, page_size=128, Hq=4096, max_q=2 ** 18, flags=1) == EWORKSPACE

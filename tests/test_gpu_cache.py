@@ -596,6 +596,26 @@ def test_prefix_sums_that_cannot_be(cu):
     assert torch.equal(cache.k.view(torch.uint8)[~owned], before[~owned])
 
 
+@pytest.mark.parametrize("cu,each", [(None, 1), (None, 3), ([0, 3, 4, 6], 0)])
+def test_more_new_rows_than_tokens(cu, each):
+    """Such a sequence takes none and says so; the others take theirs. An idle entry without rows is fine."""
+    lens = [0, 30, 2] if each != 3 else [2, 30, 0]
+    rows, t, pages = tables([16, 30, 16], 16)
+    cache = random_cache(pages, 2, 64, 64, 16)
+    c = ref.from_cache(cache)
+    x = torch.randn(3 * each or 6, 2, 64, generator=torch.Generator().manual_seed(5)).bfloat16().cuda()
+    psf.kv_cache_append(cache, x, x, t, i32(lens), None if cu is None else i32(cu))
+    assert psf.device_status() == EDEVICE_ARGS
+    at = prefix([each] * 3) if cu is None else cu
+    for b in (1, 2) if each != 3 else (1,):
+        ref.append(c, x, x, [[], [], []][:b] + [rows[b]], [0] * b + [lens[b]], [at[b]] * (b + 1) + [at[b + 1]])
+    same(cache, c)
+    psf.kv_cache_append(cache, x[:3], x[:3], t, i32([14, 0, 5]), i32([0, 2, 2, 3]))
+    assert psf.device_status() == 0
+    ref.append(c, x[:3], x[:3], rows, [14, 0, 5], [0, 2, 2, 3])
+    same(cache, c)
+
+
 def test_numbers_of_other_kinds():
     import numpy as np
 
