@@ -544,13 +544,15 @@ __global__ void __launch_bounds__(kSelectThreads, 2)
 
 // Moves the codes: one CTA per (head, sequence, K or V, column slice), the kept
 // tokens in order and in batches. A token never moves up, so a batch's writes
-// touch nothing that a later batch still has to read: read a batch, wait, write
-// it. Slices of a row go to CTAs of their own when (head, sequence) pairs alone
+// touch nothing that a later batch still has to read: the next batch is on its
+// way while one is written, which waits only until all of its own rows are read.
+// Slices of a row go to CTAs of their own when (head, sequence) pairs alone
 // would not fill the device. Bound by memory: every kept code is read and written
 // once, in rows of 128 bytes scattered over the old pages; 384 heads x 4096 of
-// 11 Ki tokens of head dim 128 move 786 MB in 156 us, three quarters of a copy's rate.
+// 11 Ki tokens of head dim 128 move 786 MB in 140 us, 0.82 of a copy's rate (156 us
+// with a batch read only after the one before was written).
 constexpr int kMoveThreads = 256;
-constexpr int kMoveVecs = 4;  // of a batch per thread; more made the rows' reads and writes slower (8: 306 us for 239)
+constexpr int kMoveVecs = 2;  // of a batch per thread; with 3 or 4 fewer CTAs fit an SM (4: 227 us for 183 in all)
 __global__ void __launch_bounds__(kMoveThreads, 6)
     evict_move_kernel(CacheView c, SeqView s, int budget, EvictWorkspace ws, int slices) {
   const int tid = threadIdx.x, h = blockIdx.x, b = blockIdx.y;
@@ -566,19 +568,37 @@ __global__ void __launch_bounds__(kMoveThreads, 6)
   const int last = mine < rows ? budget : 0;  // threads past the rows of a pass have none
   after_previous_kernel();
   if (!ws.live[unit]) return;
-  for (int j0 = mine; j0 - mine < budget; j0 += rows * kMoveVecs) {
-    uint4 x[kMoveVecs];
-    float r[kMoveVecs];
+  uint4 x[kMoveVecs], next[kMoveVecs];
+  float r[kMoveVecs], r_next[kMoveVecs];
+  int2 at[kMoveVecs];  // page and row of the next batch's tokens
+  auto look = [&](int j0) {
 #pragma unroll
     for (int u = 0; u < kMoveVecs; ++u) {
       const int j = j0 + u * rows;
       if (j < last) {
         const int4 from = items[j];
-        r[u] = __int_as_float(is_v ? from.w : from.z);
-        x[u] = *reinterpret_cast<const uint4*>(base + sp * from.x + sr * from.y);
+        at[u] = make_int2(from.x, from.y);
+        r_next[u] = __int_as_float(is_v ? from.w : from.z);
       }
     }
-    __syncthreads();
+  };
+  auto load = [&](int j0) {
+#pragma unroll
+    for (int u = 0; u < kMoveVecs; ++u)
+      if (j0 + u * rows < last) next[u] = *reinterpret_cast<const uint4*>(base + sp * at[u].x + sr * at[u].y);
+  };
+  const int step = rows * kMoveVecs;
+  look(mine);
+  load(mine);
+  for (int j0 = mine; j0 - mine < budget; j0 += step) {
+#pragma unroll
+    for (int u = 0; u < kMoveVecs; ++u) {
+      x[u] = next[u];
+      r[u] = r_next[u];
+    }
+    look(j0 + step);
+    __syncthreads();  // the batch is read
+    load(j0 + step);
 #pragma unroll
     for (int u = 0; u < kMoveVecs; ++u) {
       const int j = j0 + u * rows;
