@@ -1037,6 +1037,7 @@ int psf_attn_cache_fwd(const void* q, const psf_kv_cache* cache, void* out, floa
     return fail(PSF_EWORKSPACE, "cache attention workspace needs %zu bytes, 16-byte aligned (got %zu)", need, ws_bytes);
   DeviceInfo* dev = nullptr;
   if ((rc = device_info(&dev))) return rc;
+  if (dev->sms > kMaxSms) return fail(PSF_EUNSUPPORTED, "more than %d SMs", kMaxSms);
   p.s.max_rows = max_q;
   p.q = q;
   p.q_ss = vq.ss;

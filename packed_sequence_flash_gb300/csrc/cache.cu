@@ -549,7 +549,7 @@ __global__ void __launch_bounds__(kSelectThreads, 2)
 // Slices of a row go to CTAs of their own when (head, sequence) pairs alone
 // would not fill the device. Bound by memory: every kept code is read and written
 // once, in rows of 128 bytes scattered over the old pages; 384 heads x 4096 of
-// 11 Ki tokens of head dim 128 move 786 MB in 140 us, 0.82 of a copy's rate (156 us
+// 11 Ki tokens of head dim 128 move 786 MB in 136 us, 0.85 of a copy's rate (156 us
 // with a batch read only after the one before was written).
 constexpr int kMoveThreads = 256;
 constexpr int kMoveVecs = 2;  // of a batch per thread; with 3 or 4 fewer CTAs fit an SM (4: 227 us for 183 in all)
