@@ -497,7 +497,8 @@ int psf_attn_cache_fwd(const void* q, const psf_kv_cache* cache, void* out, floa
  *  weights the earliest; NaN counts as the largest, -0 as 0), in their order, moved to
  *  positions 0 .. budget - 1; weights move along. new_lens[b] = min(seq_lens[b],
  *  budget); other sequences are not touched. A new block's scale is the largest
- *  old scale of its tokens, codes become RNE_e4m3(c * (old / new)). Rows past the
+ *  old scale of its tokens, codes become RNE_e4m3(c * r), r = old / new in fp32 (exact
+ *  for powers of two, the scales that the append chooses). Rows past the
  *  kept ones keep their contents; pages past ceil(budget / page_size) are free.
  *  After an eviction positions count kept tokens (so do windows).
  *  A sequence with a page that does not exist is left as it is, its new length
@@ -513,8 +514,8 @@ int psf_kv_cache_evict(const psf_kv_cache* cache, const int32_t* page_table, con
 /*
  * The cached rows of all sequences as packed 16-bit tensors.
  *  k [total_k, Hkv, Dqk], v [total_k, Hkv, Dv] (dtype, contiguous): row
- *  cu_k[b] + j is token j of sequence b, code * scale rounded once (with scales
- *  written by the append, exact in bf16). cu_k int32 [B + 1]: prefix sums of
+ *  cu_k[b] + j is token j of sequence b, code * scale in fp32 rounded to the type
+ *  (with scales written by the append, exact in bf16). cu_k int32 [B + 1]: prefix sums of
  *  seq_lens. With q, cu_k and these the varlen forward attends a long prompt
  *  chunk over its cached prefix. total_k bounds the sum of the lengths (more is a
  *  PSF_EDEVICE_ARGS status, and the rows past it are dropped); rows past cu_k[B]

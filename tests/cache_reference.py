@@ -150,7 +150,7 @@ def evict(c, table, lens, budget, recent):
                     r0, r1 = p * page, min((p + 1) * page, budget)
                     s = max(old[r0:r1])
                     for r in range(r0, r1):
-                        ratio = old[r] / s if s > 0 else 1.0
+                        ratio = float(torch.tensor(old[r] / s, dtype=torch.float32)) if s > 0 else 1.0  # as declared
                         c[name][table[b][p], h, r - r0] = e4m3(x[r] * ratio)
                     c[name + "s"][table[b][p], h] = s
             w = [float(at("w", j)) for j in kept]

@@ -768,6 +768,18 @@ def test_evict_ties_and_odd_weights():
     check_evict(cache, rows, t, lens, 150, 10)
 
 
+def test_evict_scales_that_are_no_powers_of_two():
+    """Ratios that fp32 rounds (17/16 over 3/2), ones whose products are ties (1/2, 13/16), and a zero scale."""
+    lens = [150, 90, 300]
+    rows, t, pages = tables(lens, 16)
+    cache = random_cache(pages, 2, 128, 128, 16, weights=True)
+    g = torch.Generator().manual_seed(9)
+    scales = torch.tensor([17 / 16, 3 / 2, 1.3, 0.65, 1.0, 0.5, 13 / 16, 0.0, 1.7, 1e-3])
+    for x in (cache.k_scale, cache.v_scale):
+        x.copy_(scales[torch.randint(0, len(scales), x.shape, generator=g)])
+    check_evict(cache, rows, t, lens, 80, 20)
+
+
 def test_evict_sequence_longer_than_shared_memory_holds():
     n = 50000
     rows, t, pages = tables([n, 200], 128)
