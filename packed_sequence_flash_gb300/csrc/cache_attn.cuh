@@ -449,53 +449,59 @@ __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV, NT>::CTAS)
       ++nu;
       return true;
     };
+    // The first unit is an empty one, which only looks for the next: the code for
+    // that stands here once (instructions are fetched anew for every short unit).
     CaUnit u, next;
-    bool more = walk.next(p, u);
-    int pg = more ? page_at(u, u.ta) : -1;
-    ok = announce(more, u);
+    u.b = u.h = u.lo = u.hi = u.ta = u.tb = 0;
+    int pg = -1;
+    bool more = true;
     while (ok && more) {
       float2 sc = scales_at(u.h, pg);
       int pg_next = page_at(u, u.ta + 8), pg_unit = -1;
-      bool looked = false, more_next = false;
-      for (int t8 = u.ta; ok && t8 < u.tb; t8 += 8) {
+      bool first = true;
+      for (int t8 = u.ta; ok && (first || t8 < u.tb); t8 += 8) {
         float2 sc_next = make_float2(0.f, 1.f);
         int pg_after = -1;
-        for (int i = 0; i < 8 && t8 + i < u.tb; ++i, ++it) {
-          const int st = it % C::STAGES;
-          if (it >= C::STAGES && !wait_bar(&empty[st], ((it / C::STAGES) - 1) & 1, ctl)) {
-            ok = false;
-            break;
-          }
-          const int key0 = (t8 + i) * kCaKeys;
-          uint8_t* dst = smem + st * C::STAGE;
-          const int b0 = max(u.lo - key0, 0) / box, b1 = min((u.hi - key0 + box - 1) / box, boxes);
-          if (lane == 0) mbar_expect_tx(&full[st], (uint32_t)(b1 - b0) * box * C::ROWB * (C::KP + C::VP));
-          for (int x = b0; x < b1; ++x) {
-            const int use = __shfl_sync(0xffffffffu, pg, i * 4 + x * per_box);
-            if (lane == 0) {
-              const int row = (key0 + x * box) & (p.c.page - 1);
-#pragma unroll
-              for (int k = 0; k < C::KP; ++k)
-                tma_load_4d(dst + k * C::PLANE + x * box * C::ROWB, &p.tm_k, &full[st], k * 128, row, u.h, use);
-#pragma unroll
-              for (int k = 0; k < C::VP; ++k)
-                tma_load_4d(dst + (C::KP + k) * C::PLANE + x * box * C::ROWB, &p.tm_v, &full[st], k * 128, row, u.h,
-                            use);
+#pragma unroll 1
+        for (int i = 0; i < 8 && (first || t8 + i < u.tb); ++i) {
+          if (t8 + i < u.tb) {
+            const int st = it % C::STAGES;
+            if (it >= C::STAGES && !wait_bar(&empty[st], ((it / C::STAGES) - 1) & 1, ctl)) {
+              ok = false;
+              break;
             }
+            const int key0 = (t8 + i) * kCaKeys;
+            uint8_t* dst = smem + st * C::STAGE;
+            const int b0 = max(u.lo - key0, 0) / box, b1 = min((u.hi - key0 + box - 1) / box, boxes);
+            if (lane == 0) mbar_expect_tx(&full[st], (uint32_t)(b1 - b0) * box * C::ROWB * (C::KP + C::VP));
+            for (int x = b0; x < b1; ++x) {
+              const int use = __shfl_sync(0xffffffffu, pg, i * 4 + x * per_box);
+              if (lane == 0) {
+                const int row = (key0 + x * box) & (p.c.page - 1);
+#pragma unroll
+                for (int k = 0; k < C::KP; ++k)
+                  tma_load_4d(dst + k * C::PLANE + x * box * C::ROWB, &p.tm_k, &full[st], k * 128, row, u.h, use);
+#pragma unroll
+                for (int k = 0; k < C::VP; ++k)
+                  tma_load_4d(dst + (C::KP + k) * C::PLANE + x * box * C::ROWB, &p.tm_v, &full[st], k * 128, row, u.h,
+                              use);
+              }
+            }
+            // The scales are waited for only here, with the codes on their way.
+            if ((lane >> 2) == i) meta[st][lane & 3] = make_float2(sc.x, log2f(sc.y));
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&full[st]);
+            ++it;
           }
-          // The scales are waited for only here, with the codes on their way.
-          if ((lane >> 2) == i) meta[st][lane & 3] = make_float2(sc.x, log2f(sc.y));
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&full[st]);
           if (i == 0) {
             sc_next = scales_at(u.h, pg_next);
             pg_after = page_at(u, t8 + 16);
-            if (!looked) {
+            if (first) {
               // With the first tile out: which unit comes next, its queries and first pages.
-              looked = true;
-              more_next = walk.next(p, next);
-              if (more_next) pg_unit = page_at(next, next.ta);
-              if (!announce(more_next, next)) ok = false;
+              first = false;
+              more = walk.next(p, next);
+              if (more) pg_unit = page_at(next, next.ta);
+              if (!announce(more, next)) ok = false;
             }
           }
         }
@@ -503,12 +509,6 @@ __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV, NT>::CTAS)
         sc = sc_next;
         pg_next = pg_after;
       }
-      if (!looked) {  // a unit whose rows see no key
-        more_next = walk.next(p, next);
-        if (more_next) pg_unit = page_at(next, next.ta);
-        ok = announce(more_next, next);
-      }
-      more = more_next;
       u = next;
       pg = pg_unit;
     }
