@@ -141,6 +141,11 @@ struct CaShares {
   }
 };
 
+// x / G for a row x of the tile order (token-major), 0 <= x < 2^31, G's reciprocal rounded up to 33 bits: exact.
+__device__ __forceinline__ int ca_token(const CacheAttnParams& p, int x) {
+  return (int)((__umulhi((uint32_t)x, p.g_mul) + (uint32_t)x) >> p.g_shift);
+}
+
 // Keys [lo, hi) that row i of m sees of n cached tokens (the last row sits at the last token).
 __device__ __forceinline__ void ca_row_keys(const CacheAttnParams& p, int n, int m, int i, int& lo, int& hi) {
   const int at = i + n - m;
@@ -315,26 +320,38 @@ struct CaUnit {
   float* scores;     // where the tile's first row keeps its scores
 };
 struct CaWalk {
-  int64_t pos, end, base;
-  int b;
+  int64_t left;       // places still to come
+  int b, h, rt, off;  // the unit they begin in, and how far into it
   CaSeq s;
+  __device__ __forceinline__ void start(const CacheAttnParams& p, int64_t pos, int64_t end, int seq, int64_t base) {
+    left = end - pos;
+    b = seq;
+    s = ca_seq(p, b);
+    const int64_t x = quotient(pos - base, s.cost());
+    off = (int)(pos - base - x * s.cost());
+    h = (int)quotient(x, s.rt);
+    rt = (int)(x - (int64_t)h * s.rt);
+  }
   __device__ __forceinline__ bool next(const CacheAttnParams& p, CaUnit& u) {
-    while (pos < end) {
-      int64_t n = s.places(p.c.Hkv);
-      while (pos >= base + n) {
-        base += n;
-        s = ca_seq(p, ++b);
-        n = s.places(p.c.Hkv);
+    while (left > 0) {
+      if (h == p.c.Hkv || s.kt == 0) {
+        if (++b >= p.s.B) return false;
+        s = ca_seq(p, b);
+        h = rt = off = 0;
+        continue;
       }
-      const int64_t rel = pos - base, x = quotient(rel, s.cost());
-      const int off = (int)(rel - x * s.cost());
-      const int stop = (int)min((int64_t)s.cost(), off + (end - pos));
-      pos += stop - off;
+      const int stop = (int)min((int64_t)s.cost(), off + left);
       const int k0 = max(off - kCaUnit, 0), k1 = stop - kCaUnit;
+      u.h = h;
+      u.rt = rt;
+      left -= stop - off;
+      off = 0;
+      if (++rt == s.rt) {
+        rt = 0;
+        ++h;
+      }
       if (k1 <= k0) continue;  // nothing but the places in front of the tiles
       u.b = b;
-      u.h = (int)(x / s.rt);
-      u.rt = (int)(x - (int64_t)u.h * s.rt);
       u.n = s.q.n;
       u.m = s.q.m;
       u.q0 = s.q.q0;
@@ -342,7 +359,7 @@ struct CaWalk {
       u.t1 = s.t0 + k1;
       u.whole = k1 - k0 == s.kt;
       u.slot = k0 == 0;
-      const int i0 = (u.rt << p.tile_lg) / p.G, i1 = (min((u.rt + 1) << p.tile_lg, u.m * p.G) - 1) / p.G;
+      const int i0 = ca_token(p, u.rt << p.tile_lg), i1 = ca_token(p, min((u.rt + 1) << p.tile_lg, u.m * p.G) - 1);
       ca_row_keys(p, u.n, u.m, i0, u.lo, u.in_hi);
       ca_row_keys(p, u.n, u.m, i1, u.in_lo, u.hi);
       u.scores = p.scores + (((int64_t)b * p.c.Hkv + u.h) * p.score_rows + (u.rt << p.tile_lg)) * p.score_cap;
@@ -398,18 +415,15 @@ __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV, NT>::CTAS)
   const int parts = ca_parts(count.total, gridDim.x, p.min_share);
   if ((int)blockIdx.x >= parts) return;
   const CaShares shares(count.total, parts);
-  CaWalk walk;
-  walk.pos = shares.first(blockIdx.x);
-  walk.end = shares.first(blockIdx.x + 1);
-  ca_locate(p, count, walk.pos, &found_b, &found_base);
+  const int64_t pos = shares.first(blockIdx.x);
+  ca_locate(p, count, pos, &found_b, &found_base);
   const Ctl ctl{p.status, p.limit_ns, &abort_flag};
 
   if (warp == kCaWarps) {
     // ------------------------------------------------------------ producer
-    walk.b = found_b;
-    walk.base = found_base;
-    walk.s = ca_seq(p, found_b);
-    const int box = min(p.c.page, kCaKeys), per_box = box / 16, boxes = kCaKeys / box;
+    CaWalk walk;
+    walk.start(p, pos, shares.first(blockIdx.x + 1), found_b, found_base);
+    const int box_lg = min(p.c.page_lg, 6), box = 1 << box_lg, per_box = box / 16, boxes = kCaKeys >> box_lg;
     uint32_t it = 0, nu = 0;
     bool ok = true;
     // Lane l looks after 16-key slice l of the next eight tiles.
@@ -442,7 +456,7 @@ __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV, NT>::CTAS)
       }
       __syncwarp();
       if (lane < rows) {
-        const int x = n0 + lane, i = x / p.G, hq = u.h * p.G + (x - i * p.G);
+        const int x = n0 + lane, i = ca_token(p, x), hq = u.h * p.G + (x - i * p.G);
         bulk_load(smem + C::RAW_OFF + qb * C::RAW + lane * DQK * 2,
                   static_cast<const uint16_t*>(p.q) + p.q_ss * (u.q0 + i) + p.q_sh * hq, DQK * 2, &q_full[qb]);
       }
@@ -472,7 +486,7 @@ __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV, NT>::CTAS)
             }
             const int key0 = (t8 + i) * kCaKeys;
             uint8_t* dst = smem + st * C::STAGE;
-            const int b0 = max(u.lo - key0, 0) / box, b1 = min((u.hi - key0 + box - 1) / box, boxes);
+            const int b0 = max(u.lo - key0, 0) >> box_lg, b1 = min((u.hi - key0 + box - 1) >> box_lg, boxes);
             if (lane == 0) mbar_expect_tx(&full[st], (uint32_t)(b1 - b0) * box * C::ROWB * (C::KP + C::VP));
             for (int x = b0; x < b1; ++x) {
               const int use = __shfl_sync(0xffffffffu, pg, i * 4 + x * per_box);
@@ -580,7 +594,7 @@ __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV, NT>::CTAS)
       for (int e = 0; e < E; e += 2) to[e / 2] = pack2<__half>(v[e] * up, v[e + 1] * up);
       if (lane == 0) {
         int2 lim = make_int2(0, 0);
-        if (n0 + r < rows) ca_row_keys(p, u.n, u.m, (n0 + r) / p.G, lim.x, lim.y);
+        if (n0 + r < rows) ca_row_keys(p, u.n, u.m, ca_token(p, n0 + r), lim.x, lim.y);
         row_lim[r] = lim;
         row_fac[r] = down * (p.softcap > 0.f ? p.scale / p.softcap : p.scale * 1.4426950408889634f);
       }
@@ -739,7 +753,7 @@ __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV, NT>::CTAS)
         p0[nt] = transpose8x8(pack2<__half>(w[0], w[1]));
         p1[nt] = transpose8x8(pack2<__half>(w[2], w[3]));
       }
-      uint32_t nan_seen = 0;
+      bool nan_seen = false;  // the same for all lanes
 #pragma unroll
       for (int j = 0; j < C::VP; ++j) {
         uint32_t v[4][4];
@@ -757,18 +771,29 @@ __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV, NT>::CTAS)
             v[r][2] = a.z;
             v[r][3] = a.w;
           }
-          if constexpr (MASK) {
-            // Rows that no query row sees count as 0 (stale codes may be NaN);
-            // a NaN that some row sees is put in below, for that row alone.
-            const int k = tile * kCaKeys + rows4[r];
-            const bool in = k >= lo && k < hi;
+        }
+        if constexpr (MASK) {
+          // A row's probability is 0 for a key that it does not see, which keeps out
+          // any code but NaN. NaN codes (stale ones may be) become 0 here; one
+          // that some row sees is put in below, for that row alone.
+          uint32_t nan = 0;
 #pragma unroll
-            for (int e = 0; e < VW; ++e) {
-              const uint32_t z = in ? v[r][e] : 0u;
-              const uint32_t nan = ((z & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-              nan_seen |= nan;
-              v[r][e] = z & ~((nan >> 7) * 0xffu);
+          for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int e = 0; e < VW; ++e) nan |= (v[r][e] & 0x7f7f7f7fu) + 0x01010101u;
+          if (__any_sync(0xffffffffu, nan & 0x80808080u)) {
+            uint32_t seen = 0;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const int k = tile * kCaKeys + rows4[r];
+#pragma unroll
+              for (int e = 0; e < VW; ++e) {
+                const uint32_t x = ((v[r][e] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+                if (k >= lo && k < hi) seen |= x;
+                v[r][e] &= ~((x >> 7) * 0xffu);
+              }
             }
+            nan_seen |= __any_sync(0xffffffffu, seen) != 0;
           }
         }
 #pragma unroll
@@ -788,7 +813,7 @@ __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV, NT>::CTAS)
         }
       }
       if constexpr (MASK) {
-        if (__any_sync(0xffffffffu, nan_seen != 0)) {
+        if (nan_seen) {
 #pragma unroll 1
           for (int r = 0; r < 16; ++r) {
             const int row = warp * 16 + r, k = tile * kCaKeys + row;
@@ -867,7 +892,7 @@ __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV, NT>::CTAS)
     const int live = min(C::R, rows - n0);
     const int64_t slot = (int64_t)blockIdx.x * 2 + u.slot;
     for (int x = tid; x < live * (DV / 4); x += kCaConsumers) {
-      const int r = x / (DV / 4), d = (x - r * (DV / 4)) * 4, z = n0 + r, i = z / p.G;
+      const int r = x / (DV / 4), d = (x - r * (DV / 4)) * 4, z = n0 + r, i = ca_token(p, z);
       float4 a = *reinterpret_cast<const float4*>(ob + r * C::OPITCH + d);
 #pragma unroll
       for (int w = 1; w < kCaWarps; ++w) {
@@ -887,7 +912,7 @@ __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV, NT>::CTAS)
       }
     }
     if (tid < live) {
-      const int z = n0 + tid, i = z / p.G;
+      const int z = n0 + tid, i = ca_token(p, z);
       if (u.whole)
         p.lse[(int64_t)(u.h * p.G + z - i * p.G) * p.s.T + u.q0 + i] = fin_l[tid] * 0.69314718055994531f;
       else
@@ -916,7 +941,7 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
   let_next_kernel_start();
   auto zero_rows = [&](const Seq& q, int h, int n0, int count) {  // `count` rows of head h from row n0 of the tile order
     for (int x = tid; x < count * (DV / 8); x += kJoinThreads) {
-      const int r = x / (DV / 8), y = n0 + r, i = y / p.G, hq = h * p.G + y - i * p.G;
+      const int r = x / (DV / 8), y = n0 + r, i = ca_token(p, y), hq = h * p.G + y - i * p.G;
       *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + p.o_ss * (q.q0 + i) + p.o_sh * hq +
                                 (x - r * (DV / 8)) * 8) = make_uint4(0, 0, 0, 0);
       if (x == r * (DV / 8)) p.lse[(int64_t)hq * p.s.T + q.q0 + i] = -CUDART_INF_F;
@@ -1047,7 +1072,7 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
         acc.w = fmaf(a.w, f, acc.w);
       }
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
-      const int y = n0 + r, i = y / p.G;
+      const int y = n0 + r, i = ca_token(p, y);
       acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
       const uint2 w = p.f16 ? make_uint2(pack2<__half>(acc.x, acc.y), pack2<__half>(acc.z, acc.w))
                             : make_uint2(pack2<__nv_bfloat16>(acc.x, acc.y), pack2<__nv_bfloat16>(acc.z, acc.w));

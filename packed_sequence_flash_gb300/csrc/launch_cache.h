@@ -94,6 +94,8 @@ struct CacheAttnParams {
   int64_t o_ss, o_sh;
   float* lse;  // [Hq][T]
   int Hq, G;
+  uint32_t g_mul;  // x / G = (mulhi(x, g_mul) + x) >> g_shift
+  int g_shift;
   float scale, softcap;
   int causal, window;  // window > 0: left window counting the current token
   int accumulate;      // add each key's probabilities to c.weight
