@@ -12,9 +12,11 @@
 // codes are expanded in place, so that instruction is the fitting one.
 // Measured (bf16, head dim 128, 32 query and 8 KV heads; GB300): 64 sequences of
 // 16 to 32 Ki tokens 480 us for 3.27 GB, the rate of a plain copy; 32 of 64 to
-// 8192 tokens 58.6 us for 307 MB (floor 45.2: 5 us until the first tile, 4 us of
-// join and some 4 us in which the CTAs end); one of 32 Ki tokens 21.8 us (floor
-// 9.9); one of 777 tokens with 16 / 4 heads 10 us, all latency. Out of L2 a tile of
+// 8192 tokens 59.4 us for 307 MB (floor 45.2: 5 us until the first tile, 4 us of
+// join and some 4 us in which the CTAs end); one of 32 Ki tokens 22 us (floor
+// 9.9); one of 777 tokens with 16 / 4 heads 10 us, all latency; 1024 of 10 to 200
+// tokens 102 us (floor 35: every unit runs through all of the code once, and
+// fetching it is what limits there). Out of L2 a tile of
 // 64 keys takes an SM 515 cycles for 8 rows and 790 for 16 (the expansion, two
 // cycles of the integer pipe for two codes, is most of it); from memory 690.
 //
