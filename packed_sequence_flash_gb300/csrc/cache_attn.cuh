@@ -85,7 +85,7 @@ struct CaCfg {
   static constexpr int FIXED = kCaUnits * RAW + OBYTES + 1024;
   // As many stages as fit beside 2 KB of static and 1 KB of reserved shared
   // memory: 64 KB or more of the cache in flight per SM.
-  static constexpr int FIT = (233472 / CTAS - 3072 - FIXED) / STAGE;
+  static constexpr int FIT = (233472 / CTAS - 3 * 1024 - FIXED) / STAGE;
   static constexpr int STAGES = FIT > 8 ? 8 : FIT;
   static constexpr int RAW_OFF = STAGES * STAGE;
   static constexpr int O_OFF = RAW_OFF + kCaUnits * RAW;
