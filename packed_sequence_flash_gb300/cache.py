@@ -20,6 +20,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 
 import torch
 
@@ -96,12 +97,19 @@ class KVCache:
     [num_pages, Hkv] fp32: a code c stands for c * scale. weight [num_pages, Hkv,
     page_size] fp32 or None: the attention weight each token has received, kept
     by ``attn_cache_fwd(accumulate=True)`` and used by ``kv_cache_evict``.
+
+    Each of the five may be replaced (``cache.weight = w``) by a tensor that the
+    constructor would have taken beside the others; the sizes are read-only.
     """
 
-    __slots__ = ("k", "v", "k_scale", "v_scale", "weight", "num_pages", "Hkv", "page_size", "Dqk", "Dv", "device",
-                 "_struct", "_ref")
+    __slots__ = ("_k", "_v", "_k_scale", "_v_scale", "_weight", "_num_pages", "_Hkv", "_page_size", "_Dqk", "_Dv",
+                 "_device", "_struct", "_ref", "_addresses", "_held")
 
     def __init__(self, k, v, k_scale, v_scale, weight=None):
+        self._take(k, v, k_scale, v_scale, weight)
+
+    def _take(self, k, v, k_scale, v_scale, weight):
+        """Checks the five tensors and makes them, and the struct that the calls get, the cache's."""
         device = k.get_device()
         if device < 0:
             _wrong_device(k, "cache k")
@@ -122,15 +130,42 @@ class KVCache:
             if weight.shape != (num_pages, Hkv, page_size):
                 raise ValueError(f"weight must be {[num_pages, Hkv, page_size]}, got {list(weight.shape)}")
             wp = weight.data_ptr()
-        self.k, self.v, self.k_scale, self.v_scale, self.weight = k, v, k_scale, v_scale, weight
-        self.num_pages, self.Hkv, self.page_size, self.Dqk, self.Dv = num_pages, Hkv, page_size, Dqk, Dv
-        self.device = device
-        c = self._struct = _lib.KVCacheStruct(kp, vp, k_scale.data_ptr(), v_scale.data_ptr(), wp, num_pages, page_size,
-                                              Hkv, Dqk, Dv)
+        ksp, vsp = k_scale.data_ptr(), v_scale.data_ptr()
+        c = _lib.KVCacheStruct(kp, vp, ksp, vsp, wp, num_pages, page_size, Hkv, Dqk, Dv)
         if not (k.is_contiguous() and v.is_contiguous()):
             c.k_strides[:] = k.stride()[:3]
             c.v_strides[:] = v.stride()[:3]
-        self._ref = ctypes.byref(c)
+        self._k, self._v, self._k_scale, self._v_scale, self._weight = k, v, k_scale, v_scale, weight
+        self._num_pages, self._Hkv, self._page_size, self._Dqk, self._Dv = num_pages, Hkv, page_size, Dqk, Dv
+        self._device = device
+        self._struct, self._ref = c, ctypes.byref(c)
+        self._addresses = (kp, vp, ksp, vsp, wp)
+        # While these storages live, other memory cannot come to have their addresses.
+        self._held = [t.untyped_storage() for t in (k, v, k_scale, v_scale, weight) if t is not None]
+
+    def _call_ref(self):
+        """The struct for a call. A tensor whose memory was exchanged (t.data = u, t.set_(u)) is checked and taken anew."""
+        w = self._weight
+        if self._addresses != (self._k.data_ptr(), self._v.data_ptr(), self._k_scale.data_ptr(),
+                               self._v_scale.data_ptr(), None if w is None else w.data_ptr()):
+            self._take(self._k, self._v, self._k_scale, self._v_scale, w)
+        return self._ref
+
+
+def _replaceable(name):
+    slot = "_" + name
+    tensors = ("k", "v", "k_scale", "v_scale", "weight")
+
+    def replace(cache, t):
+        cache._take(*(t if n == name else getattr(cache, "_" + n) for n in tensors))
+
+    return property(operator.attrgetter(slot), replace)
+
+
+for _name in ("k", "v", "k_scale", "v_scale", "weight"):
+    setattr(KVCache, _name, _replaceable(_name))
+for _name in ("num_pages", "Hkv", "page_size", "Dqk", "Dv", "device"):
+    setattr(KVCache, _name, property(operator.attrgetter("_" + _name)))
 
 
 def kv_cache(num_pages, Hkv, Dqk, Dv, page_size=64, weights=False, device="cuda") -> KVCache:
@@ -144,7 +179,7 @@ def kv_cache(num_pages, Hkv, Dqk, Dv, page_size=64, weights=False, device="cuda"
 
 def _sequences(cache, page_table, seq_lens, cu=None, name=""):
     """(B, max_pages) of a call's sequences."""
-    device = cache.device
+    device = cache._device
     _tensor(page_table, "page_table", torch.int32, device)
     _tensor(seq_lens, "seq_lens", torch.int32, device)
     shape = page_table.shape
@@ -175,15 +210,15 @@ def kv_cache_append(cache, k, v, page_table, seq_lens, cu_new=None) -> None:
     Sequence b's new tokens are rows [cu_new[b], cu_new[b + 1]) (T / B each without cu_new) and go to its last
     positions: seq_lens (int32 [B], on the device) counts them already. See psf_kv_cache_append for the scales.
     """
-    dtype = _dtype16(k, "k")
-    kp, vp = _view(k, "k", dtype, cache.device), _view(v, "v", dtype, cache.device)
-    _rows3(k, "k", cache.Hkv, cache.Dqk)
-    _rows3(v, "v", cache.Hkv, cache.Dv)
+    ref, dtype = cache._call_ref(), _dtype16(k, "k")
+    kp, vp = _view(k, "k", dtype, cache._device), _view(v, "v", dtype, cache._device)
+    _rows3(k, "k", cache._Hkv, cache._Dqk)
+    _rows3(v, "v", cache._Hkv, cache._Dv)
     T = k.size(0)
     if v.size(0) != T:
         raise ValueError("k and v must have the same number of rows")
     B, max_pages = _sequences(cache, page_table, seq_lens, cu_new, "cu_new")
-    _launch(cache.device, _call("psf_kv_cache_append"), cache._ref, kp, vp, _thd_strides(k, v), _DTYPES[dtype],
+    _launch(cache._device, _call("psf_kv_cache_append"), ref, kp, vp, _thd_strides(k, v), _DTYPES[dtype],
             _ptr(cu_new), page_table.data_ptr(), seq_lens.data_ptr(), B, max_pages, T)
 
 
@@ -193,7 +228,7 @@ def _attn_workspace(*sizes) -> int:
 
 
 def attn_cache_workspace_size(cache, B, max_pages, Hq, max_q=1, accumulate=False) -> int:
-    return _attn_workspace(B, max_pages, cache.page_size, Hq, cache.Hkv, cache.Dqk, cache.Dv, max_q,
+    return _attn_workspace(B, max_pages, cache._page_size, Hq, cache._Hkv, cache._Dqk, cache._Dv, max_q,
                            PSF_CACHE_ACCUMULATE if accumulate else 0)
 
 
@@ -207,10 +242,10 @@ def attn_cache_fwd(q, cache, page_table, seq_lens, scale, cu_q=None, max_q=None,
     accumulate: add every token's attention weight, over the rows and the heads of its KV head, to cache.weight.
     Long prompt chunks run faster through ``kv_cache_gather`` and ``attn_varlen_fwd``.
     """
-    dtype, device = _dtype16(q, "q"), cache.device
+    ref, dtype, device = cache._call_ref(), _dtype16(q, "q"), cache._device
     qp = _view(q, "q", dtype, device)
-    if q.dim() != 3 or q.size(2) != cache.Dqk:
-        raise ValueError(f"q must be [T, Hq, {cache.Dqk}], got {list(q.shape)}")
+    if q.dim() != 3 or q.size(2) != cache._Dqk:
+        raise ValueError(f"q must be [T, Hq, {cache._Dqk}], got {list(q.shape)}")
     T, Hq, _ = q.shape
     B, max_pages = _sequences(cache, page_table, seq_lens, cu_q, "cu_q")
     if max_q is None:
@@ -219,11 +254,11 @@ def attn_cache_fwd(q, cache, page_table, seq_lens, scale, cu_q=None, max_q=None,
         max_q = T // B if B else 0
     max_q = int(max_q)
     if out is None:
-        out = torch.empty((T, Hq, cache.Dv), dtype=dtype, device=q.device)
+        out = torch.empty((T, Hq, cache._Dv), dtype=dtype, device=q.device)
         op = out.data_ptr()
     else:
         op = _view(out, "out", dtype, device)
-        _rows3(out, "out", Hq, cache.Dv)
+        _rows3(out, "out", Hq, cache._Dv)
         if out.size(0) != T:
             raise ValueError("out must have q's rows")
     if lse is None:
@@ -238,7 +273,7 @@ def attn_cache_fwd(q, cache, page_table, seq_lens, scale, cu_q=None, max_q=None,
     else:
         _tensor(workspace, "workspace", workspace.dtype, device)
         size = workspace.numel() * workspace.element_size()
-    _launch(device, _call("psf_attn_cache_fwd"), qp, cache._ref, op, lse.data_ptr(), _ptr(cu_q),
+    _launch(device, _call("psf_attn_cache_fwd"), qp, ref, op, lse.data_ptr(), _ptr(cu_q),
             page_table.data_ptr(), seq_lens.data_ptr(), B, max_pages, T, max_q, Hq, _thd_strides(q, out),
             _DTYPES[dtype], float(scale), 1 if causal else 0, _window(window), _cap(softcap),
             PSF_CACHE_ACCUMULATE if accumulate else 0, workspace.data_ptr(), size)
@@ -251,7 +286,7 @@ def _evict_workspace(*sizes) -> int:
 
 
 def kv_cache_evict_workspace_size(cache, B, max_pages, budget) -> int:
-    return _evict_workspace(B, max_pages, cache.page_size, cache.Hkv, budget)
+    return _evict_workspace(B, max_pages, cache._page_size, cache._Hkv, budget)
 
 
 def kv_cache_evict(cache, page_table, seq_lens, budget, recent, new_lens=None, workspace=None):
@@ -261,21 +296,22 @@ def kv_cache_evict(cache, page_table, seq_lens, budget, recent, new_lens=None, w
     accumulated weight (of equal ones the earliest), in their order. Pages past ceil(budget / page_size) are free
     afterwards. See psf_kv_cache_evict for the scales.
     """
+    ref = cache._call_ref()
     B, max_pages = _sequences(cache, page_table, seq_lens)
     budget, recent = int(budget), int(recent)
     if new_lens is None:
         new_lens = torch.empty_like(seq_lens)
     else:
-        _tensor(new_lens, "new_lens", torch.int32, cache.device)
+        _tensor(new_lens, "new_lens", torch.int32, cache._device)
         if new_lens.shape != (B,):
             raise ValueError("new_lens must be [B]")
     if workspace is None:
         size = kv_cache_evict_workspace_size(cache, B, max_pages, budget)
         workspace = torch.empty(size, dtype=torch.uint8, device=seq_lens.device)
     else:
-        _tensor(workspace, "workspace", workspace.dtype, cache.device)
+        _tensor(workspace, "workspace", workspace.dtype, cache._device)
         size = workspace.numel() * workspace.element_size()
-    _launch(cache.device, _call("psf_kv_cache_evict"), cache._ref, page_table.data_ptr(), seq_lens.data_ptr(),
+    _launch(cache._device, _call("psf_kv_cache_evict"), ref, page_table.data_ptr(), seq_lens.data_ptr(),
             new_lens.data_ptr(), B, max_pages, budget, recent, workspace.data_ptr(), size)
     return new_lens
 
@@ -291,11 +327,12 @@ def kv_cache_gather(cache, page_table, seq_lens, total_k, dtype=torch.bfloat16):
     total_k = int(total_k)
     if total_k < 0:
         raise ValueError("total_k must not be negative")
+    ref = cache._call_ref()
     B, max_pages = _sequences(cache, page_table, seq_lens)
     dev = seq_lens.device
-    k = torch.empty((total_k, cache.Hkv, cache.Dqk), dtype=dtype, device=dev)
-    v = torch.empty((total_k, cache.Hkv, cache.Dv), dtype=dtype, device=dev)
+    k = torch.empty((total_k, cache._Hkv, cache._Dqk), dtype=dtype, device=dev)
+    v = torch.empty((total_k, cache._Hkv, cache._Dv), dtype=dtype, device=dev)
     cu_k = torch.empty(B + 1, dtype=torch.int32, device=dev)
-    _launch(cache.device, _call("psf_kv_cache_gather"), cache._ref, page_table.data_ptr(), seq_lens.data_ptr(), B,
+    _launch(cache._device, _call("psf_kv_cache_gather"), ref, page_table.data_ptr(), seq_lens.data_ptr(), B,
             max_pages, k.data_ptr(), v.data_ptr(), cu_k.data_ptr(), total_k, _DTYPES[dtype])
     return k, v, cu_k
