@@ -133,6 +133,10 @@ class KVCache:
         ksp, vsp = k_scale.data_ptr(), v_scale.data_ptr()
         c = _lib.KVCacheStruct(kp, vp, ksp, vsp, wp, num_pages, page_size, Hkv, Dqk, Dv)
         if not (k.is_contiguous() and v.is_contiguous()):
+            # (All strides 0 mean contiguous ones to the library.)
+            for t, name in ((k, "cache k"), (v, "cache v")):
+                if any(n > 1 and step == 0 for n, step in zip(t.shape[:3], t.stride())):
+                    raise ValueError(f"{name}: an expanded tensor overlaps itself")
             c.k_strides[:] = k.stride()[:3]
             c.v_strides[:] = v.stride()[:3]
         self._k, self._v, self._k_scale, self._v_scale, self._weight = k, v, k_scale, v_scale, weight

@@ -160,3 +160,26 @@ def test_a_copy_of_a_cache_does_not_follow_its_replacements(calls):
     assert calls.addresses()["weight"] == p["weight"].data_ptr()
     next(every_call(other))()
     assert calls.addresses()["weight"] == other.weight.data_ptr()
+
+
+@pytest.mark.parametrize("name", ["k", "v"])
+@pytest.mark.parametrize("shape", [(1, 1, 1), (1, 2, 16), (6, 1, 16), (6, 2, 1)])
+def test_expanded_codes_are_refused(name, shape):
+    """All strides 0 would be taken for contiguous ones: a cache of 6 pages over the memory of one row."""
+    p = parts()
+    p[name] = OnDevice(e4m3(*shape, 64).expand(6, 2, 16, 64))
+    with pytest.raises(ValueError, match="overlaps"):
+        psf.KVCache(**p)
+    whole = parts()
+    cache = psf.KVCache(**whole)
+    with pytest.raises(ValueError, match="overlaps"):
+        setattr(cache, name, p[name])
+    assert getattr(cache, name) is whole[name]
+
+
+def test_strides_of_dims_of_one_do_not_matter():
+    one = OnDevice(e4m3(1, 1, 16, 64).as_strided((1, 1, 16, 64), (0, 0, 64, 1)))
+    s = OnDevice(torch.zeros(1, 1))
+    psf.KVCache(one, one, s, s)
+    wide = OnDevice(e4m3(1, 1, 16, 128)[..., :64].as_strided((1, 1, 16, 64), (0, 0, 128, 1)))
+    assert list(psf.KVCache(wide, one, s, s)._struct.k_strides) == [0, 0, 128]
