@@ -419,7 +419,8 @@ int psf_grad_add_live_rows(void* dst, const void* src, const int32_t* cu_q, cons
  *  Sequences: page_table int32 [B, max_pages] (contiguous) lists the pages of
  *  each sequence in order, seq_lens int32 [B] its tokens: token j of sequence b
  *  is row j % page_size of page page_table[b][j / page_size]. Entries past
- *  ceil(seq_lens[b] / page_size) are not read. Several sequences may name the
+ *  ceil(seq_lens[b] / page_size) are not read. max_pages * page_size is at most
+ *  2^31 - 2^16. Several sequences may name the
  *  same page (a shared prefix) as long as no call writes to it. All of it is
  *  read on the device: nothing synchronises, and the calls can be captured.
  *  A length outside [0, max_pages * page_size], prefix sums that do not begin at 0

@@ -655,11 +655,15 @@ int cache_view(const psf_kv_cache* cache, CacheView* v) {
   return PSF_OK;
 }
 
+constexpr int64_t kMaxCacheTokens = (int64_t(1) << 31) - (1 << 16);
+
 int seq_view(const int32_t* page_table, const int32_t* seq_lens, const int32_t* cu, int B, int max_pages,
              int page_size, int T, SeqView* s) {
   if (B < 1 || B > 65534 || max_pages < 1 || T < 0)
     return fail(PSF_EINVAL, "need 1 <= B <= 65534, max_pages >= 1 and T >= 0 (got B=%d max_pages=%d T=%d)", B, max_pages, T);
-  if ((int64_t)max_pages * page_size > 0x7fffffff) return fail(PSF_EINVAL, "max_pages * page_size exceeds 2^31 - 1");
+  // The kernels count keys in 32 bits and step past a length by up to a block's share of them (8 Ki).
+  if ((int64_t)max_pages * page_size > kMaxCacheTokens)
+    return fail(PSF_EINVAL, "max_pages * page_size exceeds 2^31 - 2^16");
   if (!page_table || !seq_lens) return fail(PSF_EINVAL, "null page_table or seq_lens");
   if (!cu && T % B != 0) return fail(PSF_EINVAL, "without prefix sums B=%d must divide T=%d", B, T);
   s->table = page_table;

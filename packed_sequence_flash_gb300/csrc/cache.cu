@@ -61,7 +61,7 @@ __global__ void __launch_bounds__(kAppendThreads, 8)
   const int vecs = D >> 3;  // 8-element vectors of a row
   const T* in = is_v ? vin : kin;
   const int64_t ss = is_v ? v_ss : k_ss;
-  in += (is_v ? v_sh : k_sh) * h + ss * (q.q0 + base + r0 - first);
+  in += (is_v ? v_sh : k_sh) * h + ss * (base + r0 - first + q.q0);
   uint8_t* out = is_v ? c.v + c.v_sp * pg + c.v_sh * h : c.k + c.k_sp * pg + c.k_sh * h;
   const int64_t sr = is_v ? c.v_sr : c.k_sr;
   float* scale_at = (is_v ? c.v_scale : c.k_scale) + (int64_t)pg * c.Hkv + h;

@@ -1,0 +1,21 @@
+"""Sizes at the ends of the 8-bit cache's ranges, on the CPU (stand-in addresses, never dereferenced)."""
+import pytest
+
+from test_cache_cpu import EINVAL, EWORKSPACE, append, attend, evict, gather, lib  # noqa: F401 (a fixture)
+
+
+@pytest.mark.parametrize("call", [attend, append, evict, gather])
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+@pytest.mark.parametrize("tokens", [2 ** 31 - 128, 2 ** 31 - 4096, 2 ** 31 - 2 ** 16 + 128])
+def test_tables_past_what_32_bit_counts_hold(lib, call, page, tokens):  # noqa: F811
+    """Lengths that the kernels' rounding up and striding would carry past 2^31 - 1."""
+    assert call(lib, page_size=page, max_pages=tokens // page) == EINVAL
+    assert b"2^31" in lib.psf_last_error(), lib.psf_last_error()
+
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+def test_the_longest_table(lib, page):  # noqa: F811
+    pages = (2 ** 31 - 2 ** 16) // page
+    assert attend(lib, page_size=page, max_pages=pages) == EWORKSPACE
+    assert evict(lib, page_size=page, max_pages=pages) == EWORKSPACE
+    assert append(lib, page_size=page, max_pages=pages, T=0) == 0
