@@ -942,11 +942,13 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
   const int tid = threadIdx.x;
   let_next_kernel_start();
   auto zero_rows = [&](const Seq& q, int h, int n0, int count) {  // `count` rows of head h from row n0 of the tile order
-    for (int x = tid; x < count * (DV / 8); x += kJoinThreads) {
-      const int r = x / (DV / 8), y = n0 + r, i = ca_token(p, y), hq = h * p.G + y - i * p.G;
-      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + p.o_ss * (q.q0 + i) + p.o_sh * hq +
-                                (x - r * (DV / 8)) * 8) = make_uint4(0, 0, 0, 0);
-      if (x == r * (DV / 8)) p.lse[(int64_t)hq * p.s.T + q.q0 + i] = -CUDART_INF_F;
+    // (Vectors in 64 bits: 2^27 rows of head dim 128 have 2^31.)
+    for (int64_t x = tid; x < (int64_t)count * (DV / 8); x += kJoinThreads) {
+      const int r = (int)(x / (DV / 8)), col = (int)(x % (DV / 8)), y = n0 + r, i = ca_token(p, y);
+      const int hq = h * p.G + y - i * p.G;
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + p.o_ss * (q.q0 + i) + p.o_sh * hq + col * 8) =
+          make_uint4(0, 0, 0, 0);
+      if (col == 0) p.lse[(int64_t)hq * p.s.T + q.q0 + i] = -CUDART_INF_F;
     }
   };
   // Until the attention kernel is done: which unit this CTA joins, and where its

@@ -42,3 +42,26 @@ def test_weights_cleared_by_new_tensors(how):
     assert psf.kv_cache_evict(cache, t, i32(lens), 60, 8).tolist() == ref.evict(c, rows, lens, 60, 8)
     same(cache, c)
     assert torch.equal(old, kept) and psf.device_status() == 0
+
+
+def test_a_sequence_without_keys_and_very_many_rows():
+    """2^27 rows of head dim 128, 2^31 vectors of 16 bytes, all zero; the row of a sequence behind them is right."""
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("needs 60 GB")
+    rows, D = 2 ** 27, 128
+    cache = random_cache(4, 1, D, D, 16)
+    lens, table = [0, 20], [[-1, -1], [2, 1]]
+    # query rows that overlap (8 elements apart): the rows without keys are not read
+    q = torch.randn(rows * 8 + D, dtype=torch.bfloat16, device="cuda").as_strided((rows + 1, 1, D), (8, D, 1))
+    out = torch.full((rows + 1, 1, D), 3.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((1, rows + 1), 3.0, device="cuda")
+    psf.attn_cache_fwd(q, cache, i32(table), i32(lens), 0.1, cu_q=i32([0, rows, rows + 1]), max_q=rows, out=out, lse=lse)
+    assert psf.device_status() == 0
+    for part in out[:rows].split(2 ** 24):
+        assert not part.view(torch.int64).any()
+    assert bool(lse[:, :rows].isneginf().all())
+    want = ref.attend(ref.from_cache(cache), q[rows:], table[1:], lens[1:], [0, 1], 0.1)
+    close(out[rows:], want[0], want[2], "out")
+    close(lse[:, rows:], want[1], want[3], "lse")
+    del q, out, lse, part
+    torch.cuda.empty_cache()
