@@ -1055,7 +1055,9 @@ int psf_attn_cache_fwd(const void* q, const psf_kv_cache* cache, void* out, floa
   while ((1 << p.g_shift) < p.G) ++p.g_shift;
   p.g_mul = (uint32_t)((((uint64_t)1 << 32) * ((1 << p.g_shift) - p.G)) / p.G + 1);
   p.scale = scale;
-  p.softcap = softcap;
+  // Past 2^100 and 2^-100 scale / softcap or softcap * log2(e) could leave fp32's range. A cap moved there is the same
+  // for logits up to 2^88, and caps all of them to (next to) 0.
+  p.softcap = softcap > 0.f ? fminf(fmaxf(softcap, 0x1p-100f), 0x1p100f) : 0.f;
   p.causal = causal ? 1 : 0;
   p.window = window_left > 0 && window_left < cap ? (int)window_left : 0;  // one as long as the table hides nothing
   p.accumulate = (flags & PSF_CACHE_ACCUMULATE) ? 1 : 0;

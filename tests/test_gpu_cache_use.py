@@ -65,3 +65,56 @@ def test_a_sequence_without_keys_and_very_many_rows():
     close(lse[:, rows:], want[1], want[3], "lse")
     del q, out, lse, part
     torch.cuda.empty_cache()
+
+
+def capped(c, q, row, n, scale, cap):
+    """lse, out and weights of one query row per sequence over its n keys, in 64 bits, and how far a kernel may be off:
+    as in cache_reference.attend, but with the cap's own roundings counted relative to the logit: tanh from its series
+    (below 1/4: six roundings and the next term) or, from there on, off by 2^-21.8 at most where it is 0.245 or more, so
+    20 u32 of the value, and four further products."""
+    G, D = q.shape
+    K, V = ref.rows_of(c, "k", row, n, 0), ref.rows_of(c, "v", row, n, 0)
+    x = q.cpu().double()
+    z0 = scale * (x @ K.T)
+    z = cap * torch.tanh(z0 / cap)
+    dz = ((D + 8) * (scale * (x.abs() @ K.abs().T)) + 24 * z.abs()) * ref.U32
+    l = torch.logsumexp(z, -1)
+    p = torch.exp(z - l[:, None])
+    rel = (2 * dz.amax(-1) + 2.0 ** -21 + 4 * ref.U32 * (z.abs().amax(-1) + l.abs()) + n * ref.U32)[:, None]
+    o, mass = p @ V, p @ V.abs()
+    out_tol = ((rel + 2.0 ** -11) * mass + 2.0 ** -32 * n * V.abs().max() + ref.U16[q.dtype] * o.abs()) * 1.01 + 2.0 ** -24
+    return l, rel[:, 0] + 4 * ref.U32 * l.abs(), o, out_tol, p.sum(0), (p * rel).sum(0) + G * ref.U32 + 8 * ref.U32 * p.sum(0)
+
+
+@pytest.mark.parametrize("dims", [(64, 64), (128, 128), (192, 128), (512, 512)])
+@pytest.mark.parametrize("G", [4, 12])
+@pytest.mark.parametrize("cap", [0.5, 4.0, 9.0, 30.0, 1e3, 1e4, 1e6, 1e8, 1e20, 3e38])
+def test_caps_near_and_far_above_the_logits(dims, G, cap):
+    """The cap's error is relative to the logit: a cap far above all of them is next to none."""
+    n = 300
+    rows, t, pages = tables([n], 32)
+    cache = random_cache(pages, 1, *dims, 32, seed=2, weights=True)
+    cache.weight.zero_()
+    q = (2 * torch.randn(1, G, dims[0], generator=torch.Generator().manual_seed(5))).half().cuda()
+    c = ref.from_cache(cache)
+    out, lse = psf.attn_cache_fwd(q, cache, t, i32([n]), 0.1, softcap=cap, accumulate=True)
+    assert psf.device_status() == 0
+    l, l_tol, o, o_tol, w, w_tol = capped(c, q[0], rows[0], n, 0.1, cap)
+    close(lse[:, 0], l, l_tol, "lse")
+    close(out[0], o, o_tol, "out")
+    j = torch.arange(n)
+    close(cache.weight[:, 0][torch.tensor(rows[0])[j // 32], j % 32], w, w_tol, "weight")
+
+
+@pytest.mark.parametrize("cap", [1e-45, 1e-38, 1e-30])
+def test_caps_that_leave_no_difference(cap):
+    lens = [64, 100]
+    rows, t, pages = tables(lens, 16)
+    cache = random_cache(pages, 1, 64, 64, 16)
+    q = torch.randn(2, 2, 64, generator=torch.Generator().manual_seed(5)).bfloat16().cuda()
+    q[0, 1] = 0.0
+    out, lse = psf.attn_cache_fwd(q, cache, t, i32(lens), 0.1, softcap=cap)
+    for b, n in enumerate(lens):
+        l, l_tol, o, o_tol, _, _ = capped(ref.from_cache(cache), q[b], rows[b], n, 0.1, cap)
+        close(lse[:, b], l, l_tol, "lse")
+        close(out[b], o, o_tol, "out")
