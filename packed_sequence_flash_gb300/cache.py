@@ -145,7 +145,8 @@ class KVCache:
         self._struct, self._ref = c, ctypes.byref(c)
         self._addresses = (kp, vp, ksp, vsp, wp)
         # While these storages live, other memory cannot come to have their addresses.
-        self._held = [t.untyped_storage() for t in (k, v, k_scale, v_scale, weight) if t is not None]
+        self._held = (k.untyped_storage(), v.untyped_storage(), k_scale.untyped_storage(), v_scale.untyped_storage(),
+                      None if weight is None else weight.untyped_storage())
 
     def _call_ref(self):
         """The struct for a call. A tensor whose memory was exchanged (t.data = u, t.set_(u)) is checked and taken anew."""
