@@ -78,6 +78,14 @@ def _dtype16(t, name):
     return t.dtype
 
 
+def _c_int(x, name) -> int:
+    """A number of a call; the library's are 32 bits, and ctypes would cut it to them."""
+    x = int(x)
+    if not -0x80000000 <= x <= 0x7fffffff:
+        raise ValueError(f"{name} must fit in 32 bits, got {x}")
+    return x
+
+
 def _launch(device, call, *args) -> None:
     """call(*args, stream) with `device` current (a call's tensors may be on another than the current one)."""
     if _current_device() == device:
@@ -190,6 +198,8 @@ def _sequences(cache, page_table, seq_lens, cu=None, name=""):
     shape = page_table.shape
     if len(shape) != 2 or seq_lens.shape != shape[:1]:
         raise ValueError("page_table must be [B, max_pages] and seq_lens [B]")
+    if shape[0] > 0x7fffffff or shape[1] > 0x7fffffff:
+        raise ValueError(f"page_table must be below 2^31 both ways, got {list(shape)}")
     if cu is not None:
         _tensor(cu, name, torch.int32, device)
         if cu.shape != (shape[0] + 1,):
@@ -219,7 +229,7 @@ def kv_cache_append(cache, k, v, page_table, seq_lens, cu_new=None) -> None:
     kp, vp = _view(k, "k", dtype, cache._device), _view(v, "v", dtype, cache._device)
     _rows3(k, "k", cache._Hkv, cache._Dqk)
     _rows3(v, "v", cache._Hkv, cache._Dv)
-    T = k.size(0)
+    T = _c_int(k.size(0), "the number of rows")
     if v.size(0) != T:
         raise ValueError("k and v must have the same number of rows")
     B, max_pages = _sequences(cache, page_table, seq_lens, cu_new, "cu_new")
@@ -229,6 +239,8 @@ def kv_cache_append(cache, k, v, page_table, seq_lens, cu_new=None) -> None:
 
 @functools.lru_cache(maxsize=256)
 def _attn_workspace(*sizes) -> int:
+    for x in sizes:
+        _c_int(x, "a size")
     return int(_call("psf_attn_cache_workspace_size")(*sizes))
 
 
@@ -252,12 +264,14 @@ def attn_cache_fwd(q, cache, page_table, seq_lens, scale, cu_q=None, max_q=None,
     if q.dim() != 3 or q.size(2) != cache._Dqk:
         raise ValueError(f"q must be [T, Hq, {cache._Dqk}], got {list(q.shape)}")
     T, Hq, _ = q.shape
+    if T * Hq > 0x7fffffff:
+        raise ValueError(f"q must have fewer than 2^31 rows and heads, got {list(q.shape)}")
     B, max_pages = _sequences(cache, page_table, seq_lens, cu_q, "cu_q")
     if max_q is None:
         if cu_q is not None:
             raise ValueError("cu_q needs max_q, the most query rows of a sequence")
         max_q = T // B if B else 0
-    max_q = int(max_q)
+    max_q = _c_int(max_q, "max_q")
     if out is None:
         out = torch.empty((T, Hq, cache._Dv), dtype=dtype, device=q.device)
         op = out.data_ptr()
@@ -280,13 +294,15 @@ def attn_cache_fwd(q, cache, page_table, seq_lens, scale, cu_q=None, max_q=None,
         size = workspace.numel() * workspace.element_size()
     _launch(device, _call("psf_attn_cache_fwd"), qp, ref, op, lse.data_ptr(), _ptr(cu_q),
             page_table.data_ptr(), seq_lens.data_ptr(), B, max_pages, T, max_q, Hq, _thd_strides(q, out),
-            _DTYPES[dtype], float(scale), 1 if causal else 0, _window(window), _cap(softcap),
+            _DTYPES[dtype], float(scale), 1 if causal else 0, _c_int(_window(window), "window"), _cap(softcap),
             PSF_CACHE_ACCUMULATE if accumulate else 0, workspace.data_ptr(), size)
     return out, lse
 
 
 @functools.lru_cache(maxsize=256)
 def _evict_workspace(*sizes) -> int:
+    for x in sizes:
+        _c_int(x, "a size")
     return int(_call("psf_kv_cache_evict_workspace_size")(*sizes))
 
 
@@ -303,7 +319,7 @@ def kv_cache_evict(cache, page_table, seq_lens, budget, recent, new_lens=None, w
     """
     ref = cache._call_ref()
     B, max_pages = _sequences(cache, page_table, seq_lens)
-    budget, recent = int(budget), int(recent)
+    budget, recent = _c_int(budget, "budget"), _c_int(recent, "recent")
     if new_lens is None:
         new_lens = torch.empty_like(seq_lens)
     else:
@@ -329,7 +345,7 @@ def kv_cache_gather(cache, page_table, seq_lens, total_k, dtype=torch.bfloat16):
     """
     if dtype not in _DTYPES:
         raise ValueError(f"dtype must be bfloat16 or float16, got {dtype}")
-    total_k = int(total_k)
+    total_k = _c_int(total_k, "total_k")
     if total_k < 0:
         raise ValueError("total_k must not be negative")
     ref = cache._call_ref()

@@ -183,3 +183,25 @@ def test_strides_of_dims_of_one_do_not_matter():
     psf.KVCache(one, one, s, s)
     wide = OnDevice(e4m3(1, 1, 16, 128)[..., :64].as_strided((1, 1, 16, 64), (0, 0, 128, 1)))
     assert list(psf.KVCache(wide, one, s, s)._struct.k_strides) == [0, 0, 128]
+
+
+@pytest.mark.parametrize("big", [2 ** 31, 2 ** 32 + 5, -2 ** 31 - 1])
+def test_numbers_past_32_bits_are_refused(calls, big):
+    """ctypes would cut them: a budget of 2^32 + 5 came out as 5."""
+    cache = psf.KVCache(**parts())
+    table, lens = i32([[0, 1], [2, 3]]), i32([20, 30])
+    q = OnDevice(torch.zeros(2, 4, 64, dtype=torch.bfloat16))
+    ws, new = OnDevice(torch.zeros(256, dtype=torch.uint8)), i32([0, 0])
+    attend = lambda **kw: psf.attn_cache_fwd(q, cache, table, lens, 0.1, workspace=ws, **kw)  # noqa: E731
+    for call in (lambda: psf.kv_cache_evict(cache, table, lens, big, 4, new, workspace=ws),
+                 lambda: psf.kv_cache_evict(cache, table, lens, 20, big, new, workspace=ws),
+                 lambda: attend(max_q=big), lambda: attend(window=big),
+                 lambda: psf.kv_cache_gather(cache, table, lens, big),
+                 lambda: psf.attn_cache_workspace_size(cache, 2, 2, 4, big),
+                 lambda: psf.kv_cache_evict_workspace_size(cache, 2, 2, big)):
+        with pytest.raises(ValueError, match="32 bits"):
+            call()
+    assert not calls.seen
+    attend(max_q=2 ** 31 - 1, window=2 ** 31 - 1)
+    psf.kv_cache_evict(cache, table, lens, 2 ** 31 - 1, 0, new, workspace=ws)
+    assert len(calls.seen) == 2
