@@ -504,7 +504,7 @@ int psf_attn_cache_fwd(const void* q, const psf_kv_cache* cache, void* out, floa
  *  After an eviction positions count kept tokens (so do windows).
  *  A sequence with a page that does not exist is left as it is, its new length
  *  its old one. Needs cache->weight, 1 <= budget, 0 <= recent <= budget. new_lens
- *  must not be seq_lens. A page belongs to one sequence.
+ *  must not overlap seq_lens. A page belongs to one sequence.
  *  workspace: psf_kv_cache_evict_workspace_size(...) bytes, 16-byte aligned.
  */
 size_t psf_kv_cache_evict_workspace_size(int B, int max_pages, int page_size, int Hkv, int budget);

@@ -1089,7 +1089,10 @@ int psf_kv_cache_evict(const psf_kv_cache* cache, const int32_t* page_table, con
   if (!c.weight) return fail(PSF_EINVAL, "eviction needs a cache with weights");
   if (budget < 1 || recent < 0 || recent > budget)
     return fail(PSF_EINVAL, "need budget >= 1 and 0 <= recent <= budget (got budget=%d recent=%d)", budget, recent);
-  if (!new_lens || new_lens == seq_lens) return fail(PSF_EINVAL, "new_lens must be given and not be seq_lens");
+  // (A head's selection reads its sequence's length whenever it runs.)
+  const uintptr_t from = reinterpret_cast<uintptr_t>(seq_lens), to = reinterpret_cast<uintptr_t>(new_lens);
+  if (!new_lens || (to > from ? to - from : from - to) < sizeof(int32_t) * (size_t)B)
+    return fail(PSF_EINVAL, "new_lens must be given and not overlap seq_lens");
   const size_t need = psf_kv_cache_evict_workspace_size(B, max_pages, c.page, c.Hkv, budget);
   if (!workspace || ws_bytes < need || !aligned16(workspace))
     return fail(PSF_EWORKSPACE, "eviction workspace needs %zu bytes, 16-byte aligned (got %zu)", need, ws_bytes);

@@ -1,7 +1,7 @@
 """Sizes at the ends of the 8-bit cache's ranges, on the CPU (stand-in addresses, never dereferenced)."""
 import pytest
 
-from test_cache_cpu import EINVAL, EWORKSPACE, append, attend, evict, gather, lib  # noqa: F401 (a fixture)
+from test_cache_cpu import A, EINVAL, EWORKSPACE, append, attend, evict, gather, lib  # noqa: F401 (a fixture)
 
 
 @pytest.mark.parametrize("call", [attend, append, evict, gather])
@@ -19,3 +19,15 @@ def test_the_longest_table(lib, page):  # noqa: F811
     assert attend(lib, page_size=page, max_pages=pages) == EWORKSPACE
     assert evict(lib, page_size=page, max_pages=pages) == EWORKSPACE
     assert append(lib, page_size=page, max_pages=pages, T=0) == 0
+
+
+@pytest.mark.parametrize("entries", [-3, -1, 0, 1, 3])
+def test_new_lengths_that_overlap_the_old_ones(lib, entries):  # noqa: F811
+    """Four sequences: new lengths written over others that a later selection still reads."""
+    assert evict(lib, lens=A, new=A + 4 * entries) == EINVAL
+    assert b"overlap" in lib.psf_last_error(), lib.psf_last_error()
+
+
+@pytest.mark.parametrize("entries", [-4, 4])
+def test_new_lengths_beside_the_old_ones(lib, entries):  # noqa: F811
+    assert evict(lib, lens=A, new=A + 4 * entries) == EWORKSPACE
