@@ -1002,7 +1002,20 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
   }
   after_previous_kernel();
   if (tail || !BY_UNIT) {  // rows past the last sequence
-    const int first = p.s.cu ? min(max(p.s.cu[p.s.B], 0), p.s.T) : p.s.T;
+    int first = p.s.cu ? min(max(p.s.cu[p.s.B], 0), p.s.T) : p.s.T;
+    if (first < p.s.T) {
+      // Prefix sums that fall can end in front of rows that a sequence has: those are its own.
+      __shared__ int ends;
+      if (tid == 0) ends = first;
+      __syncthreads();
+      for (int b = tid; b < p.s.B; b += kJoinThreads) {
+        const Seq x = seq_at(p.s, p.c.page, b);
+        if (x.m > 0) first = max(first, x.q0 + x.m);
+      }
+      atomicMax(&ends, first);
+      __syncthreads();
+      first = ends;
+    }
     const Seq rest = {0, p.s.T - first, first, false};
     if (rest.m > 0 && blockIdx.z == 0)
       for (int64_t x = blockIdx.x; x < (int64_t)rest.m * p.c.Hkv; x += gridDim.x)

@@ -1,5 +1,4 @@
 """GPU tests of the 8-bit cache: what a program may do with its tensors between calls, and less usual forms."""
-
 import pytest
 import torch
 
@@ -9,6 +8,7 @@ from test_gpu_cache import close, i32, random_cache, same, tables
 
 pytestmark = pytest.mark.gpu
 
+EDEVICE_ARGS = -4
 
 
 @pytest.fixture(autouse=True)
@@ -118,3 +118,57 @@ def test_caps_that_leave_no_difference(cap):
         l, l_tol, o, o_tol, _, _ = capped(ref.from_cache(cache), q[b], rows[b], n, 0.1, cap)
         close(lse[:, b], l, l_tol, "lse")
         close(out[b], o, o_tol, "out")
+
+
+# ---------------------------------------------------------------------------
+# wrong descriptions
+
+def state(cache):
+    return dict(k=cache.k.view(torch.uint8).clone(), v=cache.v.view(torch.uint8).clone(), k_scale=cache.k_scale.clone(),
+                v_scale=cache.v_scale.clone(), weight=cache.weight.clone())
+
+
+def unchanged(cache, before, pages):
+    for name, now in state(cache).items():
+        assert torch.equal(now[pages], before[name][pages]), name
+
+
+# prefix sums over 9 rows, the sequences whose rows they still describe, and whether an append finds all of those
+WRONG_SUMS = [([3, 5, 9], [0, 1], True), ([0, 5, 2], [0], True), ([0, 5, 400], [0], True), ([0, -1, 4], [], True),
+              ([-40, 2, 4], [1], True), ([1000, 1001, 1002], [], True), ([0, 2, 500, 4, 6], [0, 3], False),
+              ([0, 7, 7, 0, 5], [0, 1, 3], False), ([-2 ** 31, 2 ** 31 - 1, 3, 5], [2], False)]
+
+
+@pytest.mark.parametrize("cu,good,found", WRONG_SUMS)
+def test_wrong_prefix_sums_touch_nothing_else(cu, good, found):
+    lens = [40, 30, 25, 50][:len(cu) - 1]
+    rows, t, pages = tables(lens, 16, extra=16)
+    cache = random_cache(pages, 2, 64, 64, 16, weights=True)
+    q = torch.randn(9, 4, 64, generator=torch.Generator().manual_seed(1)).bfloat16().cuda()
+    out_buf = torch.full((9 + 80, 4, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse_buf = torch.full((4 * 9 + 160,), 7.0, device="cuda")
+    out, lse = out_buf[40:49], lse_buf[80:116].view(4, 9)
+    psf.attn_cache_fwd(q, cache, t, i32(lens), 0.1, cu_q=i32(cu), max_q=9, out=out, lse=lse)
+    assert psf.device_status() == EDEVICE_ARGS
+    claims = [sum(cu[b] <= r < cu[b + 1] for b in good) for r in range(9)]
+    for b in good:
+        want = ref.attend(ref.from_cache(cache), q[cu[b]:cu[b + 1]], rows[b:b + 1], lens[b:b + 1],
+                          [0, cu[b + 1] - cu[b]], 0.1)
+        alone = [r for r in range(cu[b], cu[b + 1]) if claims[r] == 1]
+        at = [r - cu[b] for r in alone]
+        close(out[alone], want[0][at], want[2][at], "out")
+        close(lse[:, alone], want[1][:, at], want[3][:, at], "lse")
+    out.fill_(7.0)
+    lse.fill_(7.0)
+    assert bool((out_buf == 7.0).all()) and bool((lse_buf == 7.0).all())
+
+    before, c = state(cache), ref.from_cache(cache)
+    x = torch.randn(9, 2, 64, generator=torch.Generator().manual_seed(2)).bfloat16().cuda()
+    psf.kv_cache_append(cache, x, x, t, i32(lens), cu_new=i32(cu))
+    assert psf.device_status() == EDEVICE_ARGS
+    mine = {pg for b in good for pg in rows[b]}
+    unchanged(cache, before, [pg for pg in range(pages) if pg not in mine])
+    if found:
+        for b in good:
+            ref.append(c, x, x, [rows[b]], lens[b:b + 1], cu[b:b + 2])
+        same(cache, c)
