@@ -427,7 +427,7 @@ int psf_grad_add_live_rows(void* dst, const void* src, const int32_t* cu_q, cons
  *  or whose rows lie outside the packed tensor, or a page outside [0, num_pages)
  *  is a PSF_EDEVICE_ARGS device status; nothing outside the tensors is touched, a
  *  page that does not exist is not written, and the results of the other
- *  sequences stand.
+ *  sequences stand (but see the append for its prefix sums).
  */
 typedef struct {
   void* k;
@@ -455,6 +455,8 @@ typedef struct {
  *  their contents. A page that is written belongs to one sequence. A sequence
  *  with more new rows than tokens takes none (a PSF_EDEVICE_ARGS status): idle
  *  entries of a batch have no rows in cu_new.
+ *  Pages are looked up by prefix sums, so where one falls below the entry in front
+ *  of it or passes T, new rows of any sequence may be left out.
  *  strides: NULL, or 6 element strides (batch, head, row) of k, v (batch ignored).
  */
 int psf_kv_cache_append(const psf_kv_cache* cache, const void* k, const void* v, const int64_t* strides, int dtype,
