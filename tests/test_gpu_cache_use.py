@@ -1,10 +1,12 @@
 """GPU tests of the 8-bit cache: what a program may do with its tensors between calls, and less usual forms."""
+import random
+
 import pytest
 import torch
 
 import cache_reference as ref
 import packed_sequence_flash_gb300 as psf
-from test_gpu_cache import close, i32, random_cache, same, tables
+from test_gpu_cache import check_append, check_attend, check_evict, close, i32, prefix, random_cache, same, tables
 
 pytestmark = pytest.mark.gpu
 
@@ -172,3 +174,69 @@ def test_wrong_prefix_sums_touch_nothing_else(cu, good, found):
         for b in good:
             ref.append(c, x, x, [rows[b]], lens[b:b + 1], cu[b:b + 2])
         same(cache, c)
+
+
+@pytest.mark.parametrize("how", ["one token", "prefix sums"])
+@pytest.mark.parametrize("fault", ["page too large", "page negative", "length past the table", "length negative"])
+def test_a_wrong_sequence_of_an_append_is_left_alone(how, fault):
+    lens = [100, 70, 33]
+    rows, t, pages = tables(lens, 32)
+    cache = random_cache(pages, 2, 128, 128, 32, weights=True)
+    n = i32(lens)
+    if fault.startswith("page"):
+        t[1, 69 // 32] = pages if fault == "page too large" else -1
+    else:
+        n[1] = t.shape[1] * 32 + 1 if fault == "length past the table" else -5
+    before, c = state(cache), ref.from_cache(cache)
+    x = torch.randn(3, 2, 128, generator=torch.Generator().manual_seed(2)).bfloat16().cuda()
+    psf.kv_cache_append(cache, x, x, t, n, None if how == "one token" else i32([0, 1, 2, 3]))
+    assert psf.device_status() == EDEVICE_ARGS
+    unchanged(cache, before, rows[1])
+    for b in (0, 2):
+        ref.append(c, x[b:b + 1], x[b:b + 1], [rows[b]], [lens[b]], [0, 1])
+    same(cache, c)
+
+
+# ---------------------------------------------------------------------------
+# less usual forms
+
+@pytest.mark.parametrize("dims", [(64, 64), (192, 128), (512, 512)])
+def test_a_strided_cache_through_every_call(dims):
+    """Rows of a page interleaved over the heads: one-token append, attention with weights, gather, eviction."""
+    lens = [50, 1, 17, 140]
+    rows, t, pages = tables(lens, 16)
+    cache = random_cache(pages, 3, *dims, 16, weights=True, layout="ph")
+    assert not cache.k.is_contiguous() and not cache.v.is_contiguous()
+    g = torch.Generator().manual_seed(3)
+    draw = lambda H, D: torch.randn(4, H, D, generator=g).bfloat16().cuda()  # noqa: E731
+    check_append(cache, draw(3, dims[0]) * 5, draw(3, dims[1]) * 5, rows, t, lens, [1] * 4, uniform=True)
+    check_attend(cache, draw(6, dims[0]), rows, t, lens, [1] * 4, dims[0] ** -0.5, accumulate=True, uniform=True)
+    k, v, cu = psf.kv_cache_gather(cache, t, i32(lens), sum(lens))
+    c = ref.from_cache(cache)
+    for b, n in enumerate(lens):
+        for h in range(3):
+            for name, x in (("k", k), ("v", v)):
+                assert torch.equal(x[cu[b]:cu[b + 1], h].cpu().double(), ref.rows_of(c, name, rows[b], n, h))
+    check_evict(cache, rows, t, lens, 37, 10)
+
+
+@pytest.mark.parametrize("dims,G,B", [((128, 128), 2, 480), ((128, 128), 12, 330), ((192, 128), 3, 330),
+                                      ((512, 512), 2, 170), ((64, 64), 11, 330)])
+@pytest.mark.parametrize("softcap", [None, 5.0])
+def test_more_units_than_shares_on_other_tiles(dims, G, B, softcap):
+    """Results joined by share, in tiles of 8 and of 16 rows and all widths; units that several shares have among them."""
+    r = random.Random(B)
+    lens = [r.choice([0, 1, 20, 40, r.randint(0, 40)]) for _ in range(B)]
+    lens[0], lens[B // 2], lens[-1] = 700, 2500, 900
+    m_rows = [r.choice([0, 1, 1, 2]) for _ in range(B)]
+    m_rows[0] = m_rows[B // 2] = m_rows[-1] = 2
+    rows, t, pages = tables(lens, 16, seed=B)
+    cache = random_cache(pages, 2, *dims, 16, seed=B)
+    cu = prefix(m_rows)
+    q = torch.randn(cu[-1] + 5, 2 * G, dims[0], generator=torch.Generator().manual_seed(B)).bfloat16().cuda()
+    out = torch.full((cu[-1] + 5, 2 * G, dims[1]), 3.0, dtype=torch.bfloat16, device="cuda")
+    got = psf.attn_cache_fwd(q, cache, t, i32(lens), 0.1, cu_q=i32(cu), max_q=2, softcap=softcap, out=out)
+    assert psf.device_status() == 0
+    want = ref.attend(ref.from_cache(cache), q, rows, lens, cu, 0.1, softcap=softcap)
+    close(got[0], want[0], want[2], "out")
+    close(got[1], want[1], want[3], "lse")
