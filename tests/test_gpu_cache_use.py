@@ -240,3 +240,68 @@ def test_more_units_than_shares_on_other_tiles(dims, G, B, softcap):
     want = ref.attend(ref.from_cache(cache), q, rows, lens, cu, 0.1, softcap=softcap)
     close(got[0], want[0], want[2], "out")
     close(got[1], want[1], want[3], "lse")
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_branches_that_meet_at_a_call(captured):
+    """Queries from one stream and new tokens from another, joined by events before the attention; what comes of it goes
+    to the first stream again while eviction and gather follow on the second."""
+    lens = [700, 40, 129]
+    rows, t, pages = tables(lens, 32, extra=8)
+    g = torch.Generator().manual_seed(4)
+    raw = torch.randn(3, 8, 128, generator=g).cuda()
+    x = torch.randn(3, 2, 128, generator=g).bfloat16().cuda()
+    n = i32([m + 1 for m in lens])
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+
+    def step(cache):
+        start = torch.cuda.current_stream()
+        a.wait_stream(start)
+        b.wait_stream(start)
+        with torch.cuda.stream(a):
+            q = raw
+            for _ in range(20):  # long enough for the append to be over first, or not
+                q = q * 1.0
+            q = q.bfloat16()
+        with torch.cuda.stream(b):
+            psf.kv_cache_append(cache, x, x, t, n)
+            b.wait_stream(a)
+            out, lse = psf.attn_cache_fwd(q, cache, t, n, 0.1, accumulate=True)
+            a.wait_stream(b)
+            new = psf.kv_cache_evict(cache, t, n, 100, 20)
+            k = psf.kv_cache_gather(cache, t, new, 300)[0]
+        with torch.cuda.stream(a):
+            copy = out.clone()
+            q.record_stream(b)
+            out.record_stream(a)
+        start.wait_stream(a)
+        start.wait_stream(b)
+        return out, lse, copy, new, k[:241]
+
+    cache = random_cache(pages, 2, 128, 128, 32, weights=True)
+    c = ref.from_cache(cache)
+    now = [m + 1 for m in lens]
+    ref.append(c, x, x, rows, now, [0, 1, 2, 3])
+    want = ref.attend(c, raw.bfloat16(), rows, now, [0, 1, 2, 3], 0.1, accumulate=True)
+    if captured:
+        step(random_cache(pages, 2, 128, 128, 32, weights=True))
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = step(cache)
+        graph.replay()
+    else:
+        got = step(cache)
+    torch.cuda.synchronize()
+    close(got[0], want[0], want[2], "out")
+    close(got[1], want[1], want[3], "lse")
+    assert torch.equal(got[2], got[0]) and got[3].tolist() == [100, 41, 100]
+    again = random_cache(pages, 2, 128, 128, 32, weights=True)
+    psf.kv_cache_append(again, x, x, t, n)
+    psf.attn_cache_fwd(raw.bfloat16(), again, t, n, 0.1, accumulate=True)
+    new = psf.kv_cache_evict(again, t, n, 100, 20)
+    k = psf.kv_cache_gather(again, t, new, 300)[0]
+    assert torch.equal(k[:241], got[4])
+    for name, value in state(again).items():
+        assert torch.equal(state(cache)[name], value), name
+    assert psf.device_status() == 0
