@@ -407,6 +407,7 @@ int attn_fwd_impl(const void* q, const void* k, const void* v, void* out, float*
   p.lse = lse;
   p.l_sb = vl.sb;
   p.l_sh = vl.sh;
+  p.Hq = Hq;
   p.Hkv = Hkv;
   p.pack = pack;
   p.dv_parts = Dv == 512 ? 2 : 1;
@@ -534,7 +535,8 @@ int attn_bwd_impl(const void* dout, const void* q, const void* k, const void* v,
     p.v_sb = vdv.sb;
     p.v_ss = vdv.ss;
     p.v_sh = vdv.sh;
-      p.Hkv = Hkv;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
     p.scale = scale;
     p.scale_log2 = scale * 1.4426950408889634f;
     p.softcap = softcap;
@@ -1048,6 +1050,7 @@ int psf_attn_cache_fwd(const void* q, const psf_kv_cache* cache, void* out, floa
   p.o_ss = vo.ss;
   p.o_sh = vo.sh;
   p.lse = lse;
+  p.Hq = Hq;
   p.G = Hq / p.c.Hkv;
   while ((1 << p.g_shift) < p.G) ++p.g_shift;
   p.g_mul = (uint32_t)((((uint64_t)1 << 32) * ((1 << p.g_shift) - p.G)) / p.G + 1);
