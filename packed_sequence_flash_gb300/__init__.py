@@ -18,7 +18,8 @@ from .cache import (KVCache, attn_cache_fwd, attn_cache_workspace_size, kv_cache
                     kv_cache_evict_workspace_size, kv_cache_gather)
 
 __all__ = [
-    "KVCache", "NO_WINDOW", "PSFError", "attn_cache_fwd", "attn_cache_workspace_size", "attn_dense_bwd", "attn_dense_fwd", "attn_varlen_bwd", "attn_varlen_fwd",
+    "KVCache", "NO_WINDOW", "PSFError", "attn_cache_fwd", "attn_cache_workspace_size", "attn_dense_bwd",
+    "attn_dense_fwd", "attn_varlen_bwd", "attn_varlen_fwd",
     "build_cross_segments", "build_doc_segments", "bwd_workspace_size", "check_device_status",
     "check_pipeline_wait", "chunk_attention", "chunk_attention_backward", "chunk_dense_eligible", "device_status",
     "document_causal_attention", "document_causal_attention_backward", "fwd_workspace_size",

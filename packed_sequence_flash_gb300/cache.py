@@ -107,7 +107,8 @@ class KVCache:
     by ``attn_cache_fwd(accumulate=True)`` and used by ``kv_cache_evict``.
 
     Each of the five may be replaced (``cache.weight = w``) by a tensor that the
-    constructor would have taken beside the others; the sizes are read-only.
+    constructor would have taken beside the others; the sizes are read-only. A
+    captured graph keeps the memory that it was captured with.
     """
 
     __slots__ = ("_k", "_v", "_k_scale", "_v_scale", "_weight", "_num_pages", "_Hkv", "_page_size", "_Dqk", "_Dv",
@@ -157,7 +158,7 @@ class KVCache:
                       None if weight is None else weight.untyped_storage())
 
     def _call_ref(self):
-        """The struct for a call. A tensor whose memory was exchanged (t.data = u, t.set_(u)) is checked and taken anew."""
+        """The struct for a call. Tensors whose memory was exchanged (t.data = u, t.set_(u)) are checked and taken anew."""
         w = self._weight
         if self._addresses != (self._k.data_ptr(), self._v.data_ptr(), self._k_scale.data_ptr(),
                                self._v_scale.data_ptr(), None if w is None else w.data_ptr()):

@@ -1050,7 +1050,6 @@ int psf_attn_cache_fwd(const void* q, const psf_kv_cache* cache, void* out, floa
   p.o_ss = vo.ss;
   p.o_sh = vo.sh;
   p.lse = lse;
-  p.Hq = Hq;
   p.G = Hq / p.c.Hkv;
   while ((1 << p.g_shift) < p.G) ++p.g_shift;
   p.g_mul = (uint32_t)((((uint64_t)1 << 32) * ((1 << p.g_shift) - p.G)) / p.G + 1);

@@ -93,7 +93,7 @@ struct CacheAttnParams {
   void* out;
   int64_t o_ss, o_sh;
   float* lse;  // [Hq][T]
-  int Hq, G;
+  int G;  // query heads of a KV head
   uint32_t g_mul;  // x / G = (mulhi(x, g_mul) + x) >> g_shift
   int g_shift;
   float scale, softcap;
