@@ -414,7 +414,9 @@ int psf_grad_add_live_rows(void* dst, const void* src, const int32_t* cu_q, cons
  *  k_strides / v_strides: element strides (page, head, row), all zero for the
  *  contiguous ones; else positive multiples of 16 below 2^38 (a dimension of
  *  extent 1 is ignored), and no overlap. The last dim is contiguous; k, v and
- *  weight are 16-byte aligned. Head dims as for the attention calls.
+ *  weight are 16-byte aligned. Head dims as for the attention calls. Append and
+ *  eviction change K and V at the same time and need them in memory of their own
+ *  (PSF_EINVAL where k is v or the scales overlap); the others only read them.
  *
  *  Sequences: page_table int32 [B, max_pages] (contiguous) lists the pages of
  *  each sequence in order, seq_lens int32 [B] its tokens: token j of sequence b

@@ -657,6 +657,14 @@ int cache_view(const psf_kv_cache* cache, CacheView* v) {
 
 constexpr int64_t kMaxCacheTokens = (int64_t(1) << 31) - (1 << 16);
 
+// Calls that write codes change K's and V's at the same time.
+int cache_apart(const CacheView& c) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(c.k_scale), b = reinterpret_cast<uintptr_t>(c.v_scale);
+  if (c.k == c.v || (a > b ? a - b : b - a) < sizeof(float) * (size_t)c.pages * c.Hkv)
+    return fail(PSF_EINVAL, "a cache that is written needs k and v, and k_scale and v_scale, of their own");
+  return PSF_OK;
+}
+
 int seq_view(const int32_t* page_table, const int32_t* seq_lens, const int32_t* cu, int B, int max_pages,
              int page_size, int T, SeqView* s) {
   if (B < 1 || B > 65534 || max_pages < 1 || T < 0)
@@ -994,7 +1002,7 @@ int psf_kv_cache_append(const psf_kv_cache* cache, const void* k, const void* v,
   if (T == 0) return PSF_OK;
   if (!k || !v || !aligned16(k) || !aligned16(v)) return fail(PSF_EINVAL, "null or unaligned k or v");
   DeviceInfo* dev = nullptr;
-  if ((rc = device_info(&dev))) return rc;
+  if ((rc = cache_apart(c)) || (rc = device_info(&dev))) return rc;
   cudaError_t e = launch_cache_append(c, s, k, vk.ss, vk.sh, v, vv.ss, vv.sh, dtype == PSF_DTYPE_F16, dev->status,
                                       static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? PSF_OK : cuda_fail(e, "cache append launch");
@@ -1096,7 +1104,7 @@ int psf_kv_cache_evict(const psf_kv_cache* cache, const int32_t* page_table, con
   if (!workspace || ws_bytes < need || !aligned16(workspace))
     return fail(PSF_EWORKSPACE, "eviction workspace needs %zu bytes, 16-byte aligned (got %zu)", need, ws_bytes);
   DeviceInfo* dev = nullptr;
-  if ((rc = device_info(&dev))) return rc;
+  if ((rc = cache_apart(c)) || (rc = device_info(&dev))) return rc;
   EvictWorkspace w;
   evict_ws_layout(B, max_pages, c.page, c.Hkv, budget, &w, workspace);
   cudaError_t e = launch_cache_evict(c, s, budget, recent, new_lens, w, dev->sms, dev->status,

@@ -1,7 +1,9 @@
 """Sizes at the ends of the 8-bit cache's ranges, on the CPU (stand-in addresses, never dereferenced)."""
+import ctypes
+
 import pytest
 
-from test_cache_cpu import A, EINVAL, EWORKSPACE, append, attend, evict, gather, lib  # noqa: F401 (a fixture)
+from test_cache_cpu import A, EINVAL, EWORKSPACE, append, attend, evict, gather, lib, struct  # noqa: F401 (a fixture)
 
 
 @pytest.mark.parametrize("call", [attend, append, evict, gather])
@@ -31,3 +33,13 @@ def test_new_lengths_that_overlap_the_old_ones(lib, entries):  # noqa: F811
 @pytest.mark.parametrize("entries", [-4, 4])
 def test_new_lengths_beside_the_old_ones(lib, entries):  # noqa: F811
     assert evict(lib, lens=A, new=A + 4 * entries) == EWORKSPACE
+
+
+@pytest.mark.parametrize("kw", [dict(v=A), dict(v_scale=2 * A), dict(v_scale=2 * A + 4 * 19), dict(v_scale=2 * A - 4)])
+def test_caches_whose_keys_and_values_share_memory_are_not_written(lib, kw):  # noqa: F811
+    """Ten pages of two heads: the block that has K's scale rewrites it while another one has V's."""
+    c = struct(**{**dict(k=A, v=4 * A, k_scale=2 * A, v_scale=3 * A), **kw})
+    assert lib.psf_kv_cache_append(ctypes.byref(c), A, A, None, 0, A, A, A, 4, 5, 8, None) == EINVAL
+    assert b"of their own" in lib.psf_last_error(), lib.psf_last_error()
+    assert lib.psf_kv_cache_evict(ctypes.byref(c), A, A, 2 * A, 4, 5, 100, 10, A, 2 ** 40, None) == EINVAL
+    assert b"of their own" in lib.psf_last_error(), lib.psf_last_error()
