@@ -426,7 +426,7 @@ __global__ void __launch_bounds__(kPpThreads, 1) cache_prompt_kernel(const __gri
         if (more && u.slot == 0 && u.ends) join.x |= 2;
         if (more && u.slot == 1) join = make_int4(join.x | 1, u.h, u.b, u.r0 / kPpRows);
         const int us = nunit % kPpUnits;
-        if (!wait_bar(&unit_empty[us], ((nunit / kPpUnits) & 1) ^ 1, ctl)) break;
+        if (!wait_bar_warp(&unit_empty[us], ((nunit / kPpUnits) & 1) ^ 1, ctl)) break;
         if (lane == 0) {
           unit_at[us] = u;
           mbar_arrive(&unit_full[us]);
@@ -453,7 +453,7 @@ __global__ void __launch_bounds__(kPpThreads, 1) cache_prompt_kernel(const __gri
           }
           for (int i = 0; i < 4 && t + i < u.nt; ++i) {
             const int ds = it % kPpDescs;
-            if (!wait_bar(&desc_empty[ds], ((it / kPpDescs) & 1) ^ 1, ctl)) {
+            if (!wait_bar_warp(&desc_empty[ds], ((it / kPpDescs) & 1) ^ 1, ctl)) {
               ok = false;
               break;
             }
@@ -477,7 +477,7 @@ __global__ void __launch_bounds__(kPpThreads, 1) cache_prompt_kernel(const __gri
       constexpr uint32_t id_qk = idesc_f32acc<__half>(128, 128, 0, 0);
       constexpr uint32_t id_pv = idesc_f32acc<__half>(128, DV, 0, 1);
       auto same = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
-      auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait_bar(bar, parity, ctl)) != 0; };
+      auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_bar_warp(bar, parity, ctl); };
       const int x = same(warp >> 1);
       const uint32_t tm = same(tmem), t_s = tm + C::T_S + x * 128, t_o = tm + C::T_O + x * 128;
       const uint64_t q_d = sdesc_sw128(smem_u32(smem + C::Q_OFF) + x * C::K_BYTES, 16, 1024);
@@ -624,12 +624,12 @@ __global__ void __launch_bounds__(kPpThreads, 1) cache_prompt_kernel(const __gri
       // A unit is read from shared memory whenever it is needed, and given back when the one after it is begun. -1: none left.
       auto take_unit = [&]() -> int {
         const int us = nunit % kPpUnits;
-        if (!wait_bar(&unit_full[us], (nunit / kPpUnits) & 1, ctl) || unit_at[us].b < 0) return -1;
+        if (!wait_bar_warp(&unit_full[us], (nunit / kPpUnits) & 1, ctl) || unit_at[us].b < 0) return -1;
         ++nunit;
         return us;
       };
       auto load = [&](uint32_t j) -> bool {  // the codes of the j-th tile of this CTA
-        if (!wait_bar(&desc_full[j % kPpDescs], (j / kPpDescs) & 1, ctl)) return false;
+        if (!wait_bar_warp(&desc_full[j % kPpDescs], (j / kPpDescs) & 1, ctl)) return false;
         const int64_t* at = descs[j % kPpDescs] + (w >> 1);
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
@@ -651,7 +651,7 @@ __global__ void __launch_bounds__(kPpThreads, 1) cache_prompt_kernel(const __gri
         const int nt = u.nt;
 #pragma unroll 1
         for (int jj = 0; jj < nt; ++jj, ++it) {
-          if (!wait_bar(&empty[slot], phase, ctl)) {
+          if (!wait_bar_warp(&empty[slot], phase, ctl)) {
             ok = false;
             break;
           }

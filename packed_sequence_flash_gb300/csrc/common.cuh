@@ -109,6 +109,11 @@ __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, const C
     }
   }
 }
+// wait_bar by a whole warp that stays together: all its lanes go on or none does. Each lane reads the clock and the flag for
+// itself, and one that gave up alone would leave the others at the warp's next collective operation for ever.
+__device__ __forceinline__ bool wait_bar_warp(uint64_t* bar, uint32_t parity, const Ctl& c) {
+  return __all_sync(0xffffffffu, wait_bar(bar, parity, c)) != 0;
+}
 // Drain-only wait used while winding down after an abort: bounded, no flag.
 __device__ __forceinline__ void wait_bar_drain(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
   uint64_t t0 = globaltimer_ns();
