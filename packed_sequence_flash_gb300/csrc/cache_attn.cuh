@@ -458,7 +458,7 @@ __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV, NT>::CTAS)
     // each of the first eight lanes. Without one, tells them so.
     auto announce = [&](bool more, const CaUnit& u) {
       const int qb = nu % kCaUnits;
-      if (nu >= kCaUnits && !wait_bar(&q_empty[qb], (nu / kCaUnits - 1) & 1, ctl)) return false;
+      if (nu >= kCaUnits && !wait_bar_warp(&q_empty[qb], (nu / kCaUnits - 1) & 1, ctl)) return false;
       const int n0 = u.rt * C::R, rows = more ? min(u.m * p.G - n0, C::R) : 0;
       if (lane == 0) {
         if (more)
@@ -493,7 +493,7 @@ __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV, NT>::CTAS)
         for (int i = 0; i < 8 && (first || t8 + i < u.tb); ++i) {
           if (t8 + i < u.tb) {
             const int st = it % C::STAGES;
-            if (it >= C::STAGES && !wait_bar(&empty[st], ((it / C::STAGES) - 1) & 1, ctl)) {
+            if (it >= C::STAGES && !wait_bar_warp(&empty[st], ((it / C::STAGES) - 1) & 1, ctl)) {
               ok = false;
               break;
             }
@@ -848,8 +848,7 @@ __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV, NT>::CTAS)
 
     const int ta = u.ta, tb = u.tb, in_lo = u.in_lo, in_hi = u.in_hi;
     for (int tile = ta; tile < tb; ++tile) {
-      if (ok && !wait_bar(&full[st], ring, ctl)) ok = false;
-      ok = __all_sync(0xffffffffu, ok);
+      ok = ok && wait_bar_warp(&full[st], ring, ctl);
       if (!ok) continue;
       if (tile * kCaKeys >= in_lo && (tile + 1) * kCaKeys <= in_hi)
         tile_step(MaskTag<false>(), tile);

@@ -14,13 +14,13 @@ CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
 VOTED = [r"both\(wait_bar\(", r"consumers_all\(wait_bar\(", r"const bool up = wait_bar\("]
 
 
-@pytest.mark.parametrize("name", ["cache_prompt.cuh"])
+@pytest.mark.parametrize("name", ["cache_prompt.cuh", "cache_attn.cuh"])
 def test_waits_are_voted_on(name):
     with open(os.path.join(CSRC, name)) as fh:
         text = re.sub(r"//[^\n]*", "", fh.read())
     voted = sum(len(re.findall(v, text)) for v in VOTED)
     assert voted and voted == len(re.findall(r"\bwait_bar\(", text))
-    assert "both(up)" in text  # the vote of the softmax's wait for its scores
+    assert ("bool up =" in text) == ("both(up)" in text)  # the vote of the softmax's wait for its scores
     assert re.search(r"\bwait_bar_warp\(", text)
 
 
