@@ -89,7 +89,8 @@ int psf_device_supported(void);
 int psf_device_status(int clear);
 
 /* Upper bound, in nanoseconds, of every pipeline wait inside the kernels
- * (default 2e9, or $PSF_WAIT_LIMIT_NS when set at load time). */
+ * (default 2e9, or $PSF_WAIT_LIMIT_NS when set at load time). A kernel that gives
+ * up still waits for its own copies and products under way, 1e8 at least. */
 void psf_set_wait_limit_ns(uint64_t ns);
 
 /*

@@ -539,15 +539,11 @@ __global__ void __launch_bounds__(kCaThreads, CaCfg<DQK, DV, NT>::CTAS)
       u = next;
       pg = pg_unit;
     }
-    // The CTA does not end before its copies have landed (the wait has a limit of
-    // its own: the consumers may give up and end first).
-    {
-      const uint64_t limit = p.limit_ns > 100000000ull ? p.limit_ns : 100000000ull;
-      for (uint32_t k = it > C::STAGES ? it - C::STAGES : 0; k < it; ++k)
-        wait_bar_drain(&full[k % C::STAGES], (k / C::STAGES) & 1, limit);
-      for (uint32_t k = nu > kCaUnits ? nu - kCaUnits : 0; k < nu; ++k)
-        wait_bar_drain(&q_full[k % kCaUnits], (k / kCaUnits) & 1, limit);
-    }
+    // The CTA does not end before its copies have landed.
+    for (uint32_t k = it > C::STAGES ? it - C::STAGES : 0; k < it; ++k)
+      wait_bar_drain(&full[k % C::STAGES], (k / C::STAGES) & 1, p.limit_ns);
+    for (uint32_t k = nu > kCaUnits ? nu - kCaUnits : 0; k < nu; ++k)
+      wait_bar_drain(&q_full[k % kCaUnits], (k / kCaUnits) & 1, p.limit_ns);
     return;
   }
 

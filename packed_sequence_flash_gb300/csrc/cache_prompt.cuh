@@ -1128,6 +1128,7 @@ __global__ void __launch_bounds__(kPpThreads, 1) cache_prompt_kernel(const __gri
       if (lane == 0) mbar_arrive(&o_free[x]);
       done();
     }
+    tmem_wait_st();  // (a wait that ran out can come between a store and its own)
   }
   tc_fence_before();
   __syncthreads();

@@ -114,11 +114,14 @@ __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, const C
 __device__ __forceinline__ bool wait_bar_warp(uint64_t* bar, uint32_t parity, const Ctl& c) {
   return __all_sync(0xffffffffu, wait_bar(bar, parity, c)) != 0;
 }
-// Drain-only wait used while winding down after an abort: bounded, no flag.
+// Wait used while winding down, for copies and products that are under way and end by themselves: no flag, and a limit of its
+// own where the caller's is short. A block that gave up on its waits must not end, and free its memory, before they have.
+constexpr uint64_t kDrainLimitNs = 100000000;
 __device__ __forceinline__ void wait_bar_drain(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+  const uint64_t limit = limit_ns > kDrainLimitNs ? limit_ns : kDrainLimitNs;
   uint64_t t0 = globaltimer_ns();
   while (!mbar_test(bar, parity))
-    if (globaltimer_ns() - t0 > limit_ns) return;
+    if (globaltimer_ns() - t0 > limit) return;
 }
 
 __device__ __forceinline__ void record_status(int* status, int code) { atomicCAS(status, 0, code); }

@@ -12,10 +12,10 @@ ETIMEOUT = -5
 
 
 @pytest.mark.parametrize("dims", DIMS)
-@pytest.mark.parametrize("softcap", [None, 30.0])
-def test_waits_that_run_out(dims, softcap):
+@pytest.mark.parametrize("softcap,limit", [(None, 200_000), (30.0, 200_000), (None, 1)])
+def test_waits_that_run_out(dims, softcap, limit):
     """Units of up to 128 rows leave half of the softmax warps waiting for the next unit, here for a millisecond and more: under
-    a limit of 0.2 ms they give up. The units behind them have rows for those warps, so that everything else stops there."""
+    a limit of 0.2 ms, or of none, they give up. The units behind them have rows for those warps, so that everything else stops there."""
     assert psf.device_status() == 0
     lens, m_rows, H, page = [1 << 19] * 4, [128, 400, 100, 256], 8, 128
     cache = random_cache(64, H, *dims, page)
@@ -25,7 +25,7 @@ def test_waits_that_run_out(dims, softcap):
     want = call()
     torch.cuda.synchronize()
     assert psf.device_status() == 0
-    psf.set_wait_limit_ns(200_000)
+    psf.set_wait_limit_ns(limit)
     try:
         for _ in range(3):
             call()

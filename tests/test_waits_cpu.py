@@ -29,3 +29,13 @@ def test_the_vote_is_one():
         text = fh.read()
     body = text[text.index("bool wait_bar_warp("):]
     assert "__all_sync(0xffffffffu, wait_bar(bar, parity, c))" in body[:body.index("\n}\n")]
+
+
+def test_a_short_limit_does_not_cut_the_drain():
+    """What is under way when a block gives up ends within a limit that the caller's does not shorten."""
+    with open(os.path.join(CSRC, "common.cuh")) as fh:
+        text = fh.read()
+    assert float(re.search(r"kDrainLimitNs = (\d+);", text).group(1)) >= 1e8
+    body = text[text.index("void wait_bar_drain("):]
+    body = body[:body.index("\n}\n")]
+    assert "limit_ns > kDrainLimitNs ? limit_ns : kDrainLimitNs" in body and "- t0 > limit)" in body
