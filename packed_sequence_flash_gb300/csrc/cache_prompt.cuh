@@ -1146,7 +1146,8 @@ constexpr int kPpJoinThreads = 256;
 template <int DV>
 __global__ void __launch_bounds__(kPpJoinThreads) cache_prompt_join_kernel(const __grid_constant__ PromptParams p, int grid) {
   constexpr int VEC = DV / 4, COLS = kPpJoinThreads / 32;  // columns of four at a time
-  __shared__ float stage[kPpJoinRows][DV + 4];
+  __shared__ __align__(16) float stage[kPpJoinRows][DV + 4];
+  static_assert(__alignof__(stage) >= alignof(float4) && (DV + 4) % 4 == 0, "rows are written by fours");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   let_next_kernel_start();
   after_previous_kernel();

@@ -27,7 +27,7 @@ constexpr int kRowTokens = 4;
 constexpr int kRowBatch = 4;
 
 struct RowsShared {
-  float2 cs[kRowTokens][kRotaryPairs];  // scale * (cos, sin)
+  alignas(16) float2 cs[kRowTokens][kRotaryPairs];  // scale * (cos, sin), read two pairs at a time
   int place[kRowTokens];
   uint64_t turns[kRotaryPairs];
   bool odd[kRotaryPairs];  // the frequency has no angle
@@ -35,6 +35,8 @@ struct RowsShared {
   const char* x[2][kRowTokens][2];
   char* y[2][kRowTokens][2];
 };
+
+static_assert(alignof(RowsShared) >= alignof(float4), "pairs are read by twos");
 
 // What the frequencies stand for, for rows_tables, by all threads (without a barrier behind it).
 __device__ __forceinline__ void rows_turns(RowsShared& sh, const RotaryView& r) {
@@ -284,7 +286,8 @@ __device__ __forceinline__ bool group_or(int g, bool x) {
 template <typename T, bool TABLE, bool UNITS>
 __global__ void __launch_bounds__(kPageThreads* kPageGroups, 2)
     append_rotary_kernel(const __grid_constant__ AppendArgs a, const __grid_constant__ RotaryView r) {
-  extern __shared__ float2 table[];  // [row][half]: a row as in rows_tables, PLAIN without UNITS
+  extern __shared__ __align__(16) float2 table[];  // [row][half]: a row as in rows_tables, PLAIN without UNITS
+  static_assert(__alignof__(table) >= alignof(float4), "pairs are read by twos");
   __shared__ uint64_t turns[kRotaryPairs];
   __shared__ float warp_top[kPageGroups][kPageThreads / 32];
   const CacheView& c = a.c;
@@ -505,7 +508,8 @@ __global__ void __launch_bounds__(kRowThreads, 4)
 template <typename T>
 __global__ void __launch_bounds__(kPageThreads)
     append_rotary_one_kernel(const __grid_constant__ AppendArgs a, const __grid_constant__ RotaryView r) {
-  __shared__ float row_at[kPageThreads / 32][512];
+  __shared__ __align__(8) float row_at[kPageThreads / 32][512];
+  static_assert(__alignof__(row_at) >= alignof(float2), "components are written by twos");
   __shared__ float2 cs_at[kPageThreads / 32][kRotaryPairs];
   const CacheView& c = a.c;
   const SeqView& s = a.s;
