@@ -437,6 +437,10 @@ typedef struct {
  *      have position 0. Sums that fall, do not begin at 0 or pass the rows are a
  *      PSF_EDEVICE_ARGS status;
  *    neither: a row's place s in its batch row.
+ *  A segment is all that these calls know of a document: where rows are a shard that
+ *  begins inside one (psf_build_doc_segments with q_global_start > 0), the places of
+ *  its cu_q begin at the shard's edge, not at the document's. psf_rotary_varlen_fwd
+ *  and _bwd take such rows, and so do positions.
  *  strides: NULL, or 12 element strides (batch, head, row) of q, k, q_out, k_out.
  */
 int psf_rotary_fwd(const void* q, const void* k, void* q_out, void* k_out, const psf_rotary* rotary,
@@ -445,6 +449,24 @@ int psf_rotary_fwd(const void* q, const void* k, void* q_out, void* k_out, const
 int psf_rotary_bwd(const void* dq, const void* dk, void* dq_out, void* dk_out, const psf_rotary* rotary,
                    const int32_t* positions, int axes, const int32_t* cu_seqlens, const int32_t* dev_meta, int nseg,
                    int layout, int B, int S, int Hq, int Hkv, int D, const int64_t* strides, int dtype, void* stream);
+
+/*
+ * psf_rotary_fwd and _bwd with query rows placed as psf_attn_varlen_fwd aligns them
+ * to their keys: row i of the m rows [cu_q[s], cu_q[s + 1]) of segment s, which has
+ * n = cu_k[s + 1] - cu_k[s] keys, has position i + n - m (negative in a padding run
+ * without keys). cu_q and cu_k int32 [nseg + 1] as psf_build_doc_segments writes
+ * them, for any shard; dev_meta (nullable) as above. cu_k that falls or does not
+ * begin at 0 is a PSF_EDEVICE_ARGS status, too. The keys themselves: psf_rotary_fwd
+ * with cu_k as their cu_seqlens, which places every key that a row of the shard sees.
+ * (A document that goes on past the shard's end has a second segment there, without
+ * queries, whose places begin anew.)
+ */
+int psf_rotary_varlen_fwd(const void* q, const void* k, void* q_out, void* k_out, const psf_rotary* rotary,
+                          const int32_t* cu_q, const int32_t* cu_k, const int32_t* dev_meta, int nseg, int layout, int B,
+                          int S, int Hq, int Hkv, int D, const int64_t* strides, int dtype, void* stream);
+int psf_rotary_varlen_bwd(const void* dq, const void* dk, void* dq_out, void* dk_out, const psf_rotary* rotary,
+                          const int32_t* cu_q, const int32_t* cu_k, const int32_t* dev_meta, int nseg, int layout, int B,
+                          int S, int Hq, int Hkv, int D, const int64_t* strides, int dtype, void* stream);
 
 /*
  * 8-bit paged key/value cache, for serving: append, attention of a few query

@@ -49,6 +49,8 @@ SIGNATURES = {
     "psf_kv_cache_append": (I, [P, P, P, P, I, P, P, P, I, I, I, P]),
     "psf_rotary_fwd": (I, [P, P, P, P, P, P, I, P, P, I, I, I, I, I, I, I, P, I, P]),
     "psf_rotary_bwd": (I, [P, P, P, P, P, P, I, P, P, I, I, I, I, I, I, I, P, I, P]),
+    "psf_rotary_varlen_fwd": (I, [P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, P, I, P]),
+    "psf_rotary_varlen_bwd": (I, [P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, P, I, P]),
     "psf_kv_cache_append_rotary": (I, [P, P, P, P, P, P, P, I, P, I, P, P, P, I, I, I, I, P]),
     "psf_attn_cache_workspace_size": (SZ, [I, I, I, I, I, I, I, I, I]),
     "psf_attn_cache_fwd": (I, [P, P, P, P, P, P, P, I, I, I, I, I, P, I, F, I, I32, F, I, P, SZ, P]),

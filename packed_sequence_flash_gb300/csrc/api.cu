@@ -780,8 +780,8 @@ int rotary_rows(const void* x, void* y, const char* name, const int64_t* strides
 }
 
 int rotary_impl(const void* q, const void* k, void* q_out, void* k_out, const psf_rotary* rotary,
-                const int32_t* positions, int axes, const int32_t* cu_seqlens, const int32_t* dev_meta, int nseg,
-                int layout, int B, int S, int Hq, int Hkv, int D, const int64_t* strides, int dtype, bool back,
+                const int32_t* positions, int axes, const int32_t* cu_seqlens, const int32_t* cu_k, const int32_t* dev_meta,
+                int nseg, int layout, int B, int S, int Hq, int Hkv, int D, const int64_t* strides, int dtype, bool back,
                 void* stream) {
   RotaryView r;
   PlaceView p;
@@ -806,6 +806,7 @@ int rotary_impl(const void* q, const void* k, void* q_out, void* k_out, const ps
   a.S = S;
   a.rows = rows;
   a.cu = cu_seqlens;
+  a.cu_k = cu_k;
   a.dev_meta = dev_meta;
   a.nseg = nseg;
   r.back = back;
@@ -1205,15 +1206,31 @@ int psf_kv_cache_append(const psf_kv_cache* cache, const void* k, const void* v,
 int psf_rotary_fwd(const void* q, const void* k, void* q_out, void* k_out, const psf_rotary* rotary,
                    const int32_t* positions, int axes, const int32_t* cu_seqlens, const int32_t* dev_meta, int nseg,
                    int layout, int B, int S, int Hq, int Hkv, int D, const int64_t* strides, int dtype, void* stream) {
-  return rotary_impl(q, k, q_out, k_out, rotary, positions, axes, cu_seqlens, dev_meta, nseg, layout, B, S, Hq, Hkv, D,
-                     strides, dtype, false, stream);
+  return rotary_impl(q, k, q_out, k_out, rotary, positions, axes, cu_seqlens, nullptr, dev_meta, nseg, layout, B, S, Hq,
+                     Hkv, D, strides, dtype, false, stream);
 }
 
 int psf_rotary_bwd(const void* dq, const void* dk, void* dq_out, void* dk_out, const psf_rotary* rotary,
                    const int32_t* positions, int axes, const int32_t* cu_seqlens, const int32_t* dev_meta, int nseg,
                    int layout, int B, int S, int Hq, int Hkv, int D, const int64_t* strides, int dtype, void* stream) {
-  return rotary_impl(dq, dk, dq_out, dk_out, rotary, positions, axes, cu_seqlens, dev_meta, nseg, layout, B, S, Hq, Hkv,
-                     D, strides, dtype, true, stream);
+  return rotary_impl(dq, dk, dq_out, dk_out, rotary, positions, axes, cu_seqlens, nullptr, dev_meta, nseg, layout, B, S, Hq,
+                     Hkv, D, strides, dtype, true, stream);
+}
+
+int psf_rotary_varlen_fwd(const void* q, const void* k, void* q_out, void* k_out, const psf_rotary* rotary,
+                          const int32_t* cu_q, const int32_t* cu_k, const int32_t* dev_meta, int nseg, int layout, int B,
+                          int S, int Hq, int Hkv, int D, const int64_t* strides, int dtype, void* stream) {
+  if (!cu_q || !cu_k) return fail(PSF_EINVAL, "null cu_q or cu_k");
+  return rotary_impl(q, k, q_out, k_out, rotary, nullptr, 0, cu_q, cu_k, dev_meta, nseg, layout, B, S, Hq, Hkv, D, strides,
+                     dtype, false, stream);
+}
+
+int psf_rotary_varlen_bwd(const void* dq, const void* dk, void* dq_out, void* dk_out, const psf_rotary* rotary,
+                          const int32_t* cu_q, const int32_t* cu_k, const int32_t* dev_meta, int nseg, int layout, int B,
+                          int S, int Hq, int Hkv, int D, const int64_t* strides, int dtype, void* stream) {
+  if (!cu_q || !cu_k) return fail(PSF_EINVAL, "null cu_q or cu_k");
+  return rotary_impl(dq, dk, dq_out, dk_out, rotary, nullptr, 0, cu_q, cu_k, dev_meta, nseg, layout, B, S, Hq, Hkv, D,
+                     strides, dtype, true, stream);
 }
 
 int psf_kv_cache_append_rotary(const psf_kv_cache* cache, const void* k, const void* v, const void* q, void* q_out,

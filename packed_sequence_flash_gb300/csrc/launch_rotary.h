@@ -20,8 +20,9 @@ struct RotaryRows {
   int D, S;
   int64_t rows;
   // Where positions are not given: a row's place in its segment (cu: prefix sums of
-  // nseg segments, or of dev_meta[0] of them), or in its batch row.
+  // nseg segments, or of dev_meta[0] of them), aligned to the end of the segment's keys (cu_k, nullable), or in its batch row.
   const int32_t* cu;
+  const int32_t* cu_k;
   const int32_t* dev_meta;
   int nseg;
 };

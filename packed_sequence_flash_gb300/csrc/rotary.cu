@@ -206,15 +206,17 @@ __global__ void __launch_bounds__(kRowThreads, 4)
   if (a.cu) {
     if (a.dev_meta) nseg = min(max(a.dev_meta[0], 0), nseg);
     if (blockIdx.x == 0) {
-      bool bad = a.cu[0] != 0 || a.cu[nseg] > a.rows;
-      for (int i = threadIdx.x; i < nseg; i += kRowThreads) bad |= a.cu[i + 1] < a.cu[i];
+      bool bad = a.cu[0] != 0 || a.cu[nseg] > a.rows || (a.cu_k && a.cu_k[0] != 0);
+      for (int i = threadIdx.x; i < nseg; i += kRowThreads)
+        bad |= a.cu[i + 1] < a.cu[i] || (a.cu_k && a.cu_k[i + 1] < a.cu_k[i]);
       if (bad) record_status(status, kStatusDeviceArgs);
     }
   }
   auto base = [&](int64_t row) -> int {
     if (!a.cu) return (int)(row % a.S);
     if (nseg == 0 || row >= a.cu[nseg]) return 0;
-    return (int)row - a.cu[warp_find(nseg, row, [&](int i) { return a.cu[i]; })];
+    const int s = warp_find(nseg, row, [&](int i) { return a.cu[i]; });
+    return a.cu_k ? (int)row - a.cu[s + 1] + (a.cu_k[s + 1] - a.cu_k[s]) : (int)row - a.cu[s];
   };
   auto tables = [&](int64_t row0, int n) { rows_tables<ANY>(sh, r, p, row0, n, base); };
   if constexpr (ANY) {

@@ -1,7 +1,7 @@
 """Position rotation of queries and keys, and the cache's append with it.
 
-Python binding of ``psf_rotary_fwd`` / ``_bwd`` and ``psf_kv_cache_append_rotary``:
-argument marshalling only, as in ``cache.py``.
+Python binding of ``psf_rotary_fwd`` / ``_bwd``, ``psf_rotary_varlen_fwd`` / ``_bwd`` and
+``psf_kv_cache_append_rotary``: argument marshalling only, as in ``cache.py``.
 
 Training::
 
@@ -10,6 +10,11 @@ Training::
     out, lse = attn_varlen_fwd(q, k, v, cu, cu, ...)
     dq, dk, dv = attn_varlen_bwd(dout, q, k, v, out, lse, ...)
     dq, dk = rotary_bwd(dq, dk, rotary, cu_seqlens=cu)
+
+A query shard of documents, with the segments of ``build_doc_segments``::
+
+    q, _ = rotary_fwd(q, None, rotary, cu_seqlens=cu_q, dev_meta=meta, cu_seqlens_k=cu_k)   # also where it begins inside one
+    _, k = rotary_fwd(None, k, rotary, cu_seqlens=cu_k, dev_meta=meta)
 
 Serving::
 
@@ -125,7 +130,7 @@ def _result(t, out, name, dtype, device):
     return out, _view(out, name, dtype, device)
 
 
-def _rotate(call, q, k, rotary, positions, cu_seqlens, dev_meta, q_out, k_out, names):
+def _rotate(way, q, k, rotary, positions, cu_seqlens, dev_meta, q_out, k_out, cu_seqlens_k, names):
     first, first_name = (q, names[0]) if q is not None else (k, names[1])
     if first is None:
         raise ValueError(f"{names[0]} or {names[1]} must be given")
@@ -166,28 +171,39 @@ def _rotate(call, q, k, rotary, positions, cu_seqlens, dev_meta, q_out, k_out, n
         if positions is not None:
             raise ValueError("positions and cu_seqlens exclude each other")
         cu, nseg = cu_seqlens.data_ptr(), cu_seqlens.numel() - 1
+    if cu_seqlens_k is not None:
+        _tensor(cu_seqlens_k, "cu_seqlens_k", torch.int32, device)
+        if cu_seqlens is None or cu_seqlens_k.shape != cu_seqlens.shape:
+            raise ValueError("cu_seqlens_k must be [segments + 1] like cu_seqlens, which it comes with")
     if dev_meta is not None:
         _tensor(dev_meta, "dev_meta", torch.int32, device)
         dev_meta = dev_meta.data_ptr()
     if B:
-        _launch(device, _call(call), qp, kp, qo, ko, rotary._call_ref(device), pos, axes, cu, dev_meta, nseg, layout, B, S,
+        if cu_seqlens_k is None:
+            call, places = "psf_rotary_" + way, (pos, axes, cu)
+        else:
+            call, places = "psf_rotary_varlen_" + way, (cu, cu_seqlens_k.data_ptr())
+        _launch(device, _call(call), qp, kp, qo, ko, rotary._call_ref(device), *places, dev_meta, nseg, layout, B, S,
                 Hq, Hkv, shape[-1], _strides((q, k, q_out, k_out)), _DTYPES[dtype])
     return q_out, k_out
 
 
-def rotary_fwd(q, k, rotary, positions=None, cu_seqlens=None, dev_meta=None, q_out=None, k_out=None):
+def rotary_fwd(q, k, rotary, positions=None, cu_seqlens=None, dev_meta=None, q_out=None, k_out=None, cu_seqlens_k=None):
     """Turns q [T, Hq, D] and k [T, Hkv, D] (or [B, H, S, D]; bf16 or fp16; one may be None) -> (q_out, k_out).
 
     positions int32 [T] or [axes, T] (or [B, S], [axes, B, S]); or cu_seqlens int32 [segments + 1]: a row's place in its
     segment (dev_meta: the segment builder's, with the count on the device); neither: its place in its batch row. q_out
     may be q itself (in place), k_out k. See psf_rotary.
+    cu_seqlens_k: with the keys' prefix sums beside the rows' own, a row's place is that among its segment's keys, to whose
+    end the rows are aligned as in ``attn_varlen_fwd``. A shard that begins inside a document (q_global_start > 0) needs it:
+    by cu_seqlens alone its rows would count from the shard's edge. See psf_rotary_varlen_fwd.
     """
-    return _rotate("psf_rotary_fwd", q, k, rotary, positions, cu_seqlens, dev_meta, q_out, k_out, ("q", "k"))
+    return _rotate("fwd", q, k, rotary, positions, cu_seqlens, dev_meta, q_out, k_out, cu_seqlens_k, ("q", "k"))
 
 
-def rotary_bwd(dq, dk, rotary, positions=None, cu_seqlens=None, dev_meta=None, dq_out=None, dk_out=None):
+def rotary_bwd(dq, dk, rotary, positions=None, cu_seqlens=None, dev_meta=None, dq_out=None, dk_out=None, cu_seqlens_k=None):
     """The gradients of rotary_fwd's inputs from those of its results, with the same rotation and positions."""
-    return _rotate("psf_rotary_bwd", dq, dk, rotary, positions, cu_seqlens, dev_meta, dq_out, dk_out, ("dq", "dk"))
+    return _rotate("bwd", dq, dk, rotary, positions, cu_seqlens, dev_meta, dq_out, dk_out, cu_seqlens_k, ("dq", "dk"))
 
 
 def kv_cache_append_rotary(cache, k, v, rotary, page_table, seq_lens, cu_new=None, positions=None, q=None, q_out=None):
