@@ -562,7 +562,8 @@ int psf_kv_cache_append_rotary(const psf_kv_cache* cache, const void* k, const v
  *  rows past cu_q[B] get out = 0 and lse = -inf.
  *  One query row per sequence is the decode step; a few are drafted tokens or the
  *  tail of a prompt. Any number is computed, a tile of rows at a time; for long
- *  prompt chunks psf_attn_cache_prompt_fwd is faster.
+ *  prompt chunks psf_attn_cache_prompt_fwd is faster, and at head dim 512
+ *  psf_kv_cache_gather with psf_attn_varlen_fwd.
  *  Codes that are NaN make a row NaN only where it sees them.
  *  flags: 0, or PSF_CACHE_ACCUMULATE: weight[page, hkv, row] += the sum over the
  *  sequence's query rows and the Hq / Hkv heads of hkv of exp(logit - lse), for
@@ -587,9 +588,16 @@ int psf_attn_cache_fwd(const void* q, const psf_kv_cache* cache, void* out, floa
  *  Arguments, results, masks and statuses as there, without flags (no weights are
  *  accumulated). A KV head's query heads share its tiles, so a batch may mix
  *  chunks, tails and single tokens. The kernel of psf_attn_cache_fwd runs where it
- *  is the faster one: for at most 32 rows per KV head (max_q * Hq / Hkv), where
- *  little is to be done (B * Hkv * rows / 16 * max_pages * page_size up to 4 * 10^5),
- *  and at head dim 512.
+ *  is the faster one: for at most 32 rows per KV head (max_q * Hq / Hkv), and where
+ *  little is to be done (B * Hkv * rows / 16 * max_pages * page_size up to 4 * 10^5:
+ *  by the table's width, as the lengths are on the device). It runs at head dim 512,
+ *  too, which the tiles do not do.
+ *  Faster through psf_kv_cache_gather and psf_attn_varlen_fwd, where there is memory
+ *  for the 16-bit copies: long chunks at head dim 512 (two of 2048 rows over 32 Ki
+ *  keys, 8 / 2 heads: 3.7 ms for 13.9 here), hundreds of short sequences (2000 whole
+ *  prompts of 10 to 100 tokens: 0.63 ms for 1.21) and whole prompts at 192/128 (two
+ *  of 8001 with a window: 0.50 for 0.55). Decode steps are faster in a call of their
+ *  own than beside a chunk (63 with a chunk of 512 over 8 Ki keys: 292 us for 467).
  *  P is rounded to fp16 whatever the dtype; queries are scaled by a power of two
  *  per row into fp16's range.
  *  workspace: psf_attn_cache_prompt_workspace_size(...) bytes, 16-byte aligned (42 MB

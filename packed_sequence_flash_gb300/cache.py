@@ -258,7 +258,8 @@ def attn_cache_fwd(q, cache, page_table, seq_lens, scale, cu_q=None, max_q=None,
     without cu_q. They are the last tokens of the sequence (their keys are in the cache already), so one row per
     sequence is a decode step. window, softcap, GQA, lse as for ``attn_varlen_fwd``; causal is the default.
     accumulate: add every token's attention weight, over the rows and the heads of its KV head, to cache.weight.
-    Long prompt chunks run faster through ``attn_cache_prompt_fwd``.
+    Long prompt chunks run faster through ``attn_cache_prompt_fwd``, at head dim 512 through ``kv_cache_gather`` and
+    ``attn_varlen_fwd``.
     """
     size = functools.partial(attn_cache_workspace_size, accumulate=True) if accumulate else attn_cache_workspace_size
     return _attend("psf_attn_cache_fwd", (PSF_CACHE_ACCUMULATE if accumulate else 0,), size, q, cache, page_table, seq_lens,
@@ -280,7 +281,9 @@ def attn_cache_prompt_fwd(q, cache, page_table, seq_lens, scale, cu_q=None, max_
                           softcap=None, out=None, lse=None, workspace=None):
     """``attn_cache_fwd`` for prompt chunks: sequences with many query rows, on the tensor cores' 256-row tiles.
 
-    Arguments and results as there (no weights are accumulated); a batch may mix chunks, tails and single tokens.
+    Arguments and results as there (no weights are accumulated); a batch may mix chunks, tails and single tokens. Head dim
+    512 has no such tiles: long chunks run faster through ``kv_cache_gather`` and ``attn_varlen_fwd`` there, as do hundreds of
+    short sequences at any head dim. See psf_attn_cache_prompt_fwd.
     """
     return _attend("psf_attn_cache_prompt_fwd", (), attn_cache_prompt_workspace_size, q, cache, page_table, seq_lens, scale,
                    cu_q, max_q, causal, window, softcap, out, lse, workspace)

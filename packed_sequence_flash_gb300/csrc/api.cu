@@ -894,7 +894,9 @@ int run_cache_attn(CacheAttnParams& p, int B, int max_pages, int Hq, int max_q, 
 // kernel for decode steps takes 16 rows at a time from registers: up to 32 of them it is as fast or faster (16 sequences of 8
 // Ki tokens, 8 KV heads of 128: 109 us for 121; 64 rows: 210 for 120), and where its work is small, since the tiles need 35 us
 // before the first result (one sequence of 8 Ki tokens, 128 rows: 37 us for 54; of 32 Ki: 104 for 69). `work` counts 16-row
-// tiles times keys, for sequences as long as the table: 4 * 10^5 take it some 25 us. Head dim 512 leaves no tensor memory for scores.
+// tiles times keys, for sequences as long as the table (the lengths are on the device: 40 rows at 777 tokens take 18 us, 29
+// under a table for 128 Ki): 4 * 10^5 take it some 25 us. Head dim 512 leaves no tensor memory for scores; the kernel for
+// decode steps is not the faster way there (see the header), but the only one without copies of the cache.
 bool prompt_tiles(int B, int max_pages, int page_size, int Hkv, int Dqk, int64_t rows) {
   const double work = (double)B * Hkv * ((rows + 15) / 16) * ((double)max_pages * page_size);
   return Dqk != 512 && rows > 32 && work > 4e5;
