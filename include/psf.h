@@ -586,7 +586,8 @@ int psf_attn_cache_fwd(const void* q, const psf_kv_cache* cache, void* out, floa
  * Attention of prompt chunks over the cache: what psf_attn_cache_fwd computes,
  * on the tensor cores' 256-row tiles, for sequences with many query rows.
  *  Arguments, results, masks and statuses as there, without flags (no weights are
- *  accumulated). A KV head's query heads share its tiles, so a batch may mix
+ *  accumulated: before an eviction, tokens of a chunk have only what later calls of
+ *  psf_attn_cache_fwd add). A KV head's query heads share its tiles, so a batch may mix
  *  chunks, tails and single tokens. The kernel of psf_attn_cache_fwd runs where it
  *  is the faster one: for at most 32 rows per KV head (max_q * Hq / Hkv), and where
  *  little is to be done (B * Hkv * rows / 16 * max_pages * page_size up to 4 * 10^5:
