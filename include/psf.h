@@ -428,7 +428,9 @@ typedef struct {
  *  q [T, Hq, D], k [T, Hkv, D] (dtype, PSF_LAYOUT_THD; or [B, H, S, D],
  *  PSF_LAYOUT_BHSD, with rows b * S + s) -> q_out, k_out of the same shape; dq and
  *  dk likewise. Hq or Hkv may be 0 (its pointers are not read). A result may be its
- *  input itself, with the same strides; otherwise it overlaps no input. D is a multiple of 8 up to 1024.
+ *  input itself, with the same strides; otherwise it overlaps no input, and never the
+ *  other tensor or its result (PSF_EINVAL where they begin at one address). D is a
+ *  multiple of 8 up to 1024.
  *  Positions, in one of three ways:
  *    positions int32 [axes, rows] (axes 1 to 8; 1: every pair takes it whatever its axis);
  *    cu_seqlens int32 [nseg + 1], prefix sums over the rows: a row's place in its
@@ -540,7 +542,8 @@ int psf_kv_cache_append(const psf_kv_cache* cache, const void* k, const void* v,
  * The append of new rows whose keys are turned on the way (see psf_rotary).
  *  As psf_kv_cache_append, with the keys' turned values, kept in fp32 until they
  *  become codes, in place of k's. q [T, Hq, Dqk] (Hq 0: none), the queries of the
- *  same tokens, are turned into q_out in the same call (q_out may be q itself).
+ *  same tokens, are turned into q_out in the same call (q_out may be q itself;
+ *  otherwise it overlaps no input: PSF_EINVAL where it begins at k or v).
  *  positions int32 [axes, T] as for psf_rotary_fwd, or NULL with axes 0: a token's
  *  place in its sequence, 0 for rows of no sequence. After an eviction places
  *  count kept tokens, so a cache that is evicted from wants positions.

@@ -802,6 +802,9 @@ int rotary_impl(const void* q, const void* k, void* q_out, void* k_out, const ps
       (rc = rotary_rows(k, k_out, "k", strides, 1, 3, layout, B, S, Hkv, D, 1, &a)))
     return rc;
   if (rows == 0) return PSF_OK;
+  // Both tensors turn at the same time: one that is given twice, in place, would be turned once or twice.
+  if (Hq && Hkv && (q_out == k_out || q_out == k || k_out == q))
+    return fail(PSF_EINVAL, "the results need memory of their own, apart from the other tensor's");
   a.D = D;
   a.S = S;
   a.rows = rows;
@@ -1262,7 +1265,9 @@ int psf_kv_cache_append_rotary(const psf_kv_cache* cache, const void* k, const v
   a.S = T;
   a.rows = T;
   DeviceInfo* dev = nullptr;
-  if ((rc = cache_apart(c)) || (rc = device_info(&dev))) return rc;
+  if ((rc = cache_apart(c))) return rc;
+  if (Hq && (q_out == k || q_out == v)) return fail(PSF_EINVAL, "q_out needs memory of its own, apart from k and v");
+  if ((rc = device_info(&dev))) return rc;
   cudaError_t e = launch_cache_append_rotary(c, s, r, p, k, vk.ss, vk.sh, v, vv.ss, vv.sh, a, dtype == PSF_DTYPE_F16,
                                              dev->sms, dev->status, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? PSF_OK : cuda_fail(e, "cache append launch");
