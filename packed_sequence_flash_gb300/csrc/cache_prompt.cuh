@@ -111,9 +111,11 @@ __device__ __forceinline__ PpTiles pp_tiles(const PromptParams& p, int n, int m,
 // Half-tiles that a key tile costs: half B is idle where there are no rows for it.
 __device__ __forceinline__ int pp_weight(int rows) { return rows > kPpRows / 2 ? 2 : 1; }
 __device__ __forceinline__ int pp_cost(const PpTiles& t) { return kPpUnitCost + pp_weight(t.rows) * t.kt; }
-__device__ __forceinline__ int pp_row_tiles(const PromptParams& p, const Seq& q) {
-  return (q.m * p.a.G + kPpRows - 1) / kPpRows;
-}
+// Row tiles of up to 2^31 - 1 rows (rounding up by a sum passes 32 bits in the last 255 of them).
+__host__ __device__ constexpr int pp_tiles_of(int rows) { return rows / kPpRows + (rows % kPpRows != 0); }
+static_assert(pp_tiles_of(0) == 0 && pp_tiles_of(1) == 1 && pp_tiles_of(256) == 1 && pp_tiles_of(257) == 2 &&
+              pp_tiles_of(0x7fffffff) == 1 << 23, "row tiles");
+__device__ __forceinline__ int pp_row_tiles(const PromptParams& p, const Seq& q) { return pp_tiles_of(q.m * p.a.G); }
 
 // By a whole warp: the cost of one head's units of sequence first + lane (0 past `last`).
 __device__ __forceinline__ int64_t pp_costs(const PromptParams& p, int first, int last, bool record) {
