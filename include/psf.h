@@ -603,7 +603,8 @@ int psf_attn_cache_fwd(const void* q, const psf_kv_cache* cache, void* out, floa
  *  of 8001 with a window: 0.50 for 0.55). Decode steps are faster in a call of their
  *  own than beside a chunk (63 with a chunk of 512 over 8 Ki keys: 292 us for 467).
  *  P is rounded to fp16 whatever the dtype; queries are scaled by a power of two
- *  per row into fp16's range.
+ *  per row into fp16's range. The same call gives the same bits; under a softcap a
+ *  row's last bits may depend on the rows that share its tile.
  *  workspace: psf_attn_cache_prompt_workspace_size(...) bytes, 16-byte aligned (42 MB
  *  at head dim 128, whatever the batch); nothing in it has to be kept or cleared between calls.
  */

@@ -11,7 +11,7 @@
 // so that one half's softmax runs beside the other half's products, and the
 // expansion of a key tile serves 256 rows. The halves' products take turns.
 // Measured: two chunks of 2048 tokens over 32 Ki keys (32 / 8 heads of 128) 1.70 ms,
-// 1255 TF/s, 0.67 of a large product's rate. A tile's 32 products fill the tensor pipe
+// 1255 TF/s, 0.67 of a large product's rate; two windowed prompts of 8001 at 192/128 552 us. A tile's 32 products fill the tensor pipe
 // for 2048 cycles (64 each, timed alone) of some 4000 that the tile takes: each half
 // goes round scores - softmax - P V, with the issue slots half full, and the softmax's
 // loop is faster the fewer registers and instructions it has (two threads a row, 88
@@ -53,7 +53,7 @@ constexpr int kPpUnits = 3;     // units announced and not yet done with
 constexpr int kPpDescs = 8;     // tiles described ahead (and still read by the softmax)
 // References of a row's probabilities: with the V scales (P is at most 2^kPpTop of it, 2^kPpHead when it is set) and
 // without (the row sum's, at most 2^kPpLazyM below a score). A move costs a pass over O. With 2^3 it takes 12 octaves to
-// cause one; with 2^7, 8 octaves, and 16 mixed prompts take 690 us for 672, where P would go on 4 octaves further down.
+// cause one; with 2^7, 8 octaves, and 16 mixed prompts take 3 % longer, where P would go on 4 octaves further down.
 constexpr float kPpHead = 3.f, kPpTop = 15.f, kPpLazyM = 24.f, kPpNone = kPpLazyM + 26.f;
 constexpr int kPpSnap = 8;      // places from a unit's end that a share's is moved to it
 constexpr int kPpUnitCost = 4;  // of a unit, in half-tiles: queries in, last product and result out
@@ -732,8 +732,9 @@ __global__ void __launch_bounds__(kPpThreads, 1) cache_prompt_kernel(const __gri
     // Capped logits in log2 units, cap2 tanh(a). tanh a = 1 - 2 / (e^(2a) + 1) is off by some 2^-22 however small a is:
     // 2^-16 of a logit for caps up to 64. For larger ones ca_tanh, which takes three times the instructions. Where all
     // scores of a warp are below a quarter of the cap, the series of ca_tanh, on the multipliers alone (a chunk of 512 over 32
-    // Ki keys under a cap of 30: 356 us for 401; 16 mixed prompts 642 for 674, and 702 for 672 under a cap of 5). With 192
-    // key components the registers it takes cost more than it saves (a windowed prompt 748 us for 719).
+    // Ki keys under a cap of 30: 353 us, 12 % less; 16 mixed prompts 632, 5 % less, but 4 % more under a cap of 5). With 192
+    // key components the registers it takes cost more than it saves (4 % of a windowed prompt). The vote makes a score's last
+    // bits depend on those beside it in the tile.
     const float cap2 = p.a.softcap * 1.4426950408889634f;
     const bool cap_near = p.a.softcap <= 64.f;
     // A warp's 16 rows of a unit's queries, 8 lanes a row and four rows at a time: into registers, and to shared memory as

@@ -17,7 +17,9 @@ namespace {
 // Many rows are bound by memory: 65536 tokens of 32 + 8 heads of 128 take 198 us,
 // 198 at the copy rate. Fewer are bound by latency, loads - places - angles -
 // stores, over 32 warps an SM: 20011 tokens of 12 + 12 heads of 128 take 44 us for
-// 36, 8192 tokens of 16 + 4 heads 16 us for 12.4 (issue slots 55 % busy). Measured
+// 36, 8192 tokens of 16 + 4 heads 16 to 18 us for 12.4 (issue slots 61 to 64 % busy
+// from cold). A row needs heads: 65536 tokens of 1 + 1 heads of 64 give 32 of a CTA's
+// threads a unit and take 60 us for 5. Measured
 // beside it, from cold: 1, 2, 4, 8 tokens a CTA 90, 63, 51, 53 us for the 20011
 // tokens and 342, 238, 209, 223 for the 65536; 2 loads ahead and 6 CTAs an SM for 4
 // and 4: 57 and 244; pairs' products by twos, whose operands' places cost what the
@@ -172,7 +174,9 @@ __device__ __forceinline__ void rotate_rows(RowsShared& sh, const RotaryView& r,
   }
 }
 
-// The same for any layout: a pair, or a component that passes, at a time.
+// The same for any layout: a pair, or a component that passes, at a time. Bound by its instructions (two divisions and two rows'
+// addresses for each): 65536 tokens of 16 + 4 heads of 72, all of it turned, take 221 us for 56 at the copy rate, of 128 with 50
+// turned 558 for 99.
 template <typename T>
 __device__ __forceinline__ void rotate_rows_any(RowsShared& sh, const RotaryView& r, const RotaryRows& a, int64_t row0,
                                                 int n) {
@@ -480,7 +484,8 @@ __global__ void __launch_bounds__(kPageThreads* kPageGroups, 2)
   }
 }
 
-// The query rows of an append: as rotary_kernel, with places in the cache.
+// The query rows of an append: as rotary_kernel, with places in the cache, and a CTA per group of tokens. (Resident CTAs that walk
+// over the groups, as there, have not been measured beside the pages' kernel, whose CTAs they would share the SMs with.)
 template <typename T, bool ANY>
 __global__ void __launch_bounds__(kRowThreads, 4)
     append_queries_kernel(const __grid_constant__ AppendArgs a, const __grid_constant__ RotaryView r) {
@@ -506,7 +511,9 @@ __global__ void __launch_bounds__(kRowThreads, 4)
 
 // One new row per sequence (a decode step): a warp per (sequence, K or V or query
 // head). Latency bounds it, as in the append without rotation: the row lies in
-// shared memory as fp32, so that a lane reaches the other half of its pairs.
+// shared memory as fp32, so that a lane reaches the other half of its pairs. 64
+// sequences of 8 KV and 32 query heads of 128: 4.4 us a replayed step (2.3 without
+// rotation and queries); each warp makes its sequence's angles for itself.
 template <typename T>
 __global__ void __launch_bounds__(kPageThreads)
     append_rotary_one_kernel(const __grid_constant__ AppendArgs a, const __grid_constant__ RotaryView r) {
